@@ -125,7 +125,7 @@ def prepare(case, seed):
         st["y"] = normal(t, h, std=0.5).to(dt)
         st["w_pre"] = (1 + normal(h, std=0.1)).to(dt)
         st["w_post"] = (1 + normal(h, std=0.1)).to(dt)
-        shape = {"none": None, "channel": (h,), "token": (t,), "element": (t, h)}[case["gate"]]
+        shape = {"none": None, "channel": (h,), "token": (t, 1), "element": (t, h)}[case["gate"]]
         st["gate"] = None if shape is None else torch.sigmoid(normal(*shape)).to(dt)
         st["alpha"] = 0.5
         if kind == "norm_train":
@@ -223,8 +223,6 @@ def _run_plain(st):
     res, y = st["res"].float(), st["y"].float()
     w_post, w_pre, alpha = st["w_post"].float(), st["w_pre"].float(), st["alpha"]
     gate = None if st["gate"] is None else st["gate"].float()
-    if case["gate"] == "token":
-        gate = gate[:, None]
     p = _plain_norm(y, w_post)
     r = res + alpha * (p if gate is None else gate * p)
     n = _plain_norm(r, w_pre)
@@ -240,7 +238,7 @@ def _run_plain(st):
         if case["gate"] == "channel":
             dgate = dgate.sum(dim=0)
         elif case["gate"] == "token":
-            dgate = dgate.sum(dim=1)
+            dgate = dgate.sum(dim=1, keepdim=True)
         else:
             dgate = dgate.to(dt)
     return r.to(dt), n.to(dt), dres.to(dt), dy.to(dt), dw_post, dw_pre, dgate
@@ -305,8 +303,6 @@ def exact(case, seed):
         return d["res"] + st["alpha"] * unit(y)[0] * d["w_post"]
     alpha = st["alpha"]
     gate = torch.ones((), dtype=torch.float64, device="cuda") if st["gate"] is None else d["gate"]
-    if case["gate"] == "token":
-        gate = gate.reshape(-1, 1)
     yh, yi = unit(d["y"])
     p = yh * d["w_post"]
     r = d["res"] + alpha * gate * p
@@ -319,6 +315,6 @@ def exact(case, seed):
     dp = alpha * gate * dr
     dy = back(yh, yi, dp * d["w_post"])
     dg = alpha * dr * p
-    dg = {"none": lambda: None, "channel": lambda: dg.sum(0), "token": lambda: dg.sum(1),
+    dg = {"none": lambda: None, "channel": lambda: dg.sum(0), "token": lambda: dg.sum(1, keepdim=True),
           "element": lambda: dg}[case["gate"]]()
     return r, n, dr, dy, (dp * yh).sum(0), (d["dn"] * rh).sum(0), dg
