@@ -571,6 +571,131 @@ Q4_API int int8_w8a8_group_acc(const int8_t* q, int64_t rows, int64_t k, const v
                         int32_t* acc, hipStream_t stream);
 
 /*
+ * The dense operators around the quantised FFN of a transformer block: an INT8 linear with
+ * one scale per token and per output channel, the 16-bit gated projection that the INT4
+ * experts are quantised from (with its gradients), and the norms before and after a block.
+ * Used together: block_norm_forward (INT8 codes) -> int8_linear_forward ->
+ * block_norm_forward (norm after the block, gate, residual scale).
+ */
+
+/*
+ * quantize_int8_channel -- INT8 weights with one scale per output channel (page
+ * "MoE推理优化实战：4bit存储+INT8计算的W4A8路线解析": W8A8, INT8 weights and INT8 compute).
+ *  w        device [n][k] of dtype w_dtype (Q4_F32, Q4_F16, Q4_BF16).
+ *  q        device [n][k] int8: clamp(rint(w / s), -127, 127).
+ *  s        device [n] fp32: s = amax / 127 (IEEE fp32 divisions, half-to-even); a zero
+ *           row gets s = 0 and codes 0.
+ *  flags_dev as for quantize_int4_g128 (Q4_QFLAG_NONFINITE).
+ *  Requires k % 16 == 0, 1 <= k < 131072, 1 <= n <= 2^20.
+ */
+Q4_API int quantize_int8_channel(const void* w, int w_dtype, int64_t n, int64_t k, int8_t* q, float* s,
+                                 int32_t* flags_dev, hipStream_t stream);
+
+/*
+ * int8_linear_forward -- y = (q w_q^T) * s * w_s (+ bias): INT8 x INT8 -> INT32 over all of
+ * K, rescaled once by scale_w * scale_a (page "MoE推理优化实战：4bit存储+INT8计算的W4A8路线
+ * 解析" §2.3; int8_w8a8_group_acc and the W8A8 layers scale per group of 128 instead).
+ *  q, s     device [t][k] int8 token codes and [t] fp32 token scales (act_quant_int8,
+ *           block_norm_forward).
+ *  w_q, w_s device [n][k] int8 weight codes and [n] fp32 channel scales
+ *           (quantize_int8_channel), row-major as they are.
+ *  bias     device [n] fp32 or NULL.
+ *  y        device [t][n] of dtype y_dtype (Q4_F32, Q4_F16, Q4_BF16):
+ *           float(acc) * (s[t] * w_s[n]) + bias[n] in fp32, rounded once to y_dtype.
+ *  workspace device buffer of int8_linear_workspace_bytes(t, k, n) bytes (may be 0): INT32
+ *           sums of the K slices where a product has few output tiles.
+ *  The INT32 sums are exact, so equal inputs give equal bits on every path.  A NaN scale
+ *  gives a NaN row or column.
+ *  Requires k % 16 == 0, 16 <= k < 131072 (the INT32 sums hold 2^14 k), 1 <= n <= 2^20,
+ *  0 <= t <= 2^24; t == 0 is a no-op.
+ */
+Q4_API size_t int8_linear_workspace_bytes(int64_t t, int64_t k, int64_t n);
+Q4_API int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* w_q,
+                               const float* w_s, int64_t n, const float* bias, int y_dtype, void* y,
+                               void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * swiglu_linear_forward / swiglu_linear_backward -- the gated projection of a SwiGLU FFN in
+ * 16 bits, both products, the activation and their product in one launch:
+ *   h = silu(g) * u,   g = x w_gate^T,   u = x w_up^T,   silu(g) = g / (1 + e^-g)
+ * (the first half of the FFN that moe_int4_ffn_forward computes from INT4 weights).
+ *  x        device [t][h]; w_gate, w_up device [i][h]; h_out device [t][i]; dtype Q4_BF16
+ *           or Q4_F16 for all of them; products accumulate in fp32.
+ *  gu_out   device [t][2][i] or NULL: g and u rounded to dtype, which the backward pass
+ *           reads (a serving call passes NULL).
+ * Backward, given dh [t][i]:
+ *   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh silu(g)   (rounded to dtype: operands)
+ *   dx = dg w_gate + du w_up,   dw_gate = dg^T x,   dw_up = du^T x
+ *  dx       device [t][h];  dw_gate, dw_up device [i][h] (overwritten, not accumulated).
+ *  workspace device buffers of swiglu_linear_workspace_bytes / swiglu_linear_backward_
+ *           workspace_bytes bytes (K slices of products with few output tiles; dg and du).
+ *  Sums run in a fixed order: equal inputs give equal bits.  Outputs may not alias inputs.
+ *  Requires h % 8 == 0, i % 8 == 0, 8 <= h, i <= 2^20, 0 <= t <= 2^24.  t == 0: the
+ *  forward is a no-op, the backward sets dw_gate and dw_up to zero.
+ */
+Q4_API size_t swiglu_linear_workspace_bytes(int64_t t, int64_t h, int64_t i);
+Q4_API int swiglu_linear_forward(const void* x, const void* w_gate, const void* w_up, int64_t t, int64_t h, int64_t i,
+                                 int dtype, void* h_out, void* gu_out, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream);
+Q4_API size_t swiglu_linear_backward_workspace_bytes(int64_t t, int64_t h, int64_t i);
+Q4_API int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gu,
+                                  int64_t t, int64_t h, int64_t i, int dtype, void* dx, void* dw_gate, void* dw_up,
+                                  void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * block_norm_forward / block_norm_backward -- the norms before and after a block, with the
+ * block's gate and residual scale, in one pass over the rows:
+ *   p = N(y; w_post),   r = res + alpha * gate * p,   n = N(r; w_pre),
+ *   N(v; w)_i = v_i * w_i / sqrt(mean(v^2) + eps)
+ *  res      device [rows][cols]: the residual stream.
+ *  y        device [rows][cols]: the block's output, or NULL (r = res, nothing added).
+ *  w_post   device [cols]: weight of the norm after the block, or NULL (p = y).
+ *  gate     by gate_kind: Q4_GATE_NONE (NULL), Q4_GATE_CHANNEL [cols], Q4_GATE_TOKEN
+ *           [rows] or Q4_GATE_ELEMENT [rows][cols].
+ *  w_pre    device [cols]: weight of the norm before the next block, or NULL (no n).
+ *  All of dtype Q4_F32, Q4_F16 or Q4_BF16; w_post and gate need y; y or w_pre is required.
+ *  Sums and statistics are fp32; n is formed from the unrounded r.
+ * Forward outputs:
+ *  r_out    device [rows][cols] (required with y; NULL without): may be res or y itself.
+ *  n_out    device [rows][cols], or q_out device [rows][cols] int8 and s_out device [rows]
+ *           fp32: the per-token INT8 codes of the unrounded n, by act_quant_int8's rule (a
+ *           row whose n has a NaN or an infinity gets codes 0 and a NaN scale).  One of the two
+ *           forms with w_pre; all NULL without.  n_out may not alias an input.
+ * Backward, given dr (gradient to r; NULL = 0) and dn (to n; required with w_pre):
+ *  dres     device [rows][cols];  dy device [rows][cols] (with y).
+ *  dw_post, dw_pre  device [cols] fp32 (with the weights).
+ *  dgate    channel: fp32 [cols]; token: fp32 [rows]; element: dtype [rows][cols].
+ *  workspace device buffer of block_norm_workspace_bytes bytes (partial weight gradients).
+ *  Weight gradients are added in a fixed order: equal inputs give equal bits.  dres may be dr
+ *  itself; other outputs may not alias inputs.
+ *  Requires 1 <= cols <= 16384, rows >= 0, eps > 0, finite alpha.  rows == 0: the forward
+ *  is a no-op, the backward sets the weight and channel gate gradients to zero.
+ */
+#define Q4_GATE_NONE 0
+#define Q4_GATE_CHANNEL 1
+#define Q4_GATE_TOKEN 2
+#define Q4_GATE_ELEMENT 3
+typedef struct q4_block_norm_t {
+  int64_t rows;
+  int64_t cols;
+  int32_t dtype;
+  int32_t gate_kind;
+  float alpha;
+  float eps;
+  const void* res;
+  const void* y;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+} q4_block_norm_t;
+Q4_API int block_norm_forward(const q4_block_norm_t* norm, void* r_out, void* n_out, int8_t* q_out, float* s_out,
+                              hipStream_t stream);
+Q4_API size_t block_norm_workspace_bytes(const q4_block_norm_t* norm);
+Q4_API int block_norm_backward(const q4_block_norm_t* norm, const void* dr, const void* dn, void* dres, void* dy,
+                               float* dw_post, void* dgate, float* dw_pre, void* workspace, size_t ws_bytes,
+                               hipStream_t stream);
+
+/*
  * q4_set_stage_events -- optional per-stage timing markers for profiling tools.
  * When set (count >= Q4_NUM_STAGES, non-NULL arrays), every later
  * moe_int4_ffn_forward call on this thread records begin[s] before and end[s] after

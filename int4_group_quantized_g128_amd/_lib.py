@@ -29,6 +29,7 @@ Q4_F32, Q4_F16, Q4_BF16 = 0, 1, 2
 Q4_W4A16, Q4_W4A8, Q4_W8A8 = 0, 1, 2
 Q4_REPACK_PLAIN, Q4_REPACK_GATE_UP = 0, 1
 Q4_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
+Q4_GATE_NONE, Q4_GATE_CHANNEL, Q4_GATE_TOKEN, Q4_GATE_ELEMENT = 0, 1, 2, 3
 Q4_QFLAG_NONFINITE, Q4_QFLAG_SCALE_OVERFLOW = 1, 2
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -72,6 +73,13 @@ class Q4FfnPlan(ctypes.Structure):
     _fields_ = [("kernel", _i32), ("tile_rows", _i32), ("down_ksplit", _i32), ("prefill_addr_limited", _i32),
                 ("rows_in_token_order", _i32), ("combine_in_down", _i32), ("slot_tiles", _i32),
                 ("workspace_bytes", _i64)]
+
+
+class Q4BlockNorm(ctypes.Structure):
+    """Mirror of q4_block_norm_t."""
+    _fields_ = [("rows", _i64), ("cols", _i64), ("dtype", _i32), ("gate_kind", _i32),
+                ("alpha", ctypes.c_float), ("eps", ctypes.c_float), ("res", _vp), ("y", _vp), ("w_post", _vp),
+                ("gate", _vp), ("w_pre", _vp)]
 
 
 def _sig(name, res, args):
@@ -118,6 +126,16 @@ _sig("moe_int4_ffn_plan", _int, [ctypes.POINTER(Q4MoELayer), _i64, _int, ctypes.
 _sig("moe_expert_bits_by_hotness", _int, [ctypes.POINTER(_i64), _i32, ctypes.c_double, _int, ctypes.POINTER(_i32)])
 _sig("moe_expert_groups_by_hotness", _int, [ctypes.POINTER(_i64), _i32, ctypes.c_double, ctypes.c_double, _int,
                                             ctypes.POINTER(_i32)])
+_sig("quantize_int8_channel", _int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp])
+_sig("int8_linear_workspace_bytes", _sz, [_i64, _i64, _i64])
+_sig("int8_linear_forward", _int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _vp, _sz, _vp])
+_sig("swiglu_linear_workspace_bytes", _sz, [_i64, _i64, _i64])
+_sig("swiglu_linear_forward", _int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _sz, _vp])
+_sig("swiglu_linear_backward_workspace_bytes", _sz, [_i64, _i64, _i64])
+_sig("swiglu_linear_backward", _int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("block_norm_forward", _int, [ctypes.POINTER(Q4BlockNorm), _vp, _vp, _vp, _vp, _vp])
+_sig("block_norm_workspace_bytes", _sz, [ctypes.POINTER(Q4BlockNorm)])
+_sig("block_norm_backward", _int, [ctypes.POINTER(Q4BlockNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 _sig("q4_set_stage_events", _int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _int])
 
 raw = _lib  # the C entry points, for tests of the ABI itself
@@ -716,3 +734,172 @@ def int4_w4a8_group_acc(q, w_dev, n, asymmetric=False):
     _check("int4_w4a8_group_acc", _lib.int4_w4a8_group_acc(
         _ptr(q), rows, k, _ptr(w_dev), n, int(bool(asymmetric)), _ptr(acc), _stream()))
     return acc
+
+
+# ------------------------------------------------------------------ dense operators
+_16BIT = (torch.float16, torch.bfloat16)
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _like(t, ref, shape, name, dtype=None):
+    """t as a contiguous tensor of the given shape on ref's GPU, of ref's dtype (or dtype)."""
+    _need(t, dtype or ref.dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+    return t
+
+
+def _call(name, ref, *args):
+    """The C entry point on the current stream of ref's GPU."""
+    f = getattr(_lib, name)
+    if ref.device.index == torch.cuda.current_device():
+        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(ref.device):
+            rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != Q4_OK:
+        raise Q4Error(name, rc)
+
+
+def _dp(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(nbytes, ref):
+    return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if nbytes else None
+
+
+def quantize_int8_channel(w, flags=None):
+    """INT8 weights with one scale per output channel of w [n, k] -> (q int8 [n, k], s fp32 [n])."""
+    _need(w, _FLOATS, "w", 2)
+    n, k = w.shape
+    if flags is not None:
+        _like(flags, w, (1,), "flags", torch.int32)
+    q = torch.empty((n, k), dtype=torch.int8, device=w.device)
+    s = torch.empty(n, dtype=torch.float32, device=w.device)
+    _call("quantize_int8_channel", w, w.data_ptr(), _DT[w.dtype], n, k, q.data_ptr(), s.data_ptr(), _dp(flags))
+    return q, s
+
+
+def int8_linear_forward(q, s, w_q, w_s, bias=None, out_dtype=torch.bfloat16):
+    """y [t, n] = (q w_q^T) * (s[:, None] * w_s) (+ bias) for token codes q [t, k] with scales
+    s [t] and weight codes w_q [n, k] with scales w_s [n]; exact INT32 sums, y of out_dtype."""
+    _need(q, torch.int8, "q", 2)
+    _need(w_q, torch.int8, "w_q", 2)
+    t, k = q.shape
+    n = w_q.shape[0]
+    _like(w_q, q, (n, k), "w_q")
+    _like(s, q, (t,), "s", torch.float32)
+    _like(w_s, q, (n,), "w_s", torch.float32)
+    if bias is not None:
+        _like(bias, q, (n,), "bias", torch.float32)
+    if out_dtype not in _DT:
+        raise TypeError(f"out_dtype {out_dtype} is not fp32, fp16 or bf16")
+    y = torch.empty((t, n), dtype=out_dtype, device=q.device)
+    nbytes = _lib.int8_linear_workspace_bytes(t, k, n)
+    ws = _scratch(nbytes, q)
+    _call("int8_linear_forward", q, q.data_ptr(), s.data_ptr(), t, k, w_q.data_ptr(), w_s.data_ptr(), n, _dp(bias),
+          _DT[out_dtype], y.data_ptr(), _dp(ws), nbytes)
+    return y
+
+
+def _swiglu_args(x, w_gate, w_up):
+    _need(x, _16BIT, "x", 2)
+    _need(w_gate, x.dtype, "w_gate", 2)
+    t, h = x.shape
+    i = w_gate.shape[0]
+    _like(w_gate, x, (i, h), "w_gate")
+    _like(w_up, x, (i, h), "w_up")
+    return t, h, i
+
+
+def swiglu_linear_forward(x, w_gate, w_up, save=False):
+    """h [t, i] = silu(x w_gate^T) * (x w_up^T) for x [t, h] and weights [i, h] (fp16 or bf16).
+    With ``save`` -> (h, gu): gu [t, 2, i] holds the two products for the backward pass."""
+    t, h, i = _swiglu_args(x, w_gate, w_up)
+    out = torch.empty((t, i), dtype=x.dtype, device=x.device)
+    gu = torch.empty((t, 2, i), dtype=x.dtype, device=x.device) if save else None
+    nbytes = _lib.swiglu_linear_workspace_bytes(t, h, i)
+    ws = _scratch(nbytes, x)
+    _call("swiglu_linear_forward", x, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), t, h, i, _DT[x.dtype],
+          out.data_ptr(), _dp(gu), _dp(ws), nbytes)
+    return (out, gu) if save else out
+
+
+def swiglu_linear_backward(dh, x, w_gate, w_up, gu):
+    """Gradients (dx, dw_gate, dw_up) of swiglu_linear_forward for dh [t, i] and the saved gu."""
+    t, h, i = _swiglu_args(x, w_gate, w_up)
+    _like(dh, x, (t, i), "dh")
+    _like(gu, x, (t, 2, i), "gu")
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
+    nbytes = _lib.swiglu_linear_backward_workspace_bytes(t, h, i)
+    ws = _scratch(nbytes, x)
+    _call("swiglu_linear_backward", x, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gu.data_ptr(),
+          t, h, i, _DT[x.dtype], dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), _dp(ws), nbytes)
+    return dx, dwg, dwu
+
+
+def _norm_desc(res, y, w_post, gate, alpha, w_pre, eps):
+    _need(res, _FLOATS, "res", 2)
+    rows, cols = res.shape
+    if y is None and w_pre is None:
+        raise ValueError("y or w_pre is required")
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need y")
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None:
+            _like(t, res, (cols,), name)
+    if y is not None:
+        _like(y, res, (rows, cols), "y")
+    kind = Q4_GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        kind = {(rows, cols): Q4_GATE_ELEMENT, (rows, 1): Q4_GATE_TOKEN, (cols,): Q4_GATE_CHANNEL}.get(shape)
+        if kind is None:
+            raise ValueError(f"gate must be {(cols,)}, {(rows, 1)} or {(rows, cols)}, got {shape}")
+        _like(gate, res, shape, "gate")
+    return Q4BlockNorm(rows, cols, _DT[res.dtype], kind, alpha, eps, res.data_ptr(), _dp(y), _dp(w_post), _dp(gate),
+                       _dp(w_pre))
+
+
+def block_norm_forward(res, y=None, w_post=None, gate=None, alpha=1.0, w_pre=None, eps=1e-6, quantize=False):
+    """r = res + alpha * gate * N(y; w_post) and n = N(r; w_pre), N the RMS norm with a weight,
+    gate one value per channel [cols], per token [rows, 1] or per element [rows, cols].
+    -> (r, n), or (r, q, s) with ``quantize``: n as per-token INT8 codes and scales.  Without
+    y, r is res; without w_pre, n (and q, s) is None."""
+    d = _norm_desc(res, y, w_post, gate, alpha, w_pre, eps)
+    r = res if y is None else torch.empty_like(res)
+    n = q = s = None
+    if w_pre is not None and quantize:
+        q = torch.empty(res.shape, dtype=torch.int8, device=res.device)
+        s = torch.empty(res.shape[0], dtype=torch.float32, device=res.device)
+    elif w_pre is not None:
+        n = torch.empty_like(res)
+    _call("block_norm_forward", res, ctypes.byref(d), None if y is None else r.data_ptr(), _dp(n), _dp(q), _dp(s))
+    return (r, q, s) if quantize else (r, n)
+
+
+def block_norm_backward(dr, dn, res, y=None, w_post=None, gate=None, alpha=1.0, w_pre=None, eps=1e-6):
+    """Gradients of block_norm_forward for dr (or None: 0) and dn (with w_pre): a dict with
+    "res", "y", "w_post", "gate", "w_pre" (None where the input is absent); weight, channel
+    and token gate gradients are fp32."""
+    d = _norm_desc(res, y, w_post, gate, alpha, w_pre, eps)
+    if (dn is None) != (w_pre is None):
+        raise ValueError("dn must be given iff w_pre is")
+    for name, t in (("dr", dr), ("dn", dn)):
+        if t is not None:
+            _like(t, res, res.shape, name)
+    f32 = dict(dtype=torch.float32, device=res.device)
+    cols = res.shape[1]
+    out = {"res": torch.empty_like(res), "y": None if y is None else torch.empty_like(res),
+           "w_post": None if w_post is None else torch.empty(cols, **f32),
+           "w_pre": None if w_pre is None else torch.empty(cols, **f32), "gate": None}
+    if gate is not None:
+        out["gate"] = torch.empty_like(gate) if d.gate_kind == Q4_GATE_ELEMENT else torch.empty(gate.shape, **f32)
+    nbytes = _lib.block_norm_workspace_bytes(ctypes.byref(d))
+    ws = _scratch(nbytes, res)
+    _call("block_norm_backward", res, ctypes.byref(d), _dp(dr), _dp(dn), out["res"].data_ptr(), _dp(out["y"]),
+          _dp(out["w_post"]), _dp(out["gate"]), _dp(out["w_pre"]), _dp(ws), nbytes)
+    return out

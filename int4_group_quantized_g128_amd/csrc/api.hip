@@ -1134,4 +1134,165 @@ int int4_w4a8_group_acc(const int8_t* q, int64_t rows, int64_t k, const void* w_
   return check_hip(launch_gemm(g, 2, GEMM_GROUP_ACC, 1, stream), "group acc gemm");
 }
 
+// ---------------------------------------------------------------- dense operators
+static bool float_dtype(int d) { return d == Q4_F32 || d == Q4_F16 || d == Q4_BF16; }
+static constexpr int64_t kMaxWidth = int64_t(1) << 20, kMaxTokens = int64_t(1) << 24;
+
+int quantize_int8_channel(const void* w, int w_dtype, int64_t n, int64_t k, int8_t* q, float* s, int32_t* flags_dev,
+                          hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(float_dtype(w_dtype), Q4_ERR_DTYPE, "w_dtype %d", w_dtype);
+  Q4_REQUIRE(n >= 1 && n <= kMaxWidth && k >= 16 && k % 16 == 0 && k < 131072, Q4_ERR_SHAPE,
+             "need 1 <= n <= 2^20 and k a positive multiple of 16 below 131072");
+  Q4_REQUIRE(w && q && s, Q4_ERR_NULL, "w, q and s are required");
+  Q4_REQUIRE(!misaligned(w) && !misaligned(q) && !misaligned(s), Q4_ERR_ALIGN,
+             "device pointers must be 16-byte aligned");
+  return check_hip(launch_quantize8_rows(w, w_dtype, n, k, q, s, flags_dev, stream), "quantize8 channel launch");
+}
+
+static bool int8_linear_shape(int64_t t, int64_t k, int64_t n) {
+  return t >= 0 && t <= kMaxTokens && k >= 16 && k % 16 == 0 && k < 131072 && n >= 1 && n <= kMaxWidth;
+}
+
+size_t int8_linear_workspace_bytes(int64_t t, int64_t k, int64_t n) {
+  return int8_linear_shape(t, k, n) ? size_t(int8_linear_workspace(t, k, n)) : 0;
+}
+
+int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* w_q, const float* w_s,
+                        int64_t n, const float* bias, int y_dtype, void* y, void* workspace, size_t ws_bytes,
+                        hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(float_dtype(y_dtype), Q4_ERR_DTYPE, "y_dtype %d", y_dtype);
+  Q4_REQUIRE(int8_linear_shape(t, k, n), Q4_ERR_SHAPE,
+             "need 0 <= t <= 2^24, k a positive multiple of 16 below 131072, 1 <= n <= 2^20");
+  if (t == 0) return ok();
+  Q4_REQUIRE(q && s && w_q && w_s && y, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(q) && !misaligned(s) && !misaligned(w_q) && !misaligned(w_s) && !misaligned(bias) &&
+                 !misaligned(y), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(int8_linear_workspace(t, k, n));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_int8_linear(q, s, t, k, w_q, w_s, n, bias, y_dtype, y, workspace, stream),
+                   "int8 linear launch");
+}
+
+static bool swiglu_shape(int64_t t, int64_t h, int64_t i) {
+  return t >= 0 && t <= kMaxTokens && h >= 8 && h % 8 == 0 && h <= kMaxWidth && i >= 8 && i % 8 == 0 && i <= kMaxWidth;
+}
+
+size_t swiglu_linear_workspace_bytes(int64_t t, int64_t h, int64_t i) {
+  return swiglu_shape(t, h, i) ? size_t(swiglu_linear_workspace(t, h, i)) : 0;
+}
+
+size_t swiglu_linear_backward_workspace_bytes(int64_t t, int64_t h, int64_t i) {
+  return swiglu_shape(t, h, i) ? size_t(swiglu_linear_bwd_workspace(t, h, i)) : 0;
+}
+
+int swiglu_linear_forward(const void* x, const void* w_gate, const void* w_up, int64_t t, int64_t h, int64_t i,
+                          int dtype, void* h_out, void* gu_out, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(dtype == Q4_F16 || dtype == Q4_BF16, Q4_ERR_DTYPE, "dtype must be Q4_F16 or Q4_BF16");
+  Q4_REQUIRE(swiglu_shape(t, h, i), Q4_ERR_SHAPE, "need 0 <= t <= 2^24, h and i positive multiples of 8 up to 2^20");
+  if (t == 0) return ok();
+  Q4_REQUIRE(x && w_gate && w_up && h_out, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(x) && !misaligned(w_gate) && !misaligned(w_up) && !misaligned(h_out) && !misaligned(gu_out),
+             Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(swiglu_linear_workspace(t, h, i));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_swiglu_linear(x, w_gate, w_up, t, h, i, dtype == Q4_F16, h_out, gu_out, workspace, stream),
+                   "swiglu linear launch");
+}
+
+int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gu,
+                           int64_t t, int64_t h, int64_t i, int dtype, void* dx, void* dw_gate, void* dw_up,
+                           void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(dtype == Q4_F16 || dtype == Q4_BF16, Q4_ERR_DTYPE, "dtype must be Q4_F16 or Q4_BF16");
+  Q4_REQUIRE(swiglu_shape(t, h, i), Q4_ERR_SHAPE, "need 0 <= t <= 2^24, h and i positive multiples of 8 up to 2^20");
+  Q4_REQUIRE(dw_gate && dw_up && (t == 0 || (dh && x && w_gate && w_up && gu && dx)), Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(dh) && !misaligned(x) && !misaligned(w_gate) && !misaligned(w_up) && !misaligned(gu) &&
+                 !misaligned(dx) && !misaligned(dw_gate) && !misaligned(dw_up),
+             Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(swiglu_linear_bwd_workspace(t, h, i));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_swiglu_linear_bwd(dh, x, w_gate, w_up, gu, t, h, i, dtype == Q4_F16, dx, dw_gate, dw_up,
+                                            workspace, stream),
+                   "swiglu linear backward launch");
+}
+
+static int validate_norm(const q4_block_norm_t* p) {
+  Q4_REQUIRE(p, Q4_ERR_NULL, "norm descriptor is NULL");
+  Q4_REQUIRE(float_dtype(p->dtype), Q4_ERR_DTYPE, "dtype %d", p->dtype);
+  Q4_REQUIRE(p->rows >= 0 && p->rows < (int64_t(1) << 40), Q4_ERR_SHAPE, "rows %lld", (long long)p->rows);
+  Q4_REQUIRE(p->cols >= 1 && p->cols <= block_norm_max_cols(), Q4_ERR_SHAPE, "cols %lld not in [1, %d]",
+             (long long)p->cols, block_norm_max_cols());
+  Q4_REQUIRE(p->gate_kind >= Q4_GATE_NONE && p->gate_kind <= Q4_GATE_ELEMENT, Q4_ERR_DTYPE, "gate_kind %d",
+             p->gate_kind);
+  Q4_REQUIRE(p->eps > 0.f && std::isfinite(p->eps), Q4_ERR_SHAPE, "eps must be positive and finite");
+  Q4_REQUIRE(std::isfinite(p->alpha), Q4_ERR_SHAPE, "alpha must be finite");
+  if (p->rows > 0) {   // (with no rows, res and y may be empty buffers: NULL)
+    Q4_REQUIRE(p->y || p->w_pre, Q4_ERR_NULL, "y or w_pre is required");
+    Q4_REQUIRE(p->y || (!p->w_post && p->gate_kind == Q4_GATE_NONE), Q4_ERR_NULL, "w_post and gate need y");
+    Q4_REQUIRE((p->gate != nullptr) == (p->gate_kind != Q4_GATE_NONE), Q4_ERR_NULL,
+               "gate must be given iff gate_kind is set");
+    Q4_REQUIRE(p->res, Q4_ERR_NULL, "res is required");
+  }
+  Q4_REQUIRE(!misaligned(p->res) && !misaligned(p->y) && !misaligned(p->w_post) && !misaligned(p->gate) &&
+                 !misaligned(p->w_pre), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  return ok();
+}
+
+static BlockNormArgs norm_args(const q4_block_norm_t* p) {
+  return BlockNormArgs{p->rows, int32_t(p->cols), p->gate_kind, p->alpha, p->eps, p->res, p->y, p->w_post, p->gate,
+                       p->w_pre};
+}
+
+int block_norm_forward(const q4_block_norm_t* p, void* r_out, void* n_out, int8_t* q_out, float* s_out,
+                       hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_norm(p)) return rc;
+  if (p->rows == 0) return ok();
+  Q4_REQUIRE((r_out != nullptr) == (p->y != nullptr), Q4_ERR_NULL, "r_out must be given iff y is");
+  Q4_REQUIRE((q_out != nullptr) == (s_out != nullptr), Q4_ERR_NULL, "q_out and s_out go together");
+  Q4_REQUIRE(int(n_out != nullptr) + int(q_out != nullptr) == (p->w_pre ? 1 : 0), Q4_ERR_NULL,
+             "with w_pre one of n_out and q_out is required, without it neither");
+  Q4_REQUIRE(!misaligned(r_out) && !misaligned(n_out) && !misaligned(q_out) && !misaligned(s_out), Q4_ERR_ALIGN,
+             "device pointers must be 16-byte aligned");
+  return check_hip(launch_block_norm(norm_args(p), p->dtype, r_out, n_out, q_out, s_out, stream), "block norm launch");
+}
+
+size_t block_norm_workspace_bytes(const q4_block_norm_t* p) {
+  if (validate_norm(p) != Q4_OK) return 0;
+  return size_t(block_norm_bwd_workspace(p->rows, p->cols));
+}
+
+int block_norm_backward(const q4_block_norm_t* p, const void* dr, const void* dn, void* dres, void* dy, float* dw_post,
+                        void* dgate, float* dw_pre, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_norm(p)) return rc;
+  Q4_REQUIRE((dw_post != nullptr) == (p->w_post != nullptr) && (dw_pre != nullptr) == (p->w_pre != nullptr),
+             Q4_ERR_NULL, "dw_post and dw_pre must be given iff their weights are");
+  if (p->rows > 0) {
+    Q4_REQUIRE((dn != nullptr) == (p->w_pre != nullptr), Q4_ERR_NULL, "dn must be given iff w_pre is");
+    Q4_REQUIRE(dres && (dy != nullptr) == (p->y != nullptr), Q4_ERR_NULL, "dres is required, dy iff y is given");
+  }
+  Q4_REQUIRE((p->rows == 0 && p->gate_kind != Q4_GATE_CHANNEL) ||
+                 (dgate != nullptr) == (p->gate_kind != Q4_GATE_NONE),
+             Q4_ERR_NULL, "dgate must be given iff the gate is");
+  Q4_REQUIRE(!misaligned(dr) && !misaligned(dn) && !misaligned(dres) && !misaligned(dy) && !misaligned(dw_post) &&
+                 !misaligned(dgate) && !misaligned(dw_pre), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(block_norm_bwd_workspace(p->rows, p->cols));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_block_norm_bwd(norm_args(p), p->dtype, dr, dn, dres, dy, dw_post, dgate, dw_pre,
+                                         static_cast<float*>(workspace), stream),
+                   "block norm backward launch");
+}
+
 }  // extern "C"

@@ -1,0 +1,680 @@
+// Dense products on the matrix cores: the INT8 linear with a scale per token and per
+// output channel, and the 16-bit gated projection with its gradients.
+//
+//   int8    y[t][n]  = (sum_k q[t][k] wq[n][k]) * (s[t] ws[n]) + b[n]
+//   swiglu  h        = silu(g) * u,  g = x Wg^T,  u = x Wu^T
+//   grads   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh silu(g)
+//           dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+//
+// Operands are read as they lie in memory: "KC" panels are contiguous along K (x, q and
+// the weights of the forward products), "MC" panels along their own row index (the
+// weights in dx; dg, du and x in the weight gradients), whose fragments come out of LDS
+// through the transposing 8-byte reads, so no transposed copy is ever made.
+//
+// Tiles: K advances 128 bytes (64 16-bit values, 128 codes) per step.  Panels are copied
+// global -> LDS in 16-byte chunks; the buffer descriptor of each step covers exactly what
+// is left of the panel, so rows past its end and the masked K tail read as zero.  Chunks
+// are XOR-swizzled so that the fragment reads hit distinct banks:
+//   KC  [rows][128 B]: chunk c of row r at c ^ (r / 2 % 8)  (two rows per bank period)
+//   MC  [64 k][2 rows B]: 32-byte piece p of row k at p ^ f(k), f from the bits of k that
+//       differ between the 8 rows a transposing read touches at once.
+#include <type_traits>
+
+#include "common.h"
+#include "internal.h"
+#include "lds_copy.h"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kStepBytes = 128;
+constexpr uint32_t kNoByte = 0x80000000u;   // a byte offset past every descriptor's range
+
+enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_INT8 = 2 };
+
+template <Act A> struct Num {
+  static constexpr int ESZ = A == Act::I8 ? 1 : 2;
+  static constexpr int STEP = kStepBytes / ESZ;   // K elements per step
+  typedef typename std::conditional<A == Act::I8, i32x4_t, f32x4_t>::type acc_t;
+  static Q4_DEVICE acc_t mfma(u32x4_t a, u32x4_t b, acc_t c) {
+    if constexpr (A == Act::I8) return mfma_i8_16x16x64(a, b, c);
+    else return mfma16x16x32<A>(a, b, c);
+  }
+};
+
+// One product C[m][n] = sum_k A(m, k) B(n, k), possibly over two K segments (a[s], b[s]),
+// for two batches (a[z], c[z]) or with two B panels side by side (swiglu: b[0], b[1]).
+struct DenseArgs {
+  const void* a[2];
+  const void* b[2];
+  int64_t lda, ldb;
+  int32_t M, N, K;
+  int32_t segs, batches, ksplit;
+  void* c[2];
+  int64_t ldc;
+  int32_t c_dtype;          // 0 fp32, 1 fp16, 2 bf16
+  const float* s_row;       // int8: token scales
+  const float* s_col;       // int8: channel scales
+  const float* bias;        // int8: or NULL
+  void* gu;                 // swiglu: [M][2][N] products, or NULL
+  void* part;               // ksplit > 1: [ksplit][batches][panels][M][N] fp32 / int32 sums
+};
+
+Q4_DEVICE uint16_t to16(float v, int dtype) {
+  return dtype == 1 ? bitcast<uint16_t>(_Float16(v)) : bitcast<uint16_t>(__bf16(v));
+}
+
+// Stores up to four consecutive values of a row.
+Q4_DEVICE void store4(void* c, int dtype, int64_t idx, f32x4_t v, int count, bool vec) {
+  if (dtype == 0) {
+    float* p = static_cast<float*>(c) + idx;
+    if (vec && count == 4) {
+      *reinterpret_cast<f32x4_t*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < count) p[i] = v[i];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(c) + idx;
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = to16(v[i], dtype);
+    if (vec && count == 4) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < count) p[i] = h[i];
+    }
+  }
+}
+
+// Result of four columns n .. n + 3 of row m (v: the product; v2: the second B panel's).
+template <Act A, int EPI>
+Q4_DEVICE void finish4(const DenseArgs& g, int z, int m, int n, typename Num<A>::acc_t v, typename Num<A>::acc_t v2) {
+  if (m >= g.M || n >= g.N) return;
+  const int count = min(4, g.N - n);
+  const bool vec = (g.ldc & 3) == 0;
+  const int64_t idx = int64_t(m) * g.ldc + n;
+  if constexpr (EPI == EPI_INT8) {
+    // the INT32 sum becomes fp32 (24 bits), then one product of the scales and one with it
+    const float sm = g.s_row[m];
+    f32x4_t y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = min(n + i, g.N - 1);
+      y[i] = float(v[i]) * (sm * g.s_col[c]) + (g.bias ? g.bias[c] : 0.f);
+    }
+    store4(g.c[0], g.c_dtype, idx, y, count, vec);
+  } else if constexpr (EPI == EPI_SWIGLU) {
+    f32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = swiglu(v[i], v2[i]);
+    store4(g.c[0], g.c_dtype, idx, h, count, vec);
+    if (g.gu) {
+      const int64_t at = int64_t(m) * 2 * g.ldc + n;
+      store4(g.gu, g.c_dtype, at, v, count, vec);
+      store4(g.gu, g.c_dtype, at + g.ldc, v2, count, vec);
+    }
+  } else {
+    store4(g.c[z], g.c_dtype, idx, v, count, vec);
+  }
+}
+
+// ---------------------------------------------------------------- panels in LDS
+// R rows of one operand, one K step: 128 R bytes, R / 8 copies of 1 KB.
+template <Act A, bool MC, int R>
+struct Panel {
+  static_assert(!MC || A != Act::I8, "transposing reads are for 16-bit values");
+  static constexpr int BYTES = R * kStepBytes;
+  static constexpr int COPIES = R / 8;
+  static constexpr int ESZ = Num<A>::ESZ;
+  static constexpr int CPR = MC ? R / 8 : 8;   // 16-byte chunks per LDS row
+
+  static Q4_DEVICE int swz(int r) {
+    if constexpr (!MC) return (r >> 1) & 7;
+    else if constexpr (R >= 128) return (r & 3) | ((r >> 3) & 1) << 2;
+    else return ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+  }
+
+  // Lane's place in copy `copy`: LDS row and the global chunk that lands in its slot.
+  static Q4_DEVICE void place(int copy, int lane, int& r, int& c) {
+    const int id = copy * 64 + lane;
+    r = id / CPR;
+    const int slot = id % CPR;
+    c = MC ? (((slot >> 1) ^ swz(r)) << 1 | (slot & 1)) : slot ^ swz(r);
+  }
+
+  // Byte offset of the lane's chunk from the panel's (first row, first k of the step).
+  // `left`: KC, bytes of K left at the step; MC, columns left at the first column.
+  static Q4_DEVICE uint32_t offset(int copy, int lane, int64_t ld, int left) {
+    int r, c;
+    place(copy, lane, r, c);
+    const bool in = MC ? c * 8 < left : c * 16 < left;
+    return in ? uint32_t(r * ld * ESZ + c * 16) : kNoByte;
+  }
+
+  // Descriptor from row `row0`, K element k0 to the panel's end (rows x K elements).
+  static Q4_DEVICE u32x4_t rsrc(const void* base, int64_t ld, int rows, int K, int row0, int k0) {
+    const int64_t at = (MC ? int64_t(k0) * ld + row0 : int64_t(row0) * ld + k0) * ESZ;
+    const int64_t left = (MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at;
+    return buffer_rsrc(static_cast<const uint8_t*>(base) + at,
+                       left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left);
+  }
+
+  // Fragment of rows r0 .. r0 + 15 (r0 % 16 == 0), half `sub` of the step: lane (row
+  // lane % 16, quarter lane / 16) holds 16 bytes of K, k = quarter-major.
+  static Q4_DEVICE u32x4_t frag(const uint8_t* lds, int r0, int sub, int lane) {
+    if constexpr (!MC) {
+      const int r = r0 + (lane & 15);
+      return *reinterpret_cast<const u32x4_t*>(lds + r * kStepBytes + (((4 * sub + (lane >> 4)) ^ swz(r)) << 4));
+    } else {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4* lptr;
+      u32x2_t v[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int k = 32 * sub + 8 * (lane >> 4) + 4 * t + ((lane & 15) >> 2);
+        const uint32_t at = lds_addr(lds) + k * (2 * R) + (((r0 >> 4) ^ swz(k)) << 5) + ((lane & 3) << 3);
+        v[t] = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uintptr_t)(at)));
+      }
+      return u32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
+    }
+  }
+};
+
+// Waits until at most N copies of this wave are in flight and its LDS reads are done,
+// then joins the workgroup's barrier.
+template <int N>
+Q4_DEVICE void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Work item of a workgroup: workgroup b runs on XCD b % 8; each XCD takes one contiguous
+// range of items (its L2 keeps the panels they share), in groups of 8 row tiles that walk
+// the column tiles together.
+struct Item {
+  int z, ks, mt, nt;
+};
+Q4_DEVICE Item item_of(int64_t b, int64_t total, int batches, int mtiles, int ntiles) {
+  const int64_t xcd = b % 8, per = total / 8, rest = total % 8;
+  int64_t i = xcd * per + (xcd < rest ? xcd : rest) + b / 8;
+  Item it;
+  const int64_t tiles = int64_t(mtiles) * ntiles;
+  it.ks = int(i / (tiles * batches));
+  i -= it.ks * tiles * batches;
+  it.z = int(i / tiles);
+  i -= it.z * tiles;
+  constexpr int GM = 8;
+  const int64_t band = i / (int64_t(GM) * ntiles);
+  const int m0 = int(band) * GM, gm = mtiles - m0 < GM ? mtiles - m0 : GM;
+  i -= band * GM * ntiles;
+  it.mt = m0 + int(i % gm);
+  it.nt = int(i / gm);
+  return it;
+}
+
+// ---------------------------------------------------------------- tile kernel
+// BM x BN per workgroup of 2 x 2 waves, a ring of three K steps in LDS: step s + 2 is
+// copied while step s is multiplied, one barrier per step.
+template <Act A, bool AMC, bool BMC, int BM, int BN, int EPI>
+__global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntiles) {
+  typedef Num<A> T;
+  typedef typename T::acc_t acc_t;
+  constexpr bool DUAL = EPI == EPI_SWIGLU;
+  constexpr int BP = DUAL ? BN / 2 : BN;            // rows of a B panel
+  typedef Panel<A, AMC, BM> PA;
+  typedef Panel<A, BMC, BP> PB;
+  constexpr int NP = DUAL ? 2 : 1;
+  constexpr int STAGE = PA::BYTES + NP * PB::BYTES;
+  constexpr int NS = 3;
+  constexpr int CA = PA::COPIES / 4, CB = PB::COPIES / 4;   // copies per wave
+  constexpr int CPW = CA + NP * CB;
+  constexpr int MB = BM / 32, NB = BP / 32;         // 16-blocks per wave
+  __shared__ __align__(16) uint8_t ring[NS * STAGE];
+
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int wm = wid & 1, wn = wid >> 1;
+  const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
+  const int m0 = it.mt * BM, n0 = it.nt * BP;
+  const int seg_steps = (g.K + T::STEP - 1) / T::STEP;
+  const int all = seg_steps * g.segs;
+  const int per = (all + g.ksplit - 1) / g.ksplit;
+  const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
+
+  auto issue = [&](int s) {
+    const int seg = s >= seg_steps ? 1 : 0;
+    const int k0 = (s - seg * seg_steps) * T::STEP;
+    const uint32_t base = lds_addr(ring) + uint32_t((s - s_begin) % NS) * STAGE;
+    const auto ra = PA::rsrc(g.a[g.batches > 1 ? it.z : seg], g.lda, g.M, g.K, m0, k0);
+    const int left = (g.K - k0) * T::ESZ;
+#pragma unroll
+    for (int j = 0; j < CA; ++j)
+      copy_to_lds<16>(ra, base + (wid * CA + j) * 1024, PA::offset(wid * CA + j, lane, g.lda, AMC ? g.M - m0 : left), 0u);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const auto rb = PB::rsrc(g.b[DUAL ? p : seg], g.ldb, g.N, g.K, n0, k0);
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        copy_to_lds<16>(rb, base + PA::BYTES + p * PB::BYTES + (wid * CB + j) * 1024,
+                        PB::offset(wid * CB + j, lane, g.ldb, BMC ? g.N - n0 : left), 0u);
+    }
+  };
+
+  acc_t acc[NP][MB][NB];
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[p][i][j] = acc_t{0, 0, 0, 0};
+
+  if (s_begin < s_end) {
+    issue(s_begin);
+    if (s_begin + 1 < s_end) issue(s_begin + 1);
+  }
+  for (int s = s_begin; s < s_end; ++s) {
+    // step s is in LDS for every wave, and every wave is done reading step s - 1
+    if (s + 1 < s_end) wait_barrier<CPW>();
+    else wait_barrier<0>();
+    if (s + 2 < s_end) issue(s + 2);
+    const uint8_t* base = ring + (s - s_begin) % NS * STAGE;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      u32x4_t fa[MB], fb[NP][NB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fa[i] = PA::frag(base, wm * (BM / 2) + 16 * i, sub, lane);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          fb[p][j] = PB::frag(base + PA::BYTES + p * PB::BYTES, wn * (BP / 2) + 16 * j, sub, lane);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[p][i][j] = T::mfma(fb[p][j], fa[i], acc[p][i][j]);
+    }
+  }
+
+  // lane: row m = lane % 16 of its block, columns 4 (lane / 16) .. + 3
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int m = m0 + wm * (BM / 2) + 16 * i + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int n = n0 + wn * (BP / 2) + 16 * j + 4 * (lane >> 4);
+      if (g.ksplit > 1) {
+        if (m < g.M) {
+          const int count = g.N - n < 4 ? g.N - n : 4;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const int64_t at = (((int64_t(it.ks) * g.batches + it.z) * NP + p) * g.M + m) * g.N + n;
+            uint32_t* o = static_cast<uint32_t*>(g.part) + at;
+            const u32x4_t v = bitcast<u32x4_t>(acc[p][i][j]);
+            if (count == 4 && (g.N & 3) == 0) {
+              *reinterpret_cast<u32x4_t*>(o) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (e < count) o[e] = v[e];
+            }
+          }
+        }
+      } else {
+        finish4<A, EPI>(g, it.z, m, n, acc[0][i][j], acc[NP - 1][i][j]);
+      }
+    }
+  }
+}
+
+// Adds the K slices of a split product in slice order and finishes four columns per thread.
+template <Act A, int EPI>
+__global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
+  typedef typename Num<A>::acc_t acc_t;
+  typedef typename std::conditional<A == Act::I8, int32_t, float>::type S;
+  constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
+  const int quads = (g.N + 3) / 4;
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= int64_t(g.batches) * g.M * quads) return;
+  const int n = int(i % quads) * 4;
+  const int64_t zm = i / quads;
+  const int z = int(zm / g.M), m = int(zm % g.M);
+  const int count = g.N - n < 4 ? g.N - n : 4;
+  const bool vec = count == 4 && (g.N & 3) == 0;
+  acc_t v[2];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    v[p] = acc_t{0, 0, 0, 0};
+    for (int s = 0; s < g.ksplit; ++s) {
+      const S* q = static_cast<const S*>(g.part) + (((int64_t(s) * g.batches + z) * NP + p) * g.M + m) * g.N + n;
+      if (vec) {
+        v[p] += *reinterpret_cast<const acc_t*>(q);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < count) v[p][e] += q[e];
+      }
+    }
+  }
+  finish4<A, EPI>(g, z, m, n, v[0], v[NP - 1]);
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 16 MB rows: bound by reading the weights once.  A workgroup owns 16 output
+// columns (16 of each projection for swiglu); its W waves take the K steps in turn and
+// feed the matrix core straight from global memory (16 bytes per lane, the lanes of one
+// column a whole 128-byte line per step), then add their sums through LDS in wave order.
+template <Act A, int MB, int W, int EPI>
+__global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
+  typedef Num<A> T;
+  typedef typename T::acc_t acc_t;
+  constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
+  __shared__ acc_t sums[W][NP * MB][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16;
+  const int64_t kb = int64_t(g.K) * T::ESZ;   // bytes of a row (a multiple of 16)
+  const int quarter = (lane >> 4) * 16;
+  const uint8_t* wp[NP];
+  const uint8_t* xp[MB];
+  const int col = min(n0 + (lane & 15), g.N - 1);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) wp[p] = static_cast<const uint8_t*>(g.b[p]) + col * kb + quarter;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    xp[i] = static_cast<const uint8_t*>(g.a[0]) + min(16 * i + (lane & 15), g.M - 1) * kb + quarter;
+  acc_t acc[NP][MB];
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[p][i] = acc_t{0, 0, 0, 0};
+
+  const int full = int(kb / kStepBytes);
+  constexpr int U = NP * MB >= 4 ? 2 : 4;   // steps in flight
+  int s = wave;
+  auto steps = [&](auto u_c) {
+    constexpr int N = decltype(u_c)::value;
+    u32x4_t w[N][2][NP], x[N][2][MB];
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = int64_t(s + u * W) * kStepBytes + h * 64;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) w[u][h][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp[p] + at));
+#pragma unroll
+        for (int i = 0; i < MB; ++i) x[u][h][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
+      }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int i = 0; i < MB; ++i) acc[p][i] = T::mfma(w[u][h][p], x[u][h][i], acc[p][i]);
+    s += N * W;
+  };
+  while (s + (U - 1) * W < full) steps(std::integral_constant<int, U>{});
+  while (s < full) steps(std::integral_constant<int, 1>{});
+  if (s == full && kb % kStepBytes) {   // the K tail: lanes past the row's end hold zeros
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = int64_t(full) * kStepBytes + h * 64;
+      const bool in = at + quarter < kb;
+      u32x4_t w[NP], x[MB];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) w[p] = in ? *reinterpret_cast<const u32x4_t*>(wp[p] + at) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < MB; ++i) x[i] = in ? *reinterpret_cast<const u32x4_t*>(xp[i] + at) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) acc[p][i] = T::mfma(w[p], x[i], acc[p][i]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) sums[wave][p * MB + i][lane] = acc[p][i];
+  __syncthreads();
+  for (int i = wave; i < MB; i += W) {
+    acc_t v[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      v[p] = sums[0][p * MB + i][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v[p] += sums[w][p * MB + i][lane];
+    }
+    finish4<A, EPI>(g, 0, 16 * i + (lane & 15), n0 + 4 * (lane >> 4), v[0], v[NP - 1]);
+  }
+}
+
+// ---------------------------------------------------------------- element-wise kernels
+// dg and du of 8 elements: bound by memory (3 reads, 2 writes of 2 bytes per element).
+// dg and du are rounded to 16 bits: they are matrix-core operands next.
+template <bool F16>
+__global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu,
+                                                     int64_t t, int64_t inter, uint16_t* __restrict__ dg,
+                                                     uint16_t* __restrict__ du) {
+  const int64_t vecs = inter / 8;
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < t * vecs; i += step) {
+    const int64_t row = i / vecs, c = (i - row * vecs) * 8;
+    uint16_t a[8], b[8], d[8];
+    *reinterpret_cast<uint4*>(a) = load16(gu + row * 2 * inter + c);
+    *reinterpret_cast<uint4*>(b) = load16(gu + row * 2 * inter + inter + c);
+    *reinterpret_cast<uint4*>(d) = load16(dh + row * inter + c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float gv = F16 ? f16_bits_to_f32(a[e]) : bf16_to_f32(a[e]);
+      const float uv = F16 ? f16_bits_to_f32(b[e]) : bf16_to_f32(b[e]);
+      const float dv = F16 ? f16_bits_to_f32(d[e]) : bf16_to_f32(d[e]);
+      const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-gv));
+      a[e] = to16(dv * uv * sig * (1.0f + gv * (1.0f - sig)), F16 ? 1 : 2);
+      b[e] = to16(dv * gv * sig, F16 ? 1 : 2);
+    }
+    *reinterpret_cast<uint4*>(dg + row * inter + c) = *reinterpret_cast<const uint4*>(a);
+    *reinterpret_cast<uint4*>(du + row * inter + c) = *reinterpret_cast<const uint4*>(b);
+  }
+}
+
+// One workgroup per weight row: amax, then the codes.
+template <int DT>
+__global__ void __launch_bounds__(256) k_quantize8_rows(const void* __restrict__ w, int64_t k, int8_t* __restrict__ q,
+                                                        float* __restrict__ s, int32_t* flags) {
+  __shared__ float red[4];
+  const int64_t row = blockIdx.x;
+  auto get = [&](int64_t i) -> float {
+    if constexpr (DT == 0) return static_cast<const float*>(w)[row * k + i];
+    else if constexpr (DT == 1) return f16_bits_to_f32(static_cast<const uint16_t*>(w)[row * k + i]);
+    else return bf16_to_f32(static_cast<const uint16_t*>(w)[row * k + i]);
+  };
+  float mx = 0.f;
+  bool bad = false;
+  for (int64_t i = threadIdx.x; i < k; i += 256) {
+    const float v = get(i);
+    bad |= !(fabsf(v) < __builtin_inff());
+    mx = fmaxf(mx, fabsf(v));
+  }
+  if (bad && flags) atomicOr(flags, 1);
+  mx = wave_max(mx);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float sc = mx / 127.0f;
+  for (int64_t i = threadIdx.x; i < k; i += 256)
+    q[row * k + i] = sc > 0.f ? int8_t(int(fminf(fmaxf(rintf(get(i) / sc), -127.f), 127.f))) : int8_t(0);
+  if (threadIdx.x == 0) s[row] = sc;
+}
+
+// ---------------------------------------------------------------- launches
+struct Plan {
+  int bm, bn, ksplit;   // bm == 0: the few-rows kernel
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile and K split of a product of `steps` K steps over `panels` B panels: the largest
+// tile that gives every CU work, else the smallest one with K split until the launch has
+// about 512 workgroups of at least 4 steps each.
+Plan plan_of(int64_t m, int64_t n, int panels, int64_t steps, int batches) {
+  const int64_t big = ceil_div(m, 128) * ceil_div(n * panels, 128) * batches;
+  if (big >= 256) return {128, 128, 1};
+  const int64_t tiles = ceil_div(m, 64) * ceil_div(n * panels, 64) * batches;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 4));
+  if (steps == 0) return {64, 64, 1};   // no tokens: the weight gradients are zero
+  const int64_t per = ceil_div(steps, std::min<int64_t>(want, 32));
+  return {64, 64, int(ceil_div(steps, per))};
+}
+
+int64_t part_bytes(const Plan& p, int64_t m, int64_t n, int panels, int batches) {
+  return p.ksplit > 1 ? int64_t(p.ksplit) * batches * panels * m * n * 4 : 0;
+}
+
+template <Act A, bool AMC, bool BMC, int EPI>
+hipError_t launch_tiles(DenseArgs g, const Plan& p, hipStream_t st) {
+  constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
+  g.ksplit = p.ksplit;
+  const int mt = int(ceil_div(g.M, p.bm)), nt = int(ceil_div(int64_t(g.N) * NP, p.bn));
+  const unsigned grid = unsigned(int64_t(mt) * nt * g.batches * p.ksplit);
+  if (p.bm == 128)
+    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 128, 128, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  else
+    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 64, 64, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ksplit == 1) return e;
+  const int64_t threads = int64_t(g.batches) * g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL((k_dense_join<A, EPI>), dim3(unsigned(ceil_div(threads, 256))), dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
+template <Act A, int EPI>
+hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
+  const dim3 grid(unsigned(ceil_div(g.N, 16)));
+  if (g.M <= 16) hipLaunchKernelGGL((k_dense_rows<A, 1, 8, EPI>), grid, dim3(512), 0, st, g);
+  else if (g.M <= 32) hipLaunchKernelGGL((k_dense_rows<A, 2, 8, EPI>), grid, dim3(512), 0, st, g);
+  else hipLaunchKernelGGL((k_dense_rows<A, 4, 8, EPI>), grid, dim3(512), 0, st, g);
+  return hipGetLastError();
+}
+
+bool few_rows(int64_t t) { return t <= 64; }
+
+}  // namespace
+
+hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k, int8_t* q, float* s, int32_t* flags,
+                                 hipStream_t st) {
+  const dim3 grid{unsigned(n)}, block(256);
+  if (dtype == 0) hipLaunchKernelGGL(k_quantize8_rows<0>, grid, block, 0, st, w, k, q, s, flags);
+  else if (dtype == 1) hipLaunchKernelGGL(k_quantize8_rows<1>, grid, block, 0, st, w, k, q, s, flags);
+  else hipLaunchKernelGGL(k_quantize8_rows<2>, grid, block, 0, st, w, k, q, s, flags);
+  return hipGetLastError();
+}
+
+int64_t int8_linear_workspace(int64_t t, int64_t k, int64_t n) {
+  if (t == 0 || few_rows(t)) return 0;
+  return part_bytes(plan_of(t, n, 1, ceil_div(k, kStepBytes), 1), t, n, 1, 1);
+}
+
+hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* wq, const float* ws,
+                              int64_t n, const float* bias, int y_dtype, void* y, void* work, hipStream_t st) {
+  DenseArgs g{};
+  g.a[0] = g.a[1] = q;
+  g.b[0] = g.b[1] = wq;
+  g.lda = g.ldb = k;
+  g.M = int32_t(t), g.N = int32_t(n), g.K = int32_t(k);
+  g.segs = g.batches = g.ksplit = 1;
+  g.c[0] = y;
+  g.ldc = n;
+  g.c_dtype = y_dtype;
+  g.s_row = s;
+  g.s_col = ws;
+  g.bias = bias;
+  g.part = work;
+  if (few_rows(t)) return launch_rows<Act::I8, EPI_INT8>(g, st);
+  return launch_tiles<Act::I8, false, false, EPI_INT8>(g, plan_of(t, n, 1, ceil_div(k, kStepBytes), 1), st);
+}
+
+int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i) {
+  if (t == 0 || few_rows(t)) return 0;
+  return part_bytes(plan_of(t, i, 2, ceil_div(h, 64), 1), t, i, 2, 1);
+}
+
+hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, int64_t t, int64_t h, int64_t i, int f16,
+                                void* out, void* gu, void* work, hipStream_t st) {
+  DenseArgs g{};
+  g.a[0] = g.a[1] = x;
+  g.b[0] = wg, g.b[1] = wu;
+  g.lda = g.ldb = h;
+  g.M = int32_t(t), g.N = int32_t(i), g.K = int32_t(h);
+  g.segs = g.batches = g.ksplit = 1;
+  g.c[0] = out;
+  g.ldc = i;
+  g.c_dtype = f16 ? 1 : 2;
+  g.gu = gu;
+  g.part = work;
+  if (few_rows(t))
+    return f16 ? launch_rows<Act::F16, EPI_SWIGLU>(g, st) : launch_rows<Act::BF16, EPI_SWIGLU>(g, st);
+  const Plan p = plan_of(t, i, 2, ceil_div(h, 64), 1);
+  return f16 ? launch_tiles<Act::F16, false, false, EPI_SWIGLU>(g, p, st)
+             : launch_tiles<Act::BF16, false, false, EPI_SWIGLU>(g, p, st);
+}
+
+// Workspace: dg and du [t][i] each, then the K slices of whichever product splits K.
+int64_t swiglu_linear_bwd_workspace(int64_t t, int64_t h, int64_t i) {
+  if (t == 0) return 0;
+  const int64_t dx = part_bytes(plan_of(t, h, 1, 2 * ceil_div(i, 64), 1), t, h, 1, 1);
+  const int64_t dw = part_bytes(plan_of(i, h, 1, ceil_div(t, 64), 2), i, h, 1, 2);
+  return 2 * align256(t * i * 2) + std::max(dx, dw);
+}
+
+hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* gu,
+                                    int64_t t, int64_t h, int64_t i, int f16, void* dx, void* dwg, void* dwu,
+                                    void* work, hipStream_t st) {
+  uint16_t* dg = static_cast<uint16_t*>(work);
+  uint16_t* du = dg + align256(t * i * 2) / 2;
+  void* part = reinterpret_cast<uint8_t*>(work) + 2 * align256(t * i * 2);
+  if (t > 0) {
+    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(t * (i / 8), 256), 4096));
+    const auto* d = static_cast<const uint16_t*>(dh);
+    const auto* p = static_cast<const uint16_t*>(gu);
+    if (f16) hipLaunchKernelGGL(k_swiglu_grad<true>, dim3(grid), dim3(256), 0, st, d, p, t, i, dg, du);
+    else hipLaunchKernelGGL(k_swiglu_grad<false>, dim3(grid), dim3(256), 0, st, d, p, t, i, dg, du);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  DenseArgs g{};
+  g.c_dtype = f16 ? 1 : 2;
+  g.ksplit = 1;
+  g.part = part;
+  g.ldc = h;
+  g.N = int32_t(h);
+  if (t > 0) {   // dx = dg Wg + du Wu: K runs over the gate rows, then the up rows
+    g.a[0] = dg, g.a[1] = du;
+    g.b[0] = wg, g.b[1] = wu;
+    g.lda = i, g.ldb = h;
+    g.M = int32_t(t), g.K = int32_t(i);
+    g.segs = 2, g.batches = 1;
+    g.c[0] = g.c[1] = dx;
+    const Plan p = plan_of(t, h, 1, 2 * ceil_div(i, 64), 1);
+    const hipError_t e = f16 ? launch_tiles<Act::F16, false, true, EPI_STORE>(g, p, st)
+                             : launch_tiles<Act::BF16, false, true, EPI_STORE>(g, p, st);
+    if (e != hipSuccess) return e;
+  }
+  // dWg = dg^T x and dWu = du^T x as two batches (t == 0: no K step, zeros)
+  g.a[0] = dg, g.a[1] = du;
+  g.b[0] = g.b[1] = x;
+  g.lda = i, g.ldb = h;
+  g.M = int32_t(i), g.K = int32_t(t);
+  g.segs = 1, g.batches = 2;
+  g.c[0] = dwg, g.c[1] = dwu;
+  const Plan p = plan_of(i, h, 1, ceil_div(t, 64), 2);
+  return f16 ? launch_tiles<Act::F16, true, true, EPI_STORE>(g, p, st)
+             : launch_tiles<Act::BF16, true, true, EPI_STORE>(g, p, st);
+}
+
+}  // namespace q4
