@@ -156,31 +156,51 @@ struct Panel {
     return in ? uint32_t(r * ld * ESZ + c * 16) : kNoByte;
   }
 
-  // Descriptor from row `row0`, K element k0 to the panel's end (rows x K elements).
-  static Q4_DEVICE u32x4_t rsrc(const void* base, int64_t ld, int rows, int K, int row0, int k0) {
-    const int64_t at = (MC ? int64_t(k0) * ld + row0 : int64_t(row0) * ld + k0) * ESZ;
-    const int64_t left = (MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at;
-    return buffer_rsrc(static_cast<const uint8_t*>(base) + at,
-                       left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left);
+  // Where the panel's K steps lie: the step at K element k0 starts k0 / STEP * inc bytes
+  // after base, and `left` bytes from there belong to the operand.
+  struct Source {
+    uint64_t base, left;
+    uint32_t inc;
+  };
+  static Q4_DEVICE Source source(const void* p, int64_t ld, int rows, int K, int row0) {
+    const uint64_t at = uint64_t(MC ? int64_t(row0) : int64_t(row0) * ld) * ESZ;
+    return Source{reinterpret_cast<uint64_t>(p) + at, uint64_t(MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at,
+                  MC ? uint32_t(ld) * uint32_t(Num<A>::STEP * ESZ) : uint32_t(kStepBytes)};
+  }
+  // Descriptor of step `s` (a step of the panel: left > s * inc), empty if !valid.
+  static Q4_DEVICE u32x4_t rsrc(const Source& f, int s, bool valid) {
+    const uint64_t off = uint64_t(uint32_t(s)) * f.inc;
+    const uint64_t a = f.base + off, left = f.left - off;
+    const uint32_t high = uint32_t(left >> 32) | uint32_t(left) >> 31;
+    const uint32_t n = high ? 0x7fffffffu : uint32_t(left);
+    return u32x4_t{uint32_t(a), uint32_t(a >> 32) & 0xffffu, valid ? n : 0u, 0x00020000u};
   }
 
-  // Fragment of rows r0 .. r0 + 15 (r0 % 16 == 0), half `sub` of the step: lane (row
-  // lane % 16, quarter lane / 16) holds 16 bytes of K, k = quarter-major.
-  static Q4_DEVICE u32x4_t frag(const uint8_t* lds, int r0, int sub, int lane) {
+  // Lane's byte address of a fragment read at block 0, half 0; blocks and halves flip bits
+  // or add constants (the swizzle depends on lane bits only).
+  static Q4_DEVICE uint32_t lane_base(int lane) {
     if constexpr (!MC) {
-      const int r = r0 + (lane & 15);
-      return *reinterpret_cast<const u32x4_t*>(lds + r * kStepBytes + (((4 * sub + (lane >> 4)) ^ swz(r)) << 4));
+      const int r = lane & 15;
+      return r * kStepBytes + (((lane >> 4) ^ swz(r)) << 4);
+    } else {
+      const int k = 8 * (lane >> 4) + ((lane & 15) >> 2);
+      return k * (2 * R) + (swz(k) << 5) + ((lane & 3) << 3);
+    }
+  }
+  // Fragment of rows r0 .. r0 + 15 (r0 % 16 == 0), half `sub` of the step: lane (row
+  // lane % 16, quarter lane / 16) holds 16 bytes of K, quarter-major.  lds: the panel's LDS
+  // byte address (a multiple of 1024), lb: lane_base.
+  static Q4_DEVICE u32x4_t frag(uint32_t lds, uint32_t lb, int r0, int sub) {
+    if constexpr (!MC) {
+      typedef __attribute__((address_space(3))) const u32x4_t* lptr;
+      return *(lptr)(uintptr_t)(lds + r0 * kStepBytes + (lb ^ (sub << 6)));
     } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* lptr;
-      u32x2_t v[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int k = 32 * sub + 8 * (lane >> 4) + 4 * t + ((lane & 15) >> 2);
-        const uint32_t at = lds_addr(lds) + k * (2 * R) + (((r0 >> 4) ^ swz(k)) << 5) + ((lane & 3) << 3);
-        v[t] = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uintptr_t)(at)));
-      }
-      return u32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
+      const uint32_t at = lds + sub * 32 * (2 * R) + (lb ^ ((r0 >> 4) << 5));
+      const u32x2_t a = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uintptr_t)(at)));
+      const u32x2_t b = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uintptr_t)(at + 4 * (2 * R))));
+      return u32x4_t{a[0], a[1], b[0], b[1]};
     }
   }
 };
@@ -245,24 +265,30 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
   const int per = (all + g.ksplit - 1) / g.ksplit;
   const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
 
+  const auto fa0 = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0);
+  const auto fb0 = PB::source(g.b[0], g.ldb, g.N, g.K, n0);
+  const auto fa1 = PA::source(g.a[1], g.lda, g.M, g.K, m0);   // second K segment
+  const auto fb1 = PB::source(g.b[1], g.ldb, g.N, g.K, n0);   // second K segment or B panel
+  const uint32_t lds0 = lds_addr(ring);
   auto issue = [&](int s) {
-    const int seg = s >= seg_steps ? 1 : 0;
-    const int k0 = (s - seg * seg_steps) * T::STEP;
-    const uint32_t base = lds_addr(ring) + uint32_t((s - s_begin) % NS) * STAGE;
-    const auto ra = PA::rsrc(g.a[g.batches > 1 ? it.z : seg], g.lda, g.M, g.K, m0, k0);
-    const int left = (g.K - k0) * T::ESZ;
+    const bool second = s >= seg_steps;
+    const int ss = second ? s - seg_steps : s;
+    const uint32_t base = lds0 + uint32_t((s - s_begin) % NS) * STAGE;
+    const auto ra = PA::rsrc(second ? fa1 : fa0, ss, true);
+    const int left = g.K * T::ESZ - ss * kStepBytes;
 #pragma unroll
     for (int j = 0; j < CA; ++j)
       copy_to_lds<16>(ra, base + (wid * CA + j) * 1024, PA::offset(wid * CA + j, lane, g.lda, AMC ? g.M - m0 : left), 0u);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const auto rb = PB::rsrc(g.b[DUAL ? p : seg], g.ldb, g.N, g.K, n0, k0);
+      const auto rb = PB::rsrc(p == 1 || second ? fb1 : fb0, ss, true);
 #pragma unroll
       for (int j = 0; j < CB; ++j)
         copy_to_lds<16>(rb, base + PA::BYTES + p * PB::BYTES + (wid * CB + j) * 1024,
                         PB::offset(wid * CB + j, lane, g.ldb, BMC ? g.N - n0 : left), 0u);
     }
   };
+  const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
 
   acc_t acc[NP][MB][NB];
 #pragma unroll
@@ -281,17 +307,17 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
     if (s + 1 < s_end) wait_barrier<CPW>();
     else wait_barrier<0>();
     if (s + 2 < s_end) issue(s + 2);
-    const uint8_t* base = ring + (s - s_begin) % NS * STAGE;
+    const uint32_t base = lds0 + uint32_t((s - s_begin) % NS) * STAGE;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       u32x4_t fa[MB], fb[NP][NB];
 #pragma unroll
-      for (int i = 0; i < MB; ++i) fa[i] = PA::frag(base, wm * (BM / 2) + 16 * i, sub, lane);
+      for (int i = 0; i < MB; ++i) fa[i] = PA::frag(base, lba, wm * (BM / 2) + 16 * i, sub);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-          fb[p][j] = PB::frag(base + PA::BYTES + p * PB::BYTES, wn * (BP / 2) + 16 * j, sub, lane);
+          fb[p][j] = PB::frag(base + PA::BYTES + p * PB::BYTES, lbb, wn * (BP / 2) + 16 * j, sub);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
@@ -330,6 +356,179 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
       }
     }
   }
+}
+
+// ---------------------------------------------------------------- large tile kernel
+// 256 x 256 per workgroup of 8 waves (2 x 4), two K steps in LDS (128 KB).  A wave owns 64
+// rows of each 128-row half and 32 columns of each 128-column half, so a K step is four
+// quadrant phases of 16 MFMAs, each needing one new half-panel fragment set in registers:
+//     phase         0        1        2        3
+//     LDS reads     A0(k)    B1(k)    A1(k)    B0(k+1)
+//     products      A0 B0    A0 B1    A1 B1    A1 B0
+//     copies        A1(k+1)  B0(k+2)  A0(k+2)  B1(k+2)
+// A half panel is copied six phases before it is read and two phases after its slot's last
+// read, so a wave waits only for its copies of five phases ago (10 stay in flight).
+// Waves 4..7 (the other wave of each SIMD) run half a phase behind waves 0..3: while one
+// wave of a SIMD reads LDS and issues copies, the other feeds the matrix core.
+template <Act A, bool AMC, bool BMC, int EPI>
+__global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, int ntiles) {
+  typedef Num<A> T;
+  typedef typename T::acc_t acc_t;
+  constexpr bool DUAL = EPI == EPI_SWIGLU;
+  typedef Panel<A, AMC, 128> PA;
+  typedef Panel<A, BMC, 128> PB;
+  constexpr int HB = PA::BYTES;                     // 16 KB per half panel
+  __shared__ __align__(16) uint8_t ring[2 * 4 * HB];   // [step % 2][A0, A1, B0, B1]
+
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int wm = wid >> 2, wn = wid & 3;
+  const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
+  const int m0 = it.mt * 256, n0 = it.nt * (DUAL ? 128 : 256);
+  const int seg_steps = (g.K + T::STEP - 1) / T::STEP;
+  const int steps = seg_steps * g.segs;
+  const uint32_t lds0 = lds_addr(ring);
+
+  // Copies half panel `h` (0, 1: A; 2, 3: B) of step s: two 1 KB copies per wave.  Past the
+  // last step (or the last row) the descriptor is empty: the copy counts, and writes zeros.
+  typename PA::Source fsa[2];
+  typename PB::Source fsb[2];
+  bool in[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int rb = n0 + (DUAL ? 0 : h * 128);
+    fsa[h] = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0 + h * 128);
+    fsb[h] = PB::source(DUAL && h ? g.b[1] : g.b[0], g.ldb, g.N, g.K, rb);
+    in[h] = m0 + h * 128 < g.M;
+    in[2 + h] = rb < g.N;
+  }
+  const uint64_t da = reinterpret_cast<uint64_t>(g.a[1]) - reinterpret_cast<uint64_t>(g.a[0]);
+  const uint64_t db = reinterpret_cast<uint64_t>(g.b[1]) - reinterpret_cast<uint64_t>(g.b[0]);
+  auto issue = [&](auto h_c, int s) {
+    constexpr int h = decltype(h_c)::value;
+    constexpr bool IS_A = h < 2;
+    constexpr int half = h & 1;
+    typedef typename std::conditional<IS_A, PA, PB>::type P;
+    constexpr bool MC = IS_A ? AMC : BMC;
+    typename P::Source f;
+    if constexpr (IS_A) f = fsa[half];
+    else f = fsb[half];
+    const bool second = s >= seg_steps;
+    const int ss = second ? s - seg_steps : s;
+    f.base += second ? (IS_A ? da : db) : 0;
+    const u32x4_t rs = P::rsrc(f, ss, in[h] && s < steps);
+    const int left = MC ? (IS_A ? g.M - m0 : g.N - n0) - half * 128 : g.K * T::ESZ - ss * kStepBytes;
+    const uint32_t at = lds0 + uint32_t(s & 1) * (4 * HB) + h * HB + wid * 2048;
+    const int64_t ld = IS_A ? g.lda : g.ldb;
+    copy2_to_lds(rs, at, P::offset(2 * wid, lane, ld, left), P::offset(2 * wid + 1, lane, ld, left));
+  };
+  const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
+  typedef std::integral_constant<int, 0> A0;
+  typedef std::integral_constant<int, 1> A1;
+  typedef std::integral_constant<int, 2> B0;
+  typedef std::integral_constant<int, 3> B1;
+
+  acc_t acc[2][2][4][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = acc_t{0, 0, 0, 0};
+  u32x4_t fa[4][2], fb[2][2][2];   // fb[register set][block][sub]
+
+  auto read_a = [&](int s, int half) {
+    const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + half * HB;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i][sub] = PA::frag(p, lba, wm * 64 + 16 * i, sub);
+  };
+  auto read_b = [&](int s, int half, auto set_c) {
+    constexpr int set = decltype(set_c)::value;
+    const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + (2 + half) * HB;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[set][j][sub] = PB::frag(p, lbb, wn * 32 + 16 * j, sub);
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  auto phase_end = [&] {   // end of a load section
+    fence();
+    asm volatile("s_waitcnt vmcnt(10)\n\ts_barrier\n\ts_waitcnt lgkmcnt(0)" ::: "memory");
+    fence();
+    __builtin_amdgcn_s_setprio(1);
+  };
+  auto multiply = [&](auto ha, auto hb, auto set_c) {
+    constexpr int a = decltype(ha)::value, b = decltype(hb)::value, set = decltype(set_c)::value;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = T::mfma(fb[set][j][sub], fa[i][sub], acc[a][b][i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    fence();
+    asm volatile("s_barrier" ::: "memory");
+    fence();
+  };
+  typedef std::integral_constant<int, 0> Z;
+  typedef std::integral_constant<int, 1> O;
+  // one K step; `lo` / `hi`: register sets of B0(k) and B1(k)
+  auto step = [&](int s, auto lo, auto hi) {
+    read_a(s, 0);
+    issue(A1{}, s + 1);
+    phase_end();
+    multiply(Z{}, Z{}, lo);
+    read_b(s, 1, hi);
+    issue(B0{}, s + 2);
+    phase_end();
+    multiply(Z{}, O{}, hi);
+    read_a(s, 1);
+    issue(A0{}, s + 2);
+    phase_end();
+    multiply(O{}, O{}, hi);
+    read_b(s + 1, 0, hi);
+    issue(B1{}, s + 2);
+    phase_end();
+    multiply(O{}, Z{}, lo);
+  };
+
+  issue(B0{}, 0);
+  issue(A0{}, 0);
+  issue(B1{}, 0);
+  issue(A1{}, 0);
+  issue(B0{}, 1);
+  issue(A0{}, 1);
+  issue(B1{}, 1);
+  asm volatile("s_waitcnt vmcnt(10)\n\ts_barrier" ::: "memory");
+  read_b(0, 0, Z{});
+  if (wid >= 4) asm volatile("s_barrier" ::: "memory");
+  for (int s = 0; s < steps; s += 2) {   // (an odd last step is followed by one of zeros)
+    step(s, Z{}, O{});
+    step(s + 1, O{}, Z{});
+  }
+  if (wid < 4) asm volatile("s_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
+
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + a * 128 + wm * 64 + 16 * i + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = n0 + wn * 32 + 16 * j + 4 * (lane >> 4);
+        if constexpr (DUAL) {
+          finish4<A, EPI>(g, it.z, m, n, acc[a][0][i][j], acc[a][1][i][j]);
+        } else {
+          finish4<A, EPI>(g, it.z, m, n, acc[a][0][i][j], acc[a][0][i][j]);
+          finish4<A, EPI>(g, it.z, m, n + 128, acc[a][1][i][j], acc[a][1][i][j]);
+        }
+      }
+    }
 }
 
 // Adds the K slices of a split product in slice order and finishes four columns per thread.
@@ -523,8 +722,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // tile that gives every CU work, else the smallest one with K split until the launch has
 // about 512 workgroups of at least 4 steps each.
 Plan plan_of(int64_t m, int64_t n, int panels, int64_t steps, int batches) {
-  const int64_t big = ceil_div(m, 128) * ceil_div(n * panels, 128) * batches;
-  if (big >= 256) return {128, 128, 1};
+  if (ceil_div(m, 256) * ceil_div(n * panels, 256) * batches >= 192) return {256, 256, 1};
+  if (ceil_div(m, 128) * ceil_div(n * panels, 128) * batches >= 256) return {128, 128, 1};
   const int64_t tiles = ceil_div(m, 64) * ceil_div(n * panels, 64) * batches;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 4));
   if (steps == 0) return {64, 64, 1};   // no tokens: the weight gradients are zero
@@ -542,7 +741,9 @@ hipError_t launch_tiles(DenseArgs g, const Plan& p, hipStream_t st) {
   g.ksplit = p.ksplit;
   const int mt = int(ceil_div(g.M, p.bm)), nt = int(ceil_div(int64_t(g.N) * NP, p.bn));
   const unsigned grid = unsigned(int64_t(mt) * nt * g.batches * p.ksplit);
-  if (p.bm == 128)
+  if (p.bm == 256)
+    hipLaunchKernelGGL((k_dense_big<A, AMC, BMC, EPI>), dim3(grid), dim3(512), 0, st, g, mt, nt);
+  else if (p.bm == 128)
     hipLaunchKernelGGL((k_dense<A, AMC, BMC, 128, 128, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else
     hipLaunchKernelGGL((k_dense<A, AMC, BMC, 64, 64, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);

@@ -56,4 +56,18 @@ Q4_DEVICE void copy_to_lds(const u32x4_t& rsrc, uint32_t lds_in, uint32_t voff, 
   (void)saved;
 }
 
+// Two direct-to-LDS copies of 16 bytes per lane, to lds and lds + 1024 (see copy_to_lds).
+Q4_DEVICE void copy2_to_lds(const u32x4_t& rsrc, uint32_t lds_in, uint32_t voff0, uint32_t voff1) {
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_in);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_nop 4\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %2, %4, 0 offen lds\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %3, %4, 0 offen lds\n\ts_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(voff0), "v"(voff1), "s"(rsrc)
+      : "memory", "scc");
+  (void)saved;
+}
+
 }  // namespace q4
