@@ -91,35 +91,121 @@ Q4_DEVICE void store4(void* c, int dtype, int64_t idx, f32x4_t v, int count, boo
   }
 }
 
-// Result of four columns n .. n + 3 of row m (v: the product; v2: the second B panel's).
-template <Act A, int EPI>
-Q4_DEVICE void finish4(const DenseArgs& g, int z, int m, int n, typename Num<A>::acc_t v, typename Num<A>::acc_t v2) {
-  if (m >= g.M || n >= g.N) return;
-  const int count = min(4, g.N - n);
-  const bool vec = (g.ldc & 3) == 0;
-  const int64_t idx = int64_t(m) * g.ldc + n;
+// Channel scales and bias of four columns n .. n + 3.
+struct ColScales {
+  f32x4_t s, b;
+};
+template <int EPI>
+Q4_DEVICE ColScales col_scales(const DenseArgs& g, int n) {
+  ColScales r;
   if constexpr (EPI == EPI_INT8) {
-    // the INT32 sum becomes fp32 (24 bits), then one product of the scales and one with it
-    const float sm = g.s_row[m];
-    f32x4_t y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = min(n + i, g.N - 1);
-      y[i] = float(v[i]) * (sm * g.s_col[c]) + (g.bias ? g.bias[c] : 0.f);
+      r.s[i] = g.s_col[c];
+      r.b[i] = g.bias ? g.bias[c] : 0.f;
     }
-    store4(g.c[0], g.c_dtype, idx, y, count, vec);
-  } else if constexpr (EPI == EPI_SWIGLU) {
-    f32x4_t h;
+  }
+  return r;
+}
+template <int EPI>
+Q4_DEVICE float row_scale(const DenseArgs& g, int m) {
+  if constexpr (EPI == EPI_INT8) return g.s_row[min(m, g.M - 1)];
+  return 0.f;
+}
+
+// Four values of the result from the sums v (v2: the second B panel's).
+template <Act A, int EPI>
+Q4_DEVICE f32x4_t result4(typename Num<A>::acc_t v, typename Num<A>::acc_t v2, float sm, const ColScales& cs) {
+  f32x4_t y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = swiglu(v[i], v2[i]);
-    store4(g.c[0], g.c_dtype, idx, h, count, vec);
+  for (int i = 0; i < 4; ++i) {
+    // int8: the INT32 sum becomes fp32 (24 bits), then one product of the scales, one with it
+    if constexpr (EPI == EPI_INT8) y[i] = float(v[i]) * (sm * cs.s[i]) + cs.b[i];
+    else if constexpr (EPI == EPI_SWIGLU) y[i] = swiglu(v[i], v2[i]);
+    else y[i] = v[i];
+  }
+  return y;
+}
+
+// Result of four columns n .. n + 3 of row m.
+template <Act A, int EPI>
+Q4_DEVICE void finish4(const DenseArgs& g, int z, int m, int n, typename Num<A>::acc_t v, typename Num<A>::acc_t v2,
+                       float sm, const ColScales& cs) {
+  if (m >= g.M || n >= g.N) return;
+  const int count = min(4, g.N - n);
+  const bool vec = (g.ldc & 3) == 0;
+  store4(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + n, result4<A, EPI>(v, v2, sm, cs), count, vec);
+  if constexpr (EPI == EPI_SWIGLU) {
     if (g.gu) {
       const int64_t at = int64_t(m) * 2 * g.ldc + n;
       store4(g.gu, g.c_dtype, at, v, count, vec);
       store4(g.gu, g.c_dtype, at + g.ldc, v2, count, vec);
     }
+  }
+}
+
+// Stores row values of two adjacent 16-column blocks, columns 4 q .. 4 q + 3 of each in
+// quarter q = lane / 16: 16-bit values are first swapped between neighbouring quarters so
+// that each lane holds 8 consecutive columns, i.e. whole 16-byte stores and 64-byte row
+// segments (8-byte stores ran the 2048 x 2048 x 16384 INT8 product at 103 us).
+Q4_DEVICE void store_pair(void* c, int dtype, int64_t at, int q, f32x4_t y0, f32x4_t y1, bool in) {
+  if (dtype == 0) {
+    if (in) {
+      float* p = static_cast<float*>(c) + at + 4 * q;
+      *reinterpret_cast<f32x4_t*>(p) = y0;
+      *reinterpret_cast<f32x4_t*>(p + 16) = y1;
+    }
   } else {
-    store4(g.c[z], g.c_dtype, idx, v, count, vec);
+    u32x4_t o;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t a = to16(y0[2 * w], dtype) | uint32_t(to16(y0[2 * w + 1], dtype)) << 16;
+      const uint32_t b = to16(y1[2 * w], dtype) | uint32_t(to16(y1[2 * w + 1], dtype)) << 16;
+      // odd quarters of a <-> even quarters of b
+      const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+      o[w] = r[0];
+      o[2 + w] = r[1];
+    }
+    if (in) *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c) + at + 16 * (q & 1) + 8 * (q >> 1)) = o;
+  }
+}
+
+// Results of row m in the adjacent blocks nb and nb + 16 (the wave's 16 rows together: every
+// lane calls).  `whole`: both blocks inside the matrix, rows of whole 16-byte stores.
+template <Act A, int EPI>
+Q4_DEVICE void finish_pair(const DenseArgs& g, int z, int m, int nb, int q, bool whole, typename Num<A>::acc_t v0,
+                           typename Num<A>::acc_t v1, typename Num<A>::acc_t w0, typename Num<A>::acc_t w1, float sm,
+                           const ColScales& cs0, const ColScales& cs1) {
+  if (!whole) {
+    finish4<A, EPI>(g, z, m, nb + 4 * q, v0, w0, sm, cs0);
+    finish4<A, EPI>(g, z, m, nb + 16 + 4 * q, v1, w1, sm, cs1);
+    return;
+  }
+  const bool in = m < g.M;
+  store_pair(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + nb, q, result4<A, EPI>(v0, w0, sm, cs0),
+             result4<A, EPI>(v1, w1, sm, cs1), in);
+  if constexpr (EPI == EPI_SWIGLU) {
+    if (g.gu) {
+      const int64_t at = int64_t(m) * 2 * g.ldc + nb;
+      store_pair(g.gu, g.c_dtype, at, q, v0, v1, in);
+      store_pair(g.gu, g.c_dtype, at + g.ldc, q, w0, w1, in);
+    }
+  }
+}
+
+// Raw sums of a K slice.
+template <typename V>
+Q4_DEVICE void store_part(const DenseArgs& g, int64_t panel, int m, int n, V v) {
+  if (m >= g.M) return;
+  uint32_t* o = static_cast<uint32_t*>(g.part) + (panel * g.M + m) * g.N + n;
+  const u32x4_t w = bitcast<u32x4_t>(v);
+  if (n + 4 <= g.N && (g.N & 3) == 0) {
+    *reinterpret_cast<u32x4_t*>(o) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < g.N) o[e] = w[e];
   }
 }
 
@@ -328,46 +414,49 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
   }
 
   // lane: row m = lane % 16 of its block, columns 4 (lane / 16) .. + 3
+  const int q = lane >> 4;
+  const int nw = n0 + wn * (BP / 2);
+  if (g.ksplit > 1) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          store_part(g, (int64_t(it.ks) * g.batches + it.z) * NP + p, m0 + wm * (BM / 2) + 16 * i + (lane & 15),
+                     nw + 16 * j + 4 * q, acc[p][i][j]);
+    return;
+  }
+  float sm[MB];
+  ColScales cs[NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) sm[i] = row_scale<EPI>(g, m0 + wm * (BM / 2) + 16 * i + (lane & 15));
+#pragma unroll
+  for (int j = 0; j < NB; ++j) cs[j] = col_scales<EPI>(g, nw + 16 * j + 4 * q);
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int m = m0 + wm * (BM / 2) + 16 * i + (lane & 15);
+    if constexpr (NB == 1) {
+      finish4<A, EPI>(g, it.z, m, nw + 4 * q, acc[0][i][0], acc[NP - 1][i][0], sm[i], cs[0]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int n = n0 + wn * (BP / 2) + 16 * j + 4 * (lane >> 4);
-      if (g.ksplit > 1) {
-        if (m < g.M) {
-          const int count = g.N - n < 4 ? g.N - n : 4;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const int64_t at = (((int64_t(it.ks) * g.batches + it.z) * NP + p) * g.M + m) * g.N + n;
-            uint32_t* o = static_cast<uint32_t*>(g.part) + at;
-            const u32x4_t v = bitcast<u32x4_t>(acc[p][i][j]);
-            if (count == 4 && (g.N & 3) == 0) {
-              *reinterpret_cast<u32x4_t*>(o) = v;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (e < count) o[e] = v[e];
-            }
-          }
-        }
-      } else {
-        finish4<A, EPI>(g, it.z, m, n, acc[0][i][j], acc[NP - 1][i][j]);
-      }
+      for (int j = 0; j < NB; j += 2)
+        finish_pair<A, EPI>(g, it.z, m, nw + 16 * j, q, (g.ldc & 7) == 0 && nw + 16 * j + 32 <= g.N, acc[0][i][j],
+                            acc[0][i][j + 1], acc[NP - 1][i][j], acc[NP - 1][i][j + 1], sm[i], cs[j], cs[j + 1]);
     }
   }
 }
 
 // ---------------------------------------------------------------- large tile kernel
 // 256 x 256 per workgroup of 8 waves (2 x 4), two K steps in LDS (128 KB).  A wave owns 64
-// rows of each 128-row half and 32 columns of each 128-column half, so a K step is four
-// quadrant phases of 16 MFMAs, each needing one new half-panel fragment set in registers:
-//     phase         0        1        2        3
-//     LDS reads     A0(k)    B1(k)    A1(k)    B0(k+1)
-//     products      A0 B0    A0 B1    A1 B1    A1 B0
-//     copies        A1(k+1)  B0(k+2)  A0(k+2)  B1(k+2)
-// A half panel is copied six phases before it is read and two phases after its slot's last
-// read, so a wave waits only for its copies of five phases ago (10 stay in flight).
+// rows of each 128-row half and 32 columns of each 128-column half; a K step is two phases
+// of 32 MFMAs:
+//     phase         0                  1
+//     LDS reads     A0(k) B0(k) B1(k)  A1(k)
+//     products      A0 x B0 B1         A1 x B0 B1
+//     copies        A1(k+1)            A0(k+2) B0(k+2) B1(k+2)
+// A half panel is copied three phases before it is read, into a slot whose last read ended
+// the phase before; a wave waits only for its copies of two phases ago (8 stay in flight).
 // Waves 4..7 (the other wave of each SIMD) run half a phase behind waves 0..3: while one
 // wave of a SIMD reads LDS and issues copies, the other feeds the matrix core.
 template <Act A, bool AMC, bool BMC, int EPI>
@@ -386,7 +475,9 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
   const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
   const int m0 = it.mt * 256, n0 = it.nt * (DUAL ? 128 : 256);
   const int seg_steps = (g.K + T::STEP - 1) / T::STEP;
-  const int steps = seg_steps * g.segs;
+  const int all = seg_steps * g.segs;
+  const int per = (all + g.ksplit - 1) / g.ksplit;
+  const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
   const uint32_t lds0 = lds_addr(ring);
 
   // Copies half panel `h` (0, 1: A; 2, 3: B) of step s: two 1 KB copies per wave.  Past the
@@ -416,7 +507,7 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
     const bool second = s >= seg_steps;
     const int ss = second ? s - seg_steps : s;
     f.base += second ? (IS_A ? da : db) : 0;
-    const u32x4_t rs = P::rsrc(f, ss, in[h] && s < steps);
+    const u32x4_t rs = P::rsrc(f, ss, in[h] && s < s_end);
     const int left = MC ? (IS_A ? g.M - m0 : g.N - n0) - half * 128 : g.K * T::ESZ - ss * kStepBytes;
     const uint32_t at = lds0 + uint32_t(s & 1) * (4 * HB) + h * HB + wid * 2048;
     const int64_t ld = IS_A ? g.lda : g.ldb;
@@ -437,7 +528,7 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[a][b][i][j] = acc_t{0, 0, 0, 0};
-  u32x4_t fa[4][2], fb[2][2][2];   // fb[register set][block][sub]
+  u32x4_t fa[4][2], fb[2][2][2];   // [half of B]
 
   auto read_a = [&](int s, int half) {
     const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + half * HB;
@@ -446,89 +537,106 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
 #pragma unroll
       for (int i = 0; i < 4; ++i) fa[i][sub] = PA::frag(p, lba, wm * 64 + 16 * i, sub);
   };
-  auto read_b = [&](int s, int half, auto set_c) {
-    constexpr int set = decltype(set_c)::value;
+  auto read_b = [&](int s, int half) {
     const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + (2 + half) * HB;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fb[set][j][sub] = PB::frag(p, lbb, wn * 32 + 16 * j, sub);
+      for (int j = 0; j < 2; ++j) fb[half][j][sub] = PB::frag(p, lbb, wn * 32 + 16 * j, sub);
   };
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-  auto phase_end = [&] {   // end of a load section
+  auto load_end = [&] {   // own fragments in registers, own copies of two phases ago in LDS
     fence();
-    asm volatile("s_waitcnt vmcnt(10)\n\ts_barrier\n\ts_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     fence();
     __builtin_amdgcn_s_setprio(1);
   };
-  auto multiply = [&](auto ha, auto hb, auto set_c) {
-    constexpr int a = decltype(ha)::value, b = decltype(hb)::value, set = decltype(set_c)::value;
+  auto multiply = [&](auto ha) {
+    constexpr int a = decltype(ha)::value;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = T::mfma(fb[set][j][sub], fa[i][sub], acc[a][b][i][j]);
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[a][b][i][j] = T::mfma(fb[b][j][sub], fa[i][sub], acc[a][b][i][j]);
     __builtin_amdgcn_s_setprio(0);
     fence();
     asm volatile("s_barrier" ::: "memory");
     fence();
   };
-  typedef std::integral_constant<int, 0> Z;
-  typedef std::integral_constant<int, 1> O;
-  // one K step; `lo` / `hi`: register sets of B0(k) and B1(k)
-  auto step = [&](int s, auto lo, auto hi) {
+
+  issue(A0{}, s_begin);
+  issue(B0{}, s_begin);
+  issue(B1{}, s_begin);
+  issue(A1{}, s_begin);
+  issue(A0{}, s_begin + 1);
+  issue(B0{}, s_begin + 1);
+  issue(B1{}, s_begin + 1);
+  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+  if (wid >= 4) asm volatile("s_barrier" ::: "memory");
+  for (int s = s_begin; s < s_end; ++s) {
     read_a(s, 0);
+    read_b(s, 0);
+    read_b(s, 1);
     issue(A1{}, s + 1);
-    phase_end();
-    multiply(Z{}, Z{}, lo);
-    read_b(s, 1, hi);
-    issue(B0{}, s + 2);
-    phase_end();
-    multiply(Z{}, O{}, hi);
+    load_end();
+    multiply(std::integral_constant<int, 0>{});
     read_a(s, 1);
     issue(A0{}, s + 2);
-    phase_end();
-    multiply(O{}, O{}, hi);
-    read_b(s + 1, 0, hi);
+    issue(B0{}, s + 2);
     issue(B1{}, s + 2);
-    phase_end();
-    multiply(O{}, Z{}, lo);
-  };
-
-  issue(B0{}, 0);
-  issue(A0{}, 0);
-  issue(B1{}, 0);
-  issue(A1{}, 0);
-  issue(B0{}, 1);
-  issue(A0{}, 1);
-  issue(B1{}, 1);
-  asm volatile("s_waitcnt vmcnt(10)\n\ts_barrier" ::: "memory");
-  read_b(0, 0, Z{});
-  if (wid >= 4) asm volatile("s_barrier" ::: "memory");
-  for (int s = 0; s < steps; s += 2) {   // (an odd last step is followed by one of zeros)
-    step(s, Z{}, O{});
-    step(s + 1, O{}, Z{});
+    load_end();
+    multiply(std::integral_constant<int, 1>{});
   }
   if (wid < 4) asm volatile("s_barrier" ::: "memory");
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
 
+  const int q = lane >> 4;
+  const int nw = n0 + wn * 32;
+  if (g.ksplit > 1) {
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t zs = int64_t(it.ks) * g.batches + it.z;
+            store_part(g, DUAL ? 2 * zs + b : zs, m0 + a * 128 + wm * 64 + 16 * i + (lane & 15),
+                       nw + (DUAL ? 0 : b * 128) + 16 * j + 4 * q, acc[a][b][i][j]);
+          }
+    return;
+  }
+  ColScales cs[2][2];
+  bool whole[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    whole[b] = (g.ldc & 7) == 0 && nw + b * 128 + 32 <= g.N;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) cs[b][j] = col_scales<EPI>(g, nw + b * 128 + 16 * j + 4 * q);
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    float sm[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm[i] = row_scale<EPI>(g, m0 + a * 128 + wm * 64 + 16 * i + (lane & 15));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + a * 128 + wm * 64 + 16 * i + (lane & 15);
+      if constexpr (DUAL) {
+        finish_pair<A, EPI>(g, it.z, m, nw, q, whole[0], acc[a][0][i][0], acc[a][0][i][1], acc[a][1][i][0],
+                            acc[a][1][i][1], sm[i], cs[0][0], cs[0][1]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + wn * 32 + 16 * j + 4 * (lane >> 4);
-        if constexpr (DUAL) {
-          finish4<A, EPI>(g, it.z, m, n, acc[a][0][i][j], acc[a][1][i][j]);
-        } else {
-          finish4<A, EPI>(g, it.z, m, n, acc[a][0][i][j], acc[a][0][i][j]);
-          finish4<A, EPI>(g, it.z, m, n + 128, acc[a][1][i][j], acc[a][1][i][j]);
-        }
+        for (int b = 0; b < 2; ++b)
+          finish_pair<A, EPI>(g, it.z, m, nw + b * 128, q, whole[b], acc[a][b][i][0], acc[a][b][i][1], acc[a][b][i][0],
+                              acc[a][b][i][1], sm[i], cs[b][0], cs[b][1]);
       }
     }
+  }
 }
 
 // Adds the K slices of a split product in slice order and finishes four columns per thread.
@@ -560,7 +668,7 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
       }
     }
   }
-  finish4<A, EPI>(g, z, m, n, v[0], v[NP - 1]);
+  finish4<A, EPI>(g, z, m, n, v[0], v[NP - 1], row_scale<EPI>(g, m), col_scales<EPI>(g, n));
 }
 
 // ---------------------------------------------------------------- few rows
@@ -649,7 +757,8 @@ __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
 #pragma unroll
       for (int w = 1; w < W; ++w) v[p] += sums[w][p * MB + i][lane];
     }
-    finish4<A, EPI>(g, 0, 16 * i + (lane & 15), n0 + 4 * (lane >> 4), v[0], v[NP - 1]);
+    const int m = 16 * i + (lane & 15), n = n0 + 4 * (lane >> 4);
+    finish4<A, EPI>(g, 0, m, n, v[0], v[NP - 1], row_scale<EPI>(g, m), col_scales<EPI>(g, n));
   }
 }
 
@@ -719,10 +828,17 @@ struct Plan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile and K split of a product of `steps` K steps over `panels` B panels: the largest
-// tile that gives every CU work, else the smallest one with K split until the launch has
-// about 512 workgroups of at least 4 steps each.
+// tile that gives (nearly) every CU work, if need be with K split in up to four slices of at
+// least 16 steps; else the smallest one with K split until the launch has about 512
+// workgroups of at least 4 steps each.
 Plan plan_of(int64_t m, int64_t n, int panels, int64_t steps, int batches) {
-  if (ceil_div(m, 256) * ceil_div(n * panels, 256) * batches >= 192) return {256, 256, 1};
+  const int64_t big = ceil_div(m, 256) * ceil_div(n * panels, 256) * batches;
+  if (big >= 192) return {256, 256, 1};
+  if (big >= 64) {
+    const int64_t want = ceil_div(192, big);
+    const int64_t per = ceil_div(steps, want);
+    if (per >= 16) return {256, 256, int(ceil_div(steps, per))};
+  }
   if (ceil_div(m, 128) * ceil_div(n * panels, 128) * batches >= 256) return {128, 128, 1};
   const int64_t tiles = ceil_div(m, 64) * ceil_div(n * panels, 64) * batches;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 4));
