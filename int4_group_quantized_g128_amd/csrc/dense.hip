@@ -210,17 +210,17 @@ Q4_DEVICE void store_part(const DenseArgs& g, int64_t panel, int m, int n, V v) 
 }
 
 // ---------------------------------------------------------------- panels in LDS
-// R rows of one operand, one K step: 128 R bytes, R / 8 copies of 1 KB.
-template <Act A, bool MC, int R>
+// R rows of one operand, one K step of SB bytes: SB R bytes in copies of 1 KB.
+template <Act A, bool MC, int R, int SB>
 struct Panel {
   static_assert(!MC || A != Act::I8, "transposing reads are for 16-bit values");
-  static constexpr int BYTES = R * kStepBytes;
-  static constexpr int COPIES = R / 8;
+  static constexpr int BYTES = R * SB;
+  static constexpr int COPIES = BYTES / 1024;
   static constexpr int ESZ = Num<A>::ESZ;
-  static constexpr int CPR = MC ? R / 8 : 8;   // 16-byte chunks per LDS row
+  static constexpr int CPR = MC ? R / 8 : SB / 16;   // 16-byte chunks per LDS row
 
   static Q4_DEVICE int swz(int r) {
-    if constexpr (!MC) return (r >> 1) & 7;
+    if constexpr (!MC) return SB == 128 ? (r >> 1) & 7 : -(r >> 2) & 3;
     else if constexpr (R >= 128) return (r & 3) | ((r >> 3) & 1) << 2;
     else return ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
   }
@@ -242,8 +242,8 @@ struct Panel {
     return in ? uint32_t(r * ld * ESZ + c * 16) : kNoByte;
   }
 
-  // Where the panel's K steps lie: the step at K element k0 starts k0 / STEP * inc bytes
-  // after base, and `left` bytes from there belong to the operand.
+  // Where the panel's K steps lie: step s starts s * inc bytes after base; `left` bytes from
+  // base on belong to the operand.
   struct Source {
     uint64_t base, left;
     uint32_t inc;
@@ -251,7 +251,7 @@ struct Panel {
   static Q4_DEVICE Source source(const void* p, int64_t ld, int rows, int K, int row0) {
     const uint64_t at = uint64_t(MC ? int64_t(row0) : int64_t(row0) * ld) * ESZ;
     return Source{reinterpret_cast<uint64_t>(p) + at, uint64_t(MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at,
-                  MC ? uint32_t(ld) * uint32_t(Num<A>::STEP * ESZ) : uint32_t(kStepBytes)};
+                  MC ? uint32_t(ld) * SB : uint32_t(SB)};
   }
   // Descriptor of step `s` (a step of the panel: left > s * inc), empty if !valid.
   static Q4_DEVICE u32x4_t rsrc(const Source& f, int s, bool valid) {
@@ -267,7 +267,7 @@ struct Panel {
   static Q4_DEVICE uint32_t lane_base(int lane) {
     if constexpr (!MC) {
       const int r = lane & 15;
-      return r * kStepBytes + (((lane >> 4) ^ swz(r)) << 4);
+      return r * SB + (((lane >> 4) ^ swz(r)) << 4);
     } else {
       const int k = 8 * (lane >> 4) + ((lane & 15) >> 2);
       return k * (2 * R) + (swz(k) << 5) + ((lane & 3) << 3);
@@ -279,7 +279,7 @@ struct Panel {
   static Q4_DEVICE u32x4_t frag(uint32_t lds, uint32_t lb, int r0, int sub) {
     if constexpr (!MC) {
       typedef __attribute__((address_space(3))) const u32x4_t* lptr;
-      return *(lptr)(uintptr_t)(lds + r0 * kStepBytes + (lb ^ (sub << 6)));
+      return *(lptr)(uintptr_t)(lds + r0 * SB + (lb ^ (sub << 6)));
     } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* lptr;
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
   typedef typename T::acc_t acc_t;
   constexpr bool DUAL = EPI == EPI_SWIGLU;
   constexpr int BP = DUAL ? BN / 2 : BN;            // rows of a B panel
-  typedef Panel<A, AMC, BM> PA;
-  typedef Panel<A, BMC, BP> PB;
+  typedef Panel<A, AMC, BM, kStepBytes> PA;
+  typedef Panel<A, BMC, BP, kStepBytes> PB;
   constexpr int NP = DUAL ? 2 : 1;
   constexpr int STAGE = PA::BYTES + NP * PB::BYTES;
   constexpr int NS = 3;
@@ -448,193 +448,131 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
 }
 
 // ---------------------------------------------------------------- large tile kernel
-// 256 x 256 per workgroup of 8 waves (2 x 4), two K steps in LDS (128 KB).  A wave owns 64
-// rows of each 128-row half and 32 columns of each 128-column half; a K step is two phases
-// of 32 MFMAs:
-//     phase         0                  1
-//     LDS reads     A0(k) B0(k) B1(k)  A1(k)
-//     products      A0 x B0 B1         A1 x B0 B1
-//     copies        A1(k+1)            A0(k+2) B0(k+2) B1(k+2)
-// A half panel is copied three phases before it is read, into a slot whose last read ended
-// the phase before; a wave waits only for its copies of two phases ago (8 stay in flight).
-// Waves 4..7 (the other wave of each SIMD) run half a phase behind waves 0..3: while one
-// wave of a SIMD reads LDS and issues copies, the other feeds the matrix core.
+// 256 x 256 per workgroup of 8 waves (2 x 4, 128 x 64 each), K steps of 64 bytes in a ring of
+// four (128 KB).  A step is 32 MFMAs per wave and needs 12 fragments: step s + 3 is copied
+// while step s is read, into the slot whose last read ended the step before; a wave waits
+// only for its copies of two steps ago (8 of 1 KB stay in flight).
+// Waves 4..7 (the other wave of each SIMD) run half a step behind waves 0..3: while one wave
+// of a SIMD reads LDS and issues copies, the other feeds the matrix core.
 template <Act A, bool AMC, bool BMC, int EPI>
 __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, int ntiles) {
   typedef Num<A> T;
   typedef typename T::acc_t acc_t;
   constexpr bool DUAL = EPI == EPI_SWIGLU;
-  typedef Panel<A, AMC, 128> PA;
-  typedef Panel<A, BMC, 128> PB;
-  constexpr int HB = PA::BYTES;                     // 16 KB per half panel
-  __shared__ __align__(16) uint8_t ring[2 * 4 * HB];   // [step % 2][A0, A1, B0, B1]
+  constexpr int SB = 64;
+  constexpr int STEP = SB / T::ESZ;
+  constexpr int BP = DUAL ? 128 : 256;              // rows of a B panel
+  typedef Panel<A, AMC, 256, SB> PA;
+  typedef Panel<A, BMC, BP, SB> PB;
+  constexpr int SLOT = 2 * PA::BYTES;               // 16 KB of A, 16 KB of B
+  constexpr int MB = 8, NB = 4;                     // 16-blocks per wave
+  __shared__ __align__(16) uint8_t ring[4 * SLOT];
 
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int wm = wid >> 2, wn = wid & 3;
   const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
-  const int m0 = it.mt * 256, n0 = it.nt * (DUAL ? 128 : 256);
-  const int seg_steps = (g.K + T::STEP - 1) / T::STEP;
+  const int m0 = it.mt * 256, n0 = it.nt * BP;
+  const int seg_steps = (g.K + STEP - 1) / STEP;
   const int all = seg_steps * g.segs;
   const int per = (all + g.ksplit - 1) / g.ksplit;
   const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
   const uint32_t lds0 = lds_addr(ring);
 
-  // Copies half panel `h` (0, 1: A; 2, 3: B) of step s: two 1 KB copies per wave.  Past the
-  // last step (or the last row) the descriptor is empty: the copy counts, and writes zeros.
-  typename PA::Source fsa[2];
-  typename PB::Source fsb[2];
-  bool in[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int rb = n0 + (DUAL ? 0 : h * 128);
-    fsa[h] = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0 + h * 128);
-    fsb[h] = PB::source(DUAL && h ? g.b[1] : g.b[0], g.ldb, g.N, g.K, rb);
-    in[h] = m0 + h * 128 < g.M;
-    in[2 + h] = rb < g.N;
-  }
+  // Each wave copies 2 KB of each operand per step (swiglu: waves 0..3 of the gate panel,
+  // 4..7 of the up panel).  Past the last step the descriptor is empty: the copy counts, and
+  // writes zeros that nothing reads.
+  const auto fa = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0);
+  const auto fb = PB::source(DUAL && wm ? g.b[1] : g.b[0], g.ldb, g.N, g.K, n0);
   const uint64_t da = reinterpret_cast<uint64_t>(g.a[1]) - reinterpret_cast<uint64_t>(g.a[0]);
   const uint64_t db = reinterpret_cast<uint64_t>(g.b[1]) - reinterpret_cast<uint64_t>(g.b[0]);
-  auto issue = [&](auto h_c, int s) {
-    constexpr int h = decltype(h_c)::value;
-    constexpr bool IS_A = h < 2;
-    constexpr int half = h & 1;
-    typedef typename std::conditional<IS_A, PA, PB>::type P;
-    constexpr bool MC = IS_A ? AMC : BMC;
-    typename P::Source f;
-    if constexpr (IS_A) f = fsa[half];
-    else f = fsb[half];
+  const int cb = DUAL ? 2 * wn : 2 * wid;           // first copy of the wave in its B panel
+  auto issue = [&](int s) {
     const bool second = s >= seg_steps;
     const int ss = second ? s - seg_steps : s;
-    f.base += second ? (IS_A ? da : db) : 0;
-    const u32x4_t rs = P::rsrc(f, ss, in[h] && s < s_end);
-    const int left = MC ? (IS_A ? g.M - m0 : g.N - n0) - half * 128 : g.K * T::ESZ - ss * kStepBytes;
-    const uint32_t at = lds0 + uint32_t(s & 1) * (4 * HB) + h * HB + wid * 2048;
-    const int64_t ld = IS_A ? g.lda : g.ldb;
-    copy2_to_lds(rs, at, P::offset(2 * wid, lane, ld, left), P::offset(2 * wid + 1, lane, ld, left));
+    const uint32_t at = lds0 + uint32_t(s & 3) * SLOT + wid * 2048;
+    const int left = g.K * T::ESZ - ss * SB;
+    auto sa = fa;
+    auto sb = fb;
+    if (g.segs > 1 && second) sa.base += da, sb.base += db;
+    const int la = AMC ? g.M - m0 : left, lb = BMC ? g.N - n0 : left;
+    copy2_to_lds(PA::rsrc(sa, ss, s < s_end), at, PA::offset(2 * wid, lane, g.lda, la),
+                 PA::offset(2 * wid + 1, lane, g.lda, la));
+    copy2_to_lds(PB::rsrc(sb, ss, s < s_end), at + PA::BYTES, PB::offset(cb, lane, g.ldb, lb),
+                 PB::offset(cb + 1, lane, g.ldb, lb));
   };
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
-  typedef std::integral_constant<int, 0> A0;
-  typedef std::integral_constant<int, 1> A1;
-  typedef std::integral_constant<int, 2> B0;
-  typedef std::integral_constant<int, 3> B1;
 
-  acc_t acc[2][2][4][2];
+  acc_t acc[MB][NB];
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = acc_t{0, 0, 0, 0};
-  u32x4_t fa[4][2], fb[2][2][2];   // [half of B]
-
-  auto read_a = [&](int s, int half) {
-    const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + half * HB;
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i][sub] = PA::frag(p, lba, wm * 64 + 16 * i, sub);
-  };
-  auto read_b = [&](int s, int half) {
-    const uint32_t p = lds0 + uint32_t(s & 1) * (4 * HB) + (2 + half) * HB;
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) fb[half][j][sub] = PB::frag(p, lbb, wn * 32 + 16 * j, sub);
-  };
+    for (int j = 0; j < NB; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-  auto load_end = [&] {   // own fragments in registers, own copies of two phases ago in LDS
+
+  issue(s_begin);
+  issue(s_begin + 1);
+  issue(s_begin + 2);
+  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+  if (wid >= 4) asm volatile("s_barrier" ::: "memory");
+  for (int s = s_begin; s < s_end; ++s) {
+    const uint32_t p = lds0 + uint32_t(s & 3) * SLOT;
+    u32x4_t va[MB], vb[NB];
+    // swiglu: blocks 0, 1 of the wave in the gate panel, 2, 3 in the up panel
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      vb[j] = DUAL ? PB::frag(p + PA::BYTES + (j / 2) * PB::BYTES, lbb, wn * 32 + 16 * (j % 2), 0)
+                   : PB::frag(p + PA::BYTES, lbb, wn * 64 + 16 * j, 0);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) va[i] = PA::frag(p, lba, wm * 128 + 16 * i, 0);
+    issue(s + 3);
+    // fragments in registers, copies of step s + 1 in LDS
     fence();
     asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     fence();
     __builtin_amdgcn_s_setprio(1);
-  };
-  auto multiply = [&](auto ha) {
-    constexpr int a = decltype(ha)::value;
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[a][b][i][j] = T::mfma(fb[b][j][sub], fa[i][sub], acc[a][b][i][j]);
+      for (int j = 0; j < NB; ++j) acc[i][j] = T::mfma(vb[j], va[i], acc[i][j]);
     __builtin_amdgcn_s_setprio(0);
     fence();
     asm volatile("s_barrier" ::: "memory");
     fence();
-  };
-
-  issue(A0{}, s_begin);
-  issue(B0{}, s_begin);
-  issue(B1{}, s_begin);
-  issue(A1{}, s_begin);
-  issue(A0{}, s_begin + 1);
-  issue(B0{}, s_begin + 1);
-  issue(B1{}, s_begin + 1);
-  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-  if (wid >= 4) asm volatile("s_barrier" ::: "memory");
-  for (int s = s_begin; s < s_end; ++s) {
-    read_a(s, 0);
-    read_b(s, 0);
-    read_b(s, 1);
-    issue(A1{}, s + 1);
-    load_end();
-    multiply(std::integral_constant<int, 0>{});
-    read_a(s, 1);
-    issue(A0{}, s + 2);
-    issue(B0{}, s + 2);
-    issue(B1{}, s + 2);
-    load_end();
-    multiply(std::integral_constant<int, 1>{});
   }
   if (wid < 4) asm volatile("s_barrier" ::: "memory");
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
 
   const int q = lane >> 4;
-  const int nw = n0 + wn * 32;
+  const int mw = m0 + wm * 128 + (lane & 15);
+  const int nw = n0 + wn * (DUAL ? 32 : 64);
   if (g.ksplit > 1) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t zs = int64_t(it.ks) * g.batches + it.z;
-            store_part(g, DUAL ? 2 * zs + b : zs, m0 + a * 128 + wm * 64 + 16 * i + (lane & 15),
-                       nw + (DUAL ? 0 : b * 128) + 16 * j + 4 * q, acc[a][b][i][j]);
-          }
+      for (int j = 0; j < NB; ++j) {
+        const int64_t zs = int64_t(it.ks) * g.batches + it.z;
+        if constexpr (DUAL) store_part(g, 2 * zs + j / 2, mw + 16 * i, nw + 16 * (j % 2) + 4 * q, acc[i][j]);
+        else store_part(g, zs, mw + 16 * i, nw + 16 * j + 4 * q, acc[i][j]);
+      }
     return;
   }
-  ColScales cs[2][2];
-  bool whole[2];
+  ColScales cs[NB];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    whole[b] = (g.ldc & 7) == 0 && nw + b * 128 + 32 <= g.N;
+  for (int j = 0; j < NB; ++j) cs[j] = col_scales<EPI>(g, nw + 16 * j + 4 * q);
+  float sm[MB];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) cs[b][j] = col_scales<EPI>(g, nw + b * 128 + 16 * j + 4 * q);
-  }
+  for (int i = 0; i < MB; ++i) sm[i] = row_scale<EPI>(g, mw + 16 * i);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    float sm[4];
+  for (int i = 0; i < MB; ++i) {
+    if constexpr (DUAL) {
+      finish_pair<A, EPI>(g, it.z, mw + 16 * i, nw, q, (g.ldc & 7) == 0 && nw + 32 <= g.N, acc[i][0], acc[i][1],
+                          acc[i][2], acc[i][3], sm[i], cs[0], cs[1]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sm[i] = row_scale<EPI>(g, m0 + a * 128 + wm * 64 + 16 * i + (lane & 15));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + a * 128 + wm * 64 + 16 * i + (lane & 15);
-      if constexpr (DUAL) {
-        finish_pair<A, EPI>(g, it.z, m, nw, q, whole[0], acc[a][0][i][0], acc[a][0][i][1], acc[a][1][i][0],
-                            acc[a][1][i][1], sm[i], cs[0][0], cs[0][1]);
-      } else {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          finish_pair<A, EPI>(g, it.z, m, nw + b * 128, q, whole[b], acc[a][b][i][0], acc[a][b][i][1], acc[a][b][i][0],
-                              acc[a][b][i][1], sm[i], cs[b][0], cs[b][1]);
-      }
+      for (int j = 0; j < NB; j += 2)
+        finish_pair<A, EPI>(g, it.z, mw + 16 * i, nw + 16 * j, q, (g.ldc & 7) == 0 && nw + 16 * j + 32 <= g.N,
+                            acc[i][j], acc[i][j + 1], acc[i][j], acc[i][j + 1], sm[i], cs[j], cs[j + 1]);
     }
   }
 }
