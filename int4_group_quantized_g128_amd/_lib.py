@@ -737,29 +737,32 @@ def int4_w4a8_group_acc(q, w_dev, n, asymmetric=False):
 
 
 # ------------------------------------------------------------------ dense operators
+# These run at a few microseconds per call for one token, so their checks take one pass per
+# tensor and the stream comes as a raw handle.
 _16BIT = (torch.float16, torch.bfloat16)
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _like(t, ref, shape, name, dtype=None):
-    """t as a contiguous tensor of the given shape on ref's GPU, of ref's dtype (or dtype)."""
-    _need(t, dtype or ref.dtype, name)
+def _arg(t, name, dtype, shape, dev):
+    """t must be a contiguous tensor of this dtype and shape on GPU `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return
+    _need(t, dtype, name, len(shape))
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _call(name, ref, *args):
-    """The C entry point on the current stream of ref's GPU."""
-    f = getattr(_lib, name)
-    if ref.device.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+def _call(name, f, dev, *args):
+    """The C entry point f on the current stream of GPU `dev`."""
+    if dev == _current_device():
+        rc = f(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(ref.device):
-            rc = f(*args, torch.cuda.current_stream().cuda_stream)
-    if rc != Q4_OK:
+        with torch.cuda.device(dev):
+            rc = f(*args, _raw_stream(dev))
+    if rc:
         raise Q4Error(name, rc)
 
 
@@ -767,19 +770,21 @@ def _dp(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(nbytes, ref):
-    return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if nbytes else None
+def _scratch(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def quantize_int8_channel(w, flags=None):
     """INT8 weights with one scale per output channel of w [n, k] -> (q int8 [n, k], s fp32 [n])."""
     _need(w, _FLOATS, "w", 2)
     n, k = w.shape
+    dev = w.get_device()
     if flags is not None:
-        _like(flags, w, (1,), "flags", torch.int32)
+        _arg(flags, "flags", torch.int32, (1,), dev)
     q = torch.empty((n, k), dtype=torch.int8, device=w.device)
     s = torch.empty(n, dtype=torch.float32, device=w.device)
-    _call("quantize_int8_channel", w, w.data_ptr(), _DT[w.dtype], n, k, q.data_ptr(), s.data_ptr(), _dp(flags))
+    _call("quantize_int8_channel", _lib.quantize_int8_channel, dev, w.data_ptr(), _DT[w.dtype], n, k, q.data_ptr(),
+          s.data_ptr(), _dp(flags))
     return q, s
 
 
@@ -790,18 +795,20 @@ def int8_linear_forward(q, s, w_q, w_s, bias=None, out_dtype=torch.bfloat16):
     _need(w_q, torch.int8, "w_q", 2)
     t, k = q.shape
     n = w_q.shape[0]
-    _like(w_q, q, (n, k), "w_q")
-    _like(s, q, (t,), "s", torch.float32)
-    _like(w_s, q, (n,), "w_s", torch.float32)
+    dev = q.get_device()
+    _arg(w_q, "w_q", torch.int8, (n, k), dev)
+    _arg(s, "s", torch.float32, (t,), dev)
+    _arg(w_s, "w_s", torch.float32, (n,), dev)
     if bias is not None:
-        _like(bias, q, (n,), "bias", torch.float32)
+        _arg(bias, "bias", torch.float32, (n,), dev)
     if out_dtype not in _DT:
         raise TypeError(f"out_dtype {out_dtype} is not fp32, fp16 or bf16")
-    y = torch.empty((t, n), dtype=out_dtype, device=q.device)
+    device = q.device
+    y = torch.empty((t, n), dtype=out_dtype, device=device)
     nbytes = _lib.int8_linear_workspace_bytes(t, k, n)
-    ws = _scratch(nbytes, q)
-    _call("int8_linear_forward", q, q.data_ptr(), s.data_ptr(), t, k, w_q.data_ptr(), w_s.data_ptr(), n, _dp(bias),
-          _DT[out_dtype], y.data_ptr(), _dp(ws), nbytes)
+    ws = _scratch(nbytes, device)
+    _call("int8_linear_forward", _lib.int8_linear_forward, dev, q.data_ptr(), s.data_ptr(), t, k, w_q.data_ptr(),
+          w_s.data_ptr(), n, _dp(bias), _DT[out_dtype], y.data_ptr(), _dp(ws), nbytes)
     return y
 
 
@@ -810,57 +817,62 @@ def _swiglu_args(x, w_gate, w_up):
     _need(w_gate, x.dtype, "w_gate", 2)
     t, h = x.shape
     i = w_gate.shape[0]
-    _like(w_gate, x, (i, h), "w_gate")
-    _like(w_up, x, (i, h), "w_up")
-    return t, h, i
+    dev = x.get_device()
+    _arg(w_gate, "w_gate", x.dtype, (i, h), dev)
+    _arg(w_up, "w_up", x.dtype, (i, h), dev)
+    return t, h, i, dev
 
 
 def swiglu_linear_forward(x, w_gate, w_up, save=False):
     """h [t, i] = silu(x w_gate^T) * (x w_up^T) for x [t, h] and weights [i, h] (fp16 or bf16).
     With ``save`` -> (h, gu): gu [t, 2, i] holds the two products for the backward pass."""
-    t, h, i = _swiglu_args(x, w_gate, w_up)
-    out = torch.empty((t, i), dtype=x.dtype, device=x.device)
-    gu = torch.empty((t, 2, i), dtype=x.dtype, device=x.device) if save else None
+    t, h, i, dev = _swiglu_args(x, w_gate, w_up)
+    dtype, device = x.dtype, x.device
+    out = torch.empty((t, i), dtype=dtype, device=device)
+    gu = torch.empty((t, 2, i), dtype=dtype, device=device) if save else None
     nbytes = _lib.swiglu_linear_workspace_bytes(t, h, i)
-    ws = _scratch(nbytes, x)
-    _call("swiglu_linear_forward", x, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), t, h, i, _DT[x.dtype],
-          out.data_ptr(), _dp(gu), _dp(ws), nbytes)
+    ws = _scratch(nbytes, device)
+    _call("swiglu_linear_forward", _lib.swiglu_linear_forward, dev, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+          t, h, i, _DT[dtype], out.data_ptr(), _dp(gu), _dp(ws), nbytes)
     return (out, gu) if save else out
 
 
 def swiglu_linear_backward(dh, x, w_gate, w_up, gu):
     """Gradients (dx, dw_gate, dw_up) of swiglu_linear_forward for dh [t, i] and the saved gu."""
-    t, h, i = _swiglu_args(x, w_gate, w_up)
-    _like(dh, x, (t, i), "dh")
-    _like(gu, x, (t, 2, i), "gu")
+    t, h, i, dev = _swiglu_args(x, w_gate, w_up)
+    _arg(dh, "dh", x.dtype, (t, i), dev)
+    _arg(gu, "gu", x.dtype, (t, 2, i), dev)
     dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
     nbytes = _lib.swiglu_linear_backward_workspace_bytes(t, h, i)
-    ws = _scratch(nbytes, x)
-    _call("swiglu_linear_backward", x, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gu.data_ptr(),
-          t, h, i, _DT[x.dtype], dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), _dp(ws), nbytes)
+    ws = _scratch(nbytes, x.device)
+    _call("swiglu_linear_backward", _lib.swiglu_linear_backward, dev, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
+          w_up.data_ptr(), gu.data_ptr(), t, h, i, _DT[x.dtype], dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
+          _dp(ws), nbytes)
     return dx, dwg, dwu
 
 
 def _norm_desc(res, y, w_post, gate, alpha, w_pre, eps):
     _need(res, _FLOATS, "res", 2)
-    rows, cols = res.shape
+    dtype, shape, dev = res.dtype, res.shape, res.get_device()
+    rows, cols = shape
     if y is None and w_pre is None:
         raise ValueError("y or w_pre is required")
     if y is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need y")
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            _like(t, res, (cols,), name)
+    if w_post is not None:
+        _arg(w_post, "w_post", dtype, (cols,), dev)
+    if w_pre is not None:
+        _arg(w_pre, "w_pre", dtype, (cols,), dev)
     if y is not None:
-        _like(y, res, (rows, cols), "y")
+        _arg(y, "y", dtype, shape, dev)
     kind = Q4_GATE_NONE
     if gate is not None:
-        shape = tuple(gate.shape)
-        kind = {(rows, cols): Q4_GATE_ELEMENT, (rows, 1): Q4_GATE_TOKEN, (cols,): Q4_GATE_CHANNEL}.get(shape)
+        g = tuple(gate.shape)
+        kind = {(rows, cols): Q4_GATE_ELEMENT, (rows, 1): Q4_GATE_TOKEN, (cols,): Q4_GATE_CHANNEL}.get(g)
         if kind is None:
-            raise ValueError(f"gate must be {(cols,)}, {(rows, 1)} or {(rows, cols)}, got {shape}")
-        _like(gate, res, shape, "gate")
-    return Q4BlockNorm(rows, cols, _DT[res.dtype], kind, alpha, eps, res.data_ptr(), _dp(y), _dp(w_post), _dp(gate),
+            raise ValueError(f"gate must be {(cols,)}, {(rows, 1)} or {(rows, cols)}, got {g}")
+        _arg(gate, "gate", dtype, g, dev)
+    return Q4BlockNorm(rows, cols, _DT[dtype], kind, alpha, eps, res.data_ptr(), _dp(y), _dp(w_post), _dp(gate),
                        _dp(w_pre))
 
 
@@ -872,12 +884,14 @@ def block_norm_forward(res, y=None, w_post=None, gate=None, alpha=1.0, w_pre=Non
     d = _norm_desc(res, y, w_post, gate, alpha, w_pre, eps)
     r = res if y is None else torch.empty_like(res)
     n = q = s = None
-    if w_pre is not None and quantize:
-        q = torch.empty(res.shape, dtype=torch.int8, device=res.device)
-        s = torch.empty(res.shape[0], dtype=torch.float32, device=res.device)
-    elif w_pre is not None:
-        n = torch.empty_like(res)
-    _call("block_norm_forward", res, ctypes.byref(d), None if y is None else r.data_ptr(), _dp(n), _dp(q), _dp(s))
+    if w_pre is not None:
+        if quantize:
+            q = torch.empty_like(res, dtype=torch.int8)
+            s = torch.empty(d.rows, dtype=torch.float32, device=res.device)
+        else:
+            n = torch.empty_like(res)
+    _call("block_norm_forward", _lib.block_norm_forward, res.get_device(), d, None if y is None else r.data_ptr(),
+          _dp(n), _dp(q), _dp(s))
     return (r, q, s) if quantize else (r, n)
 
 
@@ -886,20 +900,21 @@ def block_norm_backward(dr, dn, res, y=None, w_post=None, gate=None, alpha=1.0, 
     "res", "y", "w_post", "gate", "w_pre" (None where the input is absent); weight, channel
     and token gate gradients are fp32."""
     d = _norm_desc(res, y, w_post, gate, alpha, w_pre, eps)
+    dev, device = res.get_device(), res.device
     if (dn is None) != (w_pre is None):
         raise ValueError("dn must be given iff w_pre is")
-    for name, t in (("dr", dr), ("dn", dn)):
-        if t is not None:
-            _like(t, res, res.shape, name)
-    f32 = dict(dtype=torch.float32, device=res.device)
-    cols = res.shape[1]
-    out = {"res": torch.empty_like(res), "y": None if y is None else torch.empty_like(res),
-           "w_post": None if w_post is None else torch.empty(cols, **f32),
-           "w_pre": None if w_pre is None else torch.empty(cols, **f32), "gate": None}
-    if gate is not None:
-        out["gate"] = torch.empty_like(gate) if d.gate_kind == Q4_GATE_ELEMENT else torch.empty(gate.shape, **f32)
-    nbytes = _lib.block_norm_workspace_bytes(ctypes.byref(d))
-    ws = _scratch(nbytes, res)
-    _call("block_norm_backward", res, ctypes.byref(d), _dp(dr), _dp(dn), out["res"].data_ptr(), _dp(out["y"]),
-          _dp(out["w_post"]), _dp(out["gate"]), _dp(out["w_pre"]), _dp(ws), nbytes)
+    if dr is not None:
+        _arg(dr, "dr", res.dtype, res.shape, dev)
+    if dn is not None:
+        _arg(dn, "dn", res.dtype, res.shape, dev)
+
+    def f32(like):
+        return None if like is None else torch.empty_like(like, dtype=torch.float32)
+
+    out = {"res": torch.empty_like(res), "y": None if y is None else torch.empty_like(res), "w_post": f32(w_post),
+           "w_pre": f32(w_pre), "gate": torch.empty_like(gate) if d.gate_kind == Q4_GATE_ELEMENT else f32(gate)}
+    nbytes = _lib.block_norm_workspace_bytes(d)
+    ws = _scratch(nbytes, device)
+    _call("block_norm_backward", _lib.block_norm_backward, dev, d, _dp(dr), _dp(dn), out["res"].data_ptr(),
+          _dp(out["y"]), _dp(out["w_post"]), _dp(out["gate"]), _dp(out["w_pre"]), _dp(ws), nbytes)
     return out
