@@ -11,13 +11,13 @@
 // weights in dx; dg, du and x in the weight gradients), whose fragments come out of LDS
 // through the transposing 8-byte reads, so no transposed copy is ever made.
 //
-// Tiles: K advances 128 bytes (64 16-bit values, 128 codes) per step.  Panels are copied
+// Tiles: K advances SB = 64 or 128 bytes per step (32 to 128 elements).  Panels are copied
 // global -> LDS in 16-byte chunks; the buffer descriptor of each step covers exactly what
 // is left of the panel, so rows past its end and the masked K tail read as zero.  Chunks
 // are XOR-swizzled so that the fragment reads hit distinct banks:
-//   KC  [rows][128 B]: chunk c of row r at c ^ (r / 2 % 8)  (two rows per bank period)
-//   MC  [64 k][2 rows B]: 32-byte piece p of row k at p ^ f(k), f from the bits of k that
-//       differ between the 8 rows a transposing read touches at once.
+//   KC  [rows][SB]: chunk c of row r at c ^ f(r), f over the rows that share a bank period
+//   MC  [K of a step][2 rows B]: 32-byte piece p of row k at p ^ f(k), f from the bits of k
+//       that differ between the 8 rows a transposing read touches at once.
 #include <type_traits>
 
 #include "common.h"
@@ -35,7 +35,6 @@ enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_INT8 = 2 };
 
 template <Act A> struct Num {
   static constexpr int ESZ = A == Act::I8 ? 1 : 2;
-  static constexpr int STEP = kStepBytes / ESZ;   // K elements per step
   typedef typename std::conditional<A == Act::I8, i32x4_t, f32x4_t>::type acc_t;
   static Q4_DEVICE acc_t mfma(u32x4_t a, u32x4_t b, acc_t c) {
     if constexpr (A == Act::I8) return mfma_i8_16x16x64(a, b, c);
@@ -50,7 +49,7 @@ struct DenseArgs {
   const void* b[2];
   int64_t lda, ldb;
   int32_t M, N, K;
-  int32_t segs, batches, ksplit;
+  int32_t batches, ksplit;
   void* c[2];
   int64_t ldc;
   int32_t c_dtype;          // 0 fp32, 1 fp16, 2 bf16
@@ -242,24 +241,23 @@ struct Panel {
     return in ? uint32_t(r * ld * ESZ + c * 16) : kNoByte;
   }
 
-  // Where the panel's K steps lie: step s starts s * inc bytes after base; `left` bytes from
-  // base on belong to the operand.
-  struct Source {
-    uint64_t base, left;
+  // What is left of the panel from the next K step on: `left` bytes at `addr`; a step
+  // advances by `inc` bytes.
+  struct Feed {
+    uint64_t addr, left;
     uint32_t inc;
+    Q4_DEVICE u32x4_t rsrc(bool valid) const {   // empty if !valid
+      const uint32_t high = uint32_t(left >> 32) | uint32_t(left) >> 31;
+      return u32x4_t{uint32_t(addr), uint32_t(addr >> 32) & 0xffffu,
+                     !valid ? 0u : high ? 0x7fffffffu : uint32_t(left), 0x00020000u};
+    }
+    Q4_DEVICE void next() { addr += inc, left -= inc; }
   };
-  static Q4_DEVICE Source source(const void* p, int64_t ld, int rows, int K, int row0) {
-    const uint64_t at = uint64_t(MC ? int64_t(row0) : int64_t(row0) * ld) * ESZ;
-    return Source{reinterpret_cast<uint64_t>(p) + at, uint64_t(MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at,
-                  MC ? uint32_t(ld) * SB : uint32_t(SB)};
-  }
-  // Descriptor of step `s` (a step of the panel: left > s * inc), empty if !valid.
-  static Q4_DEVICE u32x4_t rsrc(const Source& f, int s, bool valid) {
-    const uint64_t off = uint64_t(uint32_t(s)) * f.inc;
-    const uint64_t a = f.base + off, left = f.left - off;
-    const uint32_t high = uint32_t(left >> 32) | uint32_t(left) >> 31;
-    const uint32_t n = high ? 0x7fffffffu : uint32_t(left);
-    return u32x4_t{uint32_t(a), uint32_t(a >> 32) & 0xffffu, valid ? n : 0u, 0x00020000u};
+  // The panel from row `row0` on (rows x K elements, leading dimension ld), at step `step`.
+  static Q4_DEVICE Feed feed(const void* p, int64_t ld, int rows, int K, int row0, int step) {
+    const uint32_t inc = MC ? uint32_t(ld) * SB : uint32_t(SB);
+    const uint64_t at = uint64_t(MC ? int64_t(row0) : int64_t(row0) * ld) * ESZ + uint64_t(uint32_t(step)) * inc;
+    return Feed{reinterpret_cast<uint64_t>(p) + at, uint64_t(MC ? int64_t(K) * ld : int64_t(rows) * ld) * ESZ - at, inc};
   }
 
   // Lane's byte address of a fragment read at block 0, half 0; blocks and halves flip bits
@@ -291,12 +289,27 @@ struct Panel {
   }
 };
 
+// Copies first .. first + N - 1 of a panel's K step into its LDS image at `at`.
+template <typename P, int N>
+Q4_DEVICE void copies(const u32x4_t& rs, uint32_t at, int first, int lane, int64_t ld, int left) {
+  if constexpr (N == 2) {
+    copy2_to_lds(rs, at + first * 1024, P::offset(first, lane, ld, left), P::offset(first + 1, lane, ld, left));
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) copy_to_lds<16>(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left), 0u);
+  }
+}
+
 // Waits until at most N copies of this wave are in flight and its LDS reads are done,
 // then joins the workgroup's barrier.
 template <int N>
 Q4_DEVICE void wait_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+
+// K segments of a product: dx (the one of a KC and an MC panel) runs over the gate rows, then
+// over the up rows; the others have one.
+constexpr int segments(bool amc, bool bmc) { return !amc && bmc ? 2 : 1; }
 
 // Work item of a workgroup: workgroup b runs on XCD b % 8; each XCD takes one contiguous
 // range of items (its L2 keeps the panels they share), in groups of 8 row tiles that walk
@@ -323,19 +336,22 @@ Q4_DEVICE Item item_of(int64_t b, int64_t total, int batches, int mtiles, int nt
 }
 
 // ---------------------------------------------------------------- tile kernel
-// BM x BN per workgroup of 2 x 2 waves, a ring of three K steps in LDS: step s + 2 is
-// copied while step s is multiplied, one barrier per step.
-template <Act A, bool AMC, bool BMC, int BM, int BN, int EPI>
+// BM x BN per workgroup of 2 x 2 waves, a ring of NS K steps of SB bytes in LDS: step
+// s + NS - 1 is copied while step s is multiplied, one barrier per step.  128 x 128 tiles
+// take 4 x 64 bytes (64 KB, two workgroups per CU, each hiding the other's barriers), 64 x 64
+// tiles 3 x 128 bytes (48 KB, three per CU).
+template <Act A, bool AMC, bool BMC, int BM, int BN, int SB, int NS, int EPI>
 __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntiles) {
   typedef Num<A> T;
   typedef typename T::acc_t acc_t;
   constexpr bool DUAL = EPI == EPI_SWIGLU;
+  constexpr int SEGS = segments(AMC, BMC);
   constexpr int BP = DUAL ? BN / 2 : BN;            // rows of a B panel
-  typedef Panel<A, AMC, BM, kStepBytes> PA;
-  typedef Panel<A, BMC, BP, kStepBytes> PB;
+  typedef Panel<A, AMC, BM, SB> PA;
+  typedef Panel<A, BMC, BP, SB> PB;
+  constexpr int STEP = SB / T::ESZ;                 // K elements per step
   constexpr int NP = DUAL ? 2 : 1;
   constexpr int STAGE = PA::BYTES + NP * PB::BYTES;
-  constexpr int NS = 3;
   constexpr int CA = PA::COPIES / 4, CB = PB::COPIES / 4;   // copies per wave
   constexpr int CPW = CA + NP * CB;
   constexpr int MB = BM / 32, NB = BP / 32;         // 16-blocks per wave
@@ -346,33 +362,40 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
   const int wm = wid & 1, wn = wid >> 1;
   const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
   const int m0 = it.mt * BM, n0 = it.nt * BP;
-  const int seg_steps = (g.K + T::STEP - 1) / T::STEP;
-  const int all = seg_steps * g.segs;
+  const int seg_steps = (g.K + STEP - 1) / STEP;
+  const int all = seg_steps * SEGS;
   const int per = (all + g.ksplit - 1) / g.ksplit;
   const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
 
-  const auto fa0 = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0);
-  const auto fb0 = PB::source(g.b[0], g.ldb, g.N, g.K, n0);
-  const auto fa1 = PA::source(g.a[1], g.lda, g.M, g.K, m0);   // second K segment
-  const auto fb1 = PB::source(g.b[1], g.ldb, g.N, g.K, n0);   // second K segment or B panel
   const uint32_t lds0 = lds_addr(ring);
-  auto issue = [&](int s) {
-    const bool second = s >= seg_steps;
-    const int ss = second ? s - seg_steps : s;
-    const uint32_t base = lds0 + uint32_t((s - s_begin) % NS) * STAGE;
-    const auto ra = PA::rsrc(second ? fa1 : fa0, ss, true);
-    const int left = g.K * T::ESZ - ss * kStepBytes;
+  // the next step to copy: its place in each panel, its bytes of K, its slot
+  int si = s_begin, k_left = g.K * T::ESZ, slot_in = 0;
+  typename PA::Feed fda;
+  typename PB::Feed fdb[NP];
+  auto start = [&](int seg, int step) {
+    fda = PA::feed((SEGS == 2 ? seg : it.z) ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0, step);
 #pragma unroll
-    for (int j = 0; j < CA; ++j)
-      copy_to_lds<16>(ra, base + (wid * CA + j) * 1024, PA::offset(wid * CA + j, lane, g.lda, AMC ? g.M - m0 : left), 0u);
+    for (int p = 0; p < NP; ++p)
+      fdb[p] = PB::feed((DUAL ? p : seg) ? g.b[1] : g.b[0], g.ldb, g.N, g.K, n0, step);
+    k_left = g.K * T::ESZ - step * SB;
+  };
+  if (SEGS == 1 || s_begin < seg_steps) start(0, s_begin);
+  else start(1, s_begin - seg_steps);
+  auto issue = [&]() {
+    if constexpr (SEGS == 2)
+      if (si == seg_steps) start(1, 0);
+    const bool in = si < s_end;
+    const uint32_t at = lds0 + slot_in * STAGE;
+    copies<PA, CA>(fda.rsrc(in), at, wid * CA, lane, g.lda, AMC ? g.M - m0 : k_left);
+    fda.next();
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const auto rb = PB::rsrc(p == 1 || second ? fb1 : fb0, ss, true);
-#pragma unroll
-      for (int j = 0; j < CB; ++j)
-        copy_to_lds<16>(rb, base + PA::BYTES + p * PB::BYTES + (wid * CB + j) * 1024,
-                        PB::offset(wid * CB + j, lane, g.ldb, BMC ? g.N - n0 : left), 0u);
+      copies<PB, CB>(fdb[p].rsrc(in), at + PA::BYTES + p * PB::BYTES, wid * CB, lane, g.ldb, BMC ? g.N - n0 : k_left);
+      fdb[p].next();
     }
+    k_left -= SB;
+    ++si;
+    slot_in = slot_in == NS - 1 ? 0 : slot_in + 1;
   };
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
 
@@ -384,34 +407,37 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[p][i][j] = acc_t{0, 0, 0, 0};
 
-  if (s_begin < s_end) {
-    issue(s_begin);
-    if (s_begin + 1 < s_end) issue(s_begin + 1);
-  }
+  constexpr int AHEAD = NS - 1;   // steps in flight beyond the current one's
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) issue();
+  int slot = 0;
   for (int s = s_begin; s < s_end; ++s) {
     // step s is in LDS for every wave, and every wave is done reading step s - 1
-    if (s + 1 < s_end) wait_barrier<CPW>();
-    else wait_barrier<0>();
-    if (s + 2 < s_end) issue(s + 2);
-    const uint32_t base = lds0 + uint32_t((s - s_begin) % NS) * STAGE;
+    wait_barrier<(AHEAD - 1) * CPW>();
+    const uint32_t base = lds0 + slot * STAGE;
+    slot = slot == NS - 1 ? 0 : slot + 1;
+    u32x4_t fa[SB / 64][MB], fb[SB / 64][NP][NB];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      u32x4_t fa[MB], fb[NP][NB];
+    for (int sub = 0; sub < SB / 64; ++sub) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i) fa[i] = PA::frag(base, lba, wm * (BM / 2) + 16 * i, sub);
+      for (int i = 0; i < MB; ++i) fa[sub][i] = PA::frag(base, lba, wm * (BM / 2) + 16 * i, sub);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-          fb[p][j] = PB::frag(base + PA::BYTES + p * PB::BYTES, lbb, wn * (BP / 2) + 16 * j, sub);
+          fb[sub][p][j] = PB::frag(base + PA::BYTES + p * PB::BYTES, lbb, wn * (BP / 2) + 16 * j, sub);
+    }
+    issue();   // while the fragments are on their way
+#pragma unroll
+    for (int sub = 0; sub < SB / 64; ++sub)
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-          for (int j = 0; j < NB; ++j) acc[p][i][j] = T::mfma(fb[p][j], fa[i], acc[p][i][j]);
-    }
+          for (int j = 0; j < NB; ++j) acc[p][i][j] = T::mfma(fb[sub][p][j], fa[sub][i], acc[p][i][j]);
   }
+  wait_barrier<0>();   // no copy may land after the workgroup's end
 
   // lane: row m = lane % 16 of its block, columns 4 (lane / 16) .. + 3
   const int q = lane >> 4;
@@ -459,6 +485,7 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
   typedef Num<A> T;
   typedef typename T::acc_t acc_t;
   constexpr bool DUAL = EPI == EPI_SWIGLU;
+  constexpr int SEGS = segments(AMC, BMC);
   constexpr int SB = 64;
   constexpr int STEP = SB / T::ESZ;
   constexpr int BP = DUAL ? 128 : 256;              // rows of a B panel
@@ -474,7 +501,7 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
   const Item it = item_of(blockIdx.x, gridDim.x, g.batches, mtiles, ntiles);
   const int m0 = it.mt * 256, n0 = it.nt * BP;
   const int seg_steps = (g.K + STEP - 1) / STEP;
-  const int all = seg_steps * g.segs;
+  const int all = seg_steps * SEGS;
   const int per = (all + g.ksplit - 1) / g.ksplit;
   const int s_begin = it.ks * per, s_end = min(all, s_begin + per);
   const uint32_t lds0 = lds_addr(ring);
@@ -482,24 +509,28 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
   // Each wave copies 2 KB of each operand per step (swiglu: waves 0..3 of the gate panel,
   // 4..7 of the up panel).  Past the last step the descriptor is empty: the copy counts, and
   // writes zeros that nothing reads.
-  const auto fa = PA::source(g.batches > 1 && it.z ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0);
-  const auto fb = PB::source(DUAL && wm ? g.b[1] : g.b[0], g.ldb, g.N, g.K, n0);
-  const uint64_t da = reinterpret_cast<uint64_t>(g.a[1]) - reinterpret_cast<uint64_t>(g.a[0]);
-  const uint64_t db = reinterpret_cast<uint64_t>(g.b[1]) - reinterpret_cast<uint64_t>(g.b[0]);
   const int cb = DUAL ? 2 * wn : 2 * wid;           // first copy of the wave in its B panel
-  auto issue = [&](int s) {
-    const bool second = s >= seg_steps;
-    const int ss = second ? s - seg_steps : s;
-    const uint32_t at = lds0 + uint32_t(s & 3) * SLOT + wid * 2048;
-    const int left = g.K * T::ESZ - ss * SB;
-    auto sa = fa;
-    auto sb = fb;
-    if (g.segs > 1 && second) sa.base += da, sb.base += db;
-    const int la = AMC ? g.M - m0 : left, lb = BMC ? g.N - n0 : left;
-    copy2_to_lds(PA::rsrc(sa, ss, s < s_end), at, PA::offset(2 * wid, lane, g.lda, la),
-                 PA::offset(2 * wid + 1, lane, g.lda, la));
-    copy2_to_lds(PB::rsrc(sb, ss, s < s_end), at + PA::BYTES, PB::offset(cb, lane, g.ldb, lb),
-                 PB::offset(cb + 1, lane, g.ldb, lb));
+  int si = s_begin, k_left = 0;                     // the next step to copy, its bytes of K
+  typename PA::Feed fda;
+  typename PB::Feed fdb;
+  auto start = [&](int seg, int step) {
+    fda = PA::feed((SEGS == 2 ? seg : it.z) ? g.a[1] : g.a[0], g.lda, g.M, g.K, m0, step);
+    fdb = PB::feed((DUAL ? wm : seg) ? g.b[1] : g.b[0], g.ldb, g.N, g.K, n0, step);
+    k_left = g.K * T::ESZ - step * SB;
+  };
+  if (SEGS == 1 || s_begin < seg_steps) start(0, s_begin);
+  else start(1, s_begin - seg_steps);
+  auto issue = [&]() {
+    if constexpr (SEGS == 2)
+      if (si == seg_steps) start(1, 0);
+    const bool in = si < s_end;
+    const uint32_t at = lds0 + uint32_t(si & 3) * SLOT;
+    copies<PA, 2>(fda.rsrc(in), at, 2 * wid, lane, g.lda, AMC ? g.M - m0 : k_left);
+    copies<PB, 2>(fdb.rsrc(in), at + PA::BYTES + (DUAL ? wm * PB::BYTES : 0), cb, lane, g.ldb, BMC ? g.N - n0 : k_left);
+    fda.next();
+    fdb.next();
+    k_left -= SB;
+    ++si;
   };
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
 
@@ -510,9 +541,9 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
     for (int j = 0; j < NB; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
-  issue(s_begin);
-  issue(s_begin + 1);
-  issue(s_begin + 2);
+  issue();
+  issue();
+  issue();
   asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
   if (wid >= 4) asm volatile("s_barrier" ::: "memory");
   for (int s = s_begin; s < s_end; ++s) {
@@ -525,7 +556,7 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
                    : PB::frag(p + PA::BYTES, lbb, wn * 64 + 16 * j, 0);
 #pragma unroll
     for (int i = 0; i < MB; ++i) va[i] = PA::frag(p, lba, wm * 128 + 16 * i, 0);
-    issue(s + 3);
+    issue();   // step s + 3
     // fragments in registers, copies of step s + 1 in LDS
     fence();
     asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -610,93 +641,85 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 16 MB rows: bound by reading the weights once.  A workgroup owns 16 output
-// columns (16 of each projection for swiglu); its W waves take the K steps in turn and
-// feed the matrix core straight from global memory (16 bytes per lane, the lanes of one
-// column a whole 128-byte line per step), then add their sums through LDS in wave order.
-template <Act A, int MB, int W, int EPI>
+// Up to 16 rows: bound by reading the weights once.  A wave's fragment is 16 weight rows (16
+// columns of y; for swiglu 8 gate and 8 up rows, so that twice as many workgroups share the
+// reading); the 8 waves of a workgroup own NF fragments' rows, take the 128-byte K steps in
+// turn and feed the matrix core straight from global memory (16 bytes per lane, two loads
+// cover a step's whole lines), four steps in flight, then add their sums through LDS in wave
+// order.  2048 / 8192 gated projection, one row: 14.5 us, 4.6 TB/s.
+template <Act A, int EPI, int W, int NF>
 __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
   typedef Num<A> T;
   typedef typename T::acc_t acc_t;
-  constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
-  __shared__ acc_t sums[W][NP * MB][64];
+  constexpr bool DUAL = EPI == EPI_SWIGLU;
+  __shared__ acc_t sums[W][NF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16;
+  const int row = lane & 15, quarter = (lane >> 4) * 16;
+  constexpr int COLS = DUAL ? 8 : 16;   // columns per fragment
+  const int n0 = blockIdx.x * (COLS * NF);
   const int64_t kb = int64_t(g.K) * T::ESZ;   // bytes of a row (a multiple of 16)
-  const int quarter = (lane >> 4) * 16;
-  const uint8_t* wp[NP];
-  const uint8_t* xp[MB];
-  const int col = min(n0 + (lane & 15), g.N - 1);
+  const void* wb = DUAL && row >= 8 ? g.b[1] : g.b[0];
+  const uint8_t* wp[NF];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) wp[p] = static_cast<const uint8_t*>(g.b[p]) + col * kb + quarter;
+  for (int f = 0; f < NF; ++f)
+    wp[f] = static_cast<const uint8_t*>(wb) + min(n0 + f * COLS + (DUAL ? row & 7 : row), g.N - 1) * kb + quarter;
+  const uint8_t* xp = static_cast<const uint8_t*>(g.a[0]) + min(row, g.M - 1) * kb + quarter;
+  acc_t acc[NF];
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
-    xp[i] = static_cast<const uint8_t*>(g.a[0]) + min(16 * i + (lane & 15), g.M - 1) * kb + quarter;
-  acc_t acc[NP][MB];
-#pragma unroll
-  for (int p = 0; p < NP; ++p)
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[p][i] = acc_t{0, 0, 0, 0};
+  for (int f = 0; f < NF; ++f) acc[f] = acc_t{0, 0, 0, 0};
 
   const int full = int(kb / kStepBytes);
-  constexpr int U = NP * MB >= 4 ? 2 : 4;   // steps in flight
   int s = wave;
   auto steps = [&](auto u_c) {
     constexpr int N = decltype(u_c)::value;
-    u32x4_t w[N][2][NP], x[N][2][MB];
+    u32x4_t w[N][2][NF], x[N][2];
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t at = int64_t(s + u * W) * kStepBytes + h * 64;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) w[u][h][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp[p] + at));
-#pragma unroll
-        for (int i = 0; i < MB; ++i) x[u][h][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
+        for (int f = 0; f < NF; ++f)
+          w[u][h][f] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp[f] + at));
+        x[u][h] = *reinterpret_cast<const u32x4_t*>(xp + at);
       }
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-          for (int i = 0; i < MB; ++i) acc[p][i] = T::mfma(w[u][h][p], x[u][h][i], acc[p][i]);
+        for (int f = 0; f < NF; ++f) acc[f] = T::mfma(w[u][h][f], x[u][h], acc[f]);
     s += N * W;
   };
-  while (s + (U - 1) * W < full) steps(std::integral_constant<int, U>{});
-  while (s < full) steps(std::integral_constant<int, 1>{});
+  while (s + 3 * W < full) steps(std::integral_constant<int, 4>{});
+  if (s + W < full) steps(std::integral_constant<int, 2>{});
+  if (s < full) steps(std::integral_constant<int, 1>{});
   if (s == full && kb % kStepBytes) {   // the K tail: lanes past the row's end hold zeros
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t at = int64_t(full) * kStepBytes + h * 64;
       const bool in = at + quarter < kb;
-      u32x4_t w[NP], x[MB];
+      const u32x4_t x = in ? *reinterpret_cast<const u32x4_t*>(xp + at) : u32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int p = 0; p < NP; ++p) w[p] = in ? *reinterpret_cast<const u32x4_t*>(wp[p] + at) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < MB; ++i) x[i] = in ? *reinterpret_cast<const u32x4_t*>(xp[i] + at) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) acc[p][i] = T::mfma(w[p], x[i], acc[p][i]);
+      for (int f = 0; f < NF; ++f)
+        acc[f] = T::mfma(in ? *reinterpret_cast<const u32x4_t*>(wp[f] + at) : u32x4_t{0, 0, 0, 0}, x, acc[f]);
     }
   }
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
-#pragma unroll
-    for (int i = 0; i < MB; ++i) sums[wave][p * MB + i][lane] = acc[p][i];
+  for (int f = 0; f < NF; ++f) sums[wave][f][lane] = acc[f];
   __syncthreads();
-  for (int i = wave; i < MB; i += W) {
-    acc_t v[NP];
+  if (wave >= NF) return;
+  acc_t v = sums[0][wave][lane];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      v[p] = sums[0][p * MB + i][lane];
+  for (int w = 1; w < W; ++w) v += sums[w][wave][lane];
+  const int m = row, n = n0 + wave * COLS + 4 * (lane >> 4);
+  if constexpr (DUAL) {   // quarters 0, 1: gate columns; 2, 3: the same columns' up values
+    acc_t up;
 #pragma unroll
-      for (int w = 1; w < W; ++w) v[p] += sums[w][p * MB + i][lane];
-    }
-    const int m = 16 * i + (lane & 15), n = n0 + 4 * (lane >> 4);
-    finish4<A, EPI>(g, 0, m, n, v[0], v[NP - 1], row_scale<EPI>(g, m), col_scales<EPI>(g, n));
+    for (int i = 0; i < 4; ++i) up[i] = __shfl_xor(v[i], 32, 64);
+    if (lane < 32) finish4<A, EPI>(g, 0, m, n, v, up, 0.f, col_scales<EPI>(g, n));
+  } else {
+    finish4<A, EPI>(g, 0, m, n, v, v, row_scale<EPI>(g, m), col_scales<EPI>(g, n));
   }
 }
 
@@ -798,9 +821,9 @@ hipError_t launch_tiles(DenseArgs g, const Plan& p, hipStream_t st) {
   if (p.bm == 256)
     hipLaunchKernelGGL((k_dense_big<A, AMC, BMC, EPI>), dim3(grid), dim3(512), 0, st, g, mt, nt);
   else if (p.bm == 128)
-    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 128, 128, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 128, 128, 64, 4, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else
-    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 64, 64, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+    hipLaunchKernelGGL((k_dense<A, AMC, BMC, 64, 64, 128, 3, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ksplit == 1) return e;
   const int64_t threads = int64_t(g.batches) * g.M * ((g.N + 3) / 4);
@@ -808,16 +831,25 @@ hipError_t launch_tiles(DenseArgs g, const Plan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <Act A, int EPI>
-hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
-  const dim3 grid(unsigned(ceil_div(g.N, 16)));
-  if (g.M <= 16) hipLaunchKernelGGL((k_dense_rows<A, 1, 8, EPI>), grid, dim3(512), 0, st, g);
-  else if (g.M <= 32) hipLaunchKernelGGL((k_dense_rows<A, 2, 8, EPI>), grid, dim3(512), 0, st, g);
-  else hipLaunchKernelGGL((k_dense_rows<A, 4, 8, EPI>), grid, dim3(512), 0, st, g);
+template <Act A, int EPI, int W, int NF>
+hipError_t launch_rows_as(const DenseArgs& g, hipStream_t st) {
+  const dim3 grid(unsigned(ceil_div(g.N, (EPI == EPI_SWIGLU ? 8 : 16) * NF)));
+  hipLaunchKernelGGL((k_dense_rows<A, EPI, W, NF>), grid, dim3(64 * W), 0, st, g);
   return hipGetLastError();
 }
 
-bool few_rows(int64_t t) { return t <= 64; }
+// Two fragments per wave halve the reads of x, which count from a few rows on, as long as
+// enough workgroups are left: 7168 x 7168 INT8, 16 rows, 18.8 -> 16.3 us (one row 13.8 ->
+// 13.1); but 8192 x 2048, 64 workgroups instead of 128, 10.5 -> 15.1 us.
+template <Act A, int EPI>
+hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
+  const int64_t wgs = ceil_div(g.N, EPI == EPI_SWIGLU ? 16 : 32);
+  return g.M > 4 && wgs >= 192 ? launch_rows_as<A, EPI, 8, 2>(g, st) : launch_rows_as<A, EPI, 8, 1>(g, st);
+}
+
+// Beyond 16 rows the tiles with split K are faster (7168 / 2048 gated projection, 16 rows:
+// 19.8 us against 19.0; 2048 x 2048 INT8: 4.1 us against 7.5).
+bool few_rows(int64_t t) { return t <= 16; }
 
 }  // namespace
 
@@ -842,7 +874,7 @@ hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_
   g.b[0] = g.b[1] = wq;
   g.lda = g.ldb = k;
   g.M = int32_t(t), g.N = int32_t(n), g.K = int32_t(k);
-  g.segs = g.batches = g.ksplit = 1;
+  g.batches = g.ksplit = 1;
   g.c[0] = y;
   g.ldc = n;
   g.c_dtype = y_dtype;
@@ -866,7 +898,7 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
   g.b[0] = wg, g.b[1] = wu;
   g.lda = g.ldb = h;
   g.M = int32_t(t), g.N = int32_t(i), g.K = int32_t(h);
-  g.segs = g.batches = g.ksplit = 1;
+  g.batches = g.ksplit = 1;
   g.c[0] = out;
   g.ldc = i;
   g.c_dtype = f16 ? 1 : 2;
@@ -913,7 +945,7 @@ hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* w
     g.b[0] = wg, g.b[1] = wu;
     g.lda = i, g.ldb = h;
     g.M = int32_t(t), g.K = int32_t(i);
-    g.segs = 2, g.batches = 1;
+    g.batches = 1;
     g.c[0] = g.c[1] = dx;
     const Plan p = plan_of(t, h, 1, 2 * ceil_div(i, 64), 1);
     const hipError_t e = f16 ? launch_tiles<Act::F16, false, true, EPI_STORE>(g, p, st)
@@ -925,7 +957,7 @@ hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* w
   g.b[0] = g.b[1] = x;
   g.lda = i, g.ldb = h;
   g.M = int32_t(i), g.K = int32_t(t);
-  g.segs = 1, g.batches = 2;
+  g.batches = 2;
   g.c[0] = dwg, g.c[1] = dwu;
   const Plan p = plan_of(i, h, 1, ceil_div(t, 64), 2);
   return f16 ? launch_tiles<Act::F16, true, true, EPI_STORE>(g, p, st)
