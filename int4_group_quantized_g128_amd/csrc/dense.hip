@@ -788,24 +788,40 @@ struct Plan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile and K split of a product of `steps` K steps over `panels` B panels: the largest
-// tile that gives (nearly) every CU work, if need be with K split in up to four slices of at
-// least 16 steps; else the smallest one with K split until the launch has about 512
-// workgroups of at least 4 steps each.
+// Estimated time (us) of a product of `steps` 128-byte K steps with square tiles of `bm` and
+// K in `ks` slices.  Per tile size: workgroups a CU holds, time of a step when it is alone
+// on its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
+// workgroup), time of a workgroup's start and end.  The figures are fitted to 69 shapes of
+// both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three tiles and
+// up to 8 splits: the plan below then lies within 1 % of the fastest of them on every one
+// (a rule that only counted workgroups lost up to 70 %).
+double plan_us(int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
+  const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
+  static const int held[3] = {3, 2, 1};
+  static const double alone[3] = {0.27, 0.55, 0.62}, full[3] = {0.21, 0.45, 1.23}, ends[3] = {1.9, 8.0, 4.0};
+  const int64_t per = ceil_div(steps, ks);
+  const int64_t wgs = ceil_div(m, bm) * ceil_div(n * panels, bm) * batches * ceil_div(steps, per);
+  const int64_t rounds = ceil_div(wgs, 256 * held[t]);
+  const int64_t last = std::min<int64_t>(held[t], ceil_div(wgs - (rounds - 1) * 256 * held[t], 256));
+  const auto slice = [&](int64_t on_cu) { return ends[t] + per * std::max(alone[t], full[t] * on_cu); };
+  double us = (rounds - 1) * slice(held[t]) + slice(last);
+  // the join: a launch, a chain of reads, and the slices' bytes at 4.5 TB/s
+  if (ks > 1) us += 2.9 + 0.5 * ks + double(ks) * m * n * panels * batches * 4 / 4.5e6;
+  return us;
+}
+
+// Tile and K split with the least estimated time.
 Plan plan_of(int64_t m, int64_t n, int panels, int64_t steps, int batches) {
-  const int64_t big = ceil_div(m, 256) * ceil_div(n * panels, 256) * batches;
-  if (big >= 192) return {256, 256, 1};
-  if (big >= 64) {
-    const int64_t want = ceil_div(192, big);
-    const int64_t per = ceil_div(steps, want);
-    if (per >= 16) return {256, 256, int(ceil_div(steps, per))};
-  }
-  if (ceil_div(m, 128) * ceil_div(n * panels, 128) * batches >= 256) return {128, 128, 1};
-  const int64_t tiles = ceil_div(m, 64) * ceil_div(n * panels, 64) * batches;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 4));
-  if (steps == 0) return {64, 64, 1};   // no tokens: the weight gradients are zero
-  const int64_t per = ceil_div(steps, std::min<int64_t>(want, 32));
-  return {64, 64, int(ceil_div(steps, per))};
+  Plan best{64, 64, 1};
+  if (steps == 0) return best;   // no tokens: the weight gradients are zero
+  double us = plan_us(m, n, panels, steps, batches, 64, 1);
+  for (const int bm : {64, 128, 256})
+    for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (ks > 1 && steps / ks < 2) break;
+      const double u = plan_us(m, n, panels, steps, batches, bm, ks);
+      if (u < us) us = u, best = Plan{bm, bm, int(ceil_div(steps, ceil_div(steps, ks)))};
+    }
+  return best;
 }
 
 int64_t part_bytes(const Plan& p, int64_t m, int64_t n, int panels, int batches) {
