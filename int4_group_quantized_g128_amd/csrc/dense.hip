@@ -791,9 +791,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Estimated time (us) of a product of `steps` 128-byte K steps with square tiles of `bm` and
 // K in `ks` slices.  Per tile size: workgroups a CU holds, time of a step when it is alone
 // on its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
-// workgroup), time of a workgroup's start and end.  The figures are fitted to 69 shapes of
+// workgroup), time of a workgroup's start and end.  The figures are fitted to 75 shapes of
 // both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three tiles and
-// up to 8 splits: the plan below then lies within 1 % of the fastest of them on every one
+// up to 8 splits: the plan below then lies within 2 % of the fastest of them on every one
 // (a rule that only counted workgroups lost up to 70 %).
 double plan_us(int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;

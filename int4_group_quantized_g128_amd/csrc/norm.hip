@@ -25,7 +25,8 @@ namespace q4 {
 namespace {
 
 constexpr int kMaxCols = 16384;
-constexpr int kGradSlots = 3;   // partial sums per row group: dw_pre, dw_post, channel gate
+constexpr int kBwdWaves = 8;
+constexpr int kGradSlots = 3;   // partial sums per workgroup: dw_pre, dw_post, channel gate
 
 struct NF32 {};
 struct NF16 {};
@@ -44,7 +45,7 @@ template <> struct Elem<NF16> {
 template <> struct Elem<NBF16> {
   typedef uint16_t type;
   static Q4_DEVICE float up(uint16_t v) { return bf16_to_f32(v); }
-  static Q4_DEVICE uint16_t down(float v) { return f32_to_bf16(v); }
+  static Q4_DEVICE uint16_t down(float v) { return bitcast<uint16_t>(__bf16(v)); }
 };
 
 // Columns of thread `tid` of TPR threads that share a row: NV vectors of 8 consecutive
@@ -54,31 +55,56 @@ template <typename T, int TPR, int NV, bool VEC>
 struct Row {
   typedef typename Elem<T>::type S;
   static constexpr int N = NV * 8;
-  static Q4_DEVICE int col(int tid, int i) { return VEC ? 8 * ((i / 8) * TPR + tid) + i % 8 : i * TPR + tid; }
 
-  static Q4_DEVICE void load(const void* base, int64_t row, int cols, int tid, float v[N]) {
+  // The thread's part of a row as stored (16-byte registers, or one value each).
+  struct Raw {
+    static constexpr int Q = VEC ? NV * int(sizeof(S)) / 2 : 1;
+    uint4 q[Q];
+    S e[VEC ? 1 : N];
+  };
+  static Q4_DEVICE Raw fetch(const void* base, int64_t row, int cols, int tid) {
     const S* p = static_cast<const S*>(base) + row * cols;
+    Raw r;
     if constexpr (VEC) {
+      constexpr int PER = sizeof(S) / 2;   // 16-byte registers per vector
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = 8 * (j * TPR + tid);
-        if (c < cols) {
-          S t[8];
-          *reinterpret_cast<uint4*>(t) = load16(p + c);
-          if constexpr (sizeof(S) == 4) *reinterpret_cast<uint4*>(t + 4) = load16(p + c + 4);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * j + i] = Elem<T>::up(t[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * j + i] = 0.f;
-        }
+        for (int h = 0; h < PER; ++h) r.q[j * PER + h] = c < cols ? load16(p + c + 4 * h) : make_uint4(0, 0, 0, 0);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = i * TPR + tid;
-        v[i] = c < cols ? Elem<T>::up(p[c]) : 0.f;
+        r.e[i] = c < cols ? p[c] : S(0);
       }
+    }
+    return r;
+  }
+  // Every element the same value (a missing weight is ones, a token's gate its value).
+  static Q4_DEVICE Raw fill(S v) {
+    Raw r;
+    uint32_t u;
+    if constexpr (sizeof(S) == 4) u = __float_as_uint(v);
+    else u = v | uint32_t(v) << 16;
+#pragma unroll
+    for (int j = 0; j < Raw::Q; ++j) r.q[j] = make_uint4(u, u, u, u);
+#pragma unroll
+    for (int i = 0; i < (VEC ? 1 : N); ++i) r.e[i] = v;
+    return r;
+  }
+  static Q4_DEVICE float at(const Raw& r, int i) {
+    if constexpr (!VEC) {
+      return Elem<T>::up(r.e[i]);
+    } else if constexpr (sizeof(S) == 4) {
+      const uint4 v = r.q[i / 4];
+      return __uint_as_float(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+    } else {
+      const uint4 v = r.q[i / 8];
+      const int w = i % 8 / 2;
+      const uint32_t u = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+      return Elem<T>::up(S(i % 2 ? u >> 16 : u & 0xffffu));
     }
   }
 
@@ -107,10 +133,21 @@ struct Row {
   }
 
   static Q4_DEVICE void store_f32(float* p, int cols, int tid, const float v[N]) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = col(tid, i);
-      if (c < cols) p[c] = v[i];
+      for (int j = 0; j < NV; ++j) {
+        const int c = 8 * (j * TPR + tid);
+        if (c < cols) {
+          *reinterpret_cast<f32x4_t*>(p + c) = f32x4_t{v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]};
+          *reinterpret_cast<f32x4_t*>(p + c + 4) = f32x4_t{v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * TPR + tid;
+        if (c < cols) p[c] = v[i];
+      }
     }
   }
 
@@ -173,10 +210,18 @@ Q4_DEVICE float rstd_of(float sumsq, int cols, float eps) { return 1.0f / sqrtf(
 template <int WPR> constexpr int rows_per_wg() { return WPR >= 4 ? 1 : 4 / WPR; }
 template <int WPR> constexpr int threads_per_wg() { return 64 * WPR * rows_per_wg<WPR>(); }
 
+// Whether the next row is fetched ahead (16 waves of 128 registers, or single columns, have
+// no room for it).
+template <int WPR, bool VEC> constexpr bool fetch_ahead() { return VEC && WPR < 16; }
+
+// Every workgroup walks rows base, base + step, ...: the weights stay in its registers, and
+// the next row is on its way while the current one is reduced.  Four waves per SIMD: 4096 x
+// 7168 bf16 with a channel gate, two workgroups per CU.
 template <typename T, int WPR, int NV, bool VEC>
-__global__ void __launch_bounds__(threads_per_wg<WPR>()) k_block_norm_fwd(BlockNormArgs a, void* r_out, void* n_out,
+__global__ void __launch_bounds__(threads_per_wg<WPR>()) __attribute__((amdgpu_waves_per_eu(sizeof(typename Elem<T>::type) == 2 && VEC ? 4 : 1))) k_block_norm_fwd(BlockNormArgs a, void* r_out, void* n_out,
                                                                           int8_t* q_out, float* s_out) {
   typedef Row<T, 64 * WPR, NV, VEC> R;
+  typedef typename R::Raw Raw;
   constexpr int N = R::N;
   __shared__ float slots[2 * 2 * 16];
   const int wave = threadIdx.x >> 6;
@@ -184,49 +229,53 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>()) k_block_norm_fwd(BlockN
   const int cols = a.cols;
   int phase = 0;
   const int64_t step = int64_t(gridDim.x) * rows_per_wg<WPR>();
-  for (int64_t base = int64_t(blockIdx.x) * rows_per_wg<WPR>(); base < a.rows; base += step) {
-    int64_t row = base + threadIdx.x / (64 * WPR);
-    if constexpr (rows_per_wg<WPR>() > 1)
-      if (row >= a.rows) break;   // WPR < 4: no barrier below (WPR == 1)
+  int64_t row = int64_t(blockIdx.x) * rows_per_wg<WPR>() + threadIdx.x / (64 * WPR);
+  if (row >= a.rows) return;   // whole waves, and with WPR >= 4 the whole workgroup
+  const Raw ones = R::fill(Elem<T>::down(1.f));
+  Raw w_post = ones, w_pre = ones, gate = ones, res = ones, y = ones;
+  if (a.w_post) w_post = R::fetch(a.w_post, 0, cols, tid);
+  if (a.w_pre) w_pre = R::fetch(a.w_pre, 0, cols, tid);
+  if (a.gate_kind == kGateChannel) gate = R::fetch(a.gate, 0, cols, tid);
+  auto fetch = [&](int64_t row, Raw& res, Raw& y, Raw& gate) {
+    res = R::fetch(a.res, row, cols, tid);
+    if (a.y) y = R::fetch(a.y, row, cols, tid);
+    if (a.gate_kind == kGateElement) gate = R::fetch(a.gate, row, cols, tid);
+    if (a.gate_kind == kGateToken) gate = R::fill(static_cast<const typename R::S*>(a.gate)[row]);
+  };
+  constexpr bool AHEAD = fetch_ahead<WPR, VEC>();
+  if constexpr (AHEAD) fetch(row, res, y, gate);
+  for (; row < a.rows; row += step) {
+    Raw next_res, next_y, next_gate;
+    if constexpr (AHEAD) {
+      next_res = res, next_y = y, next_gate = gate;
+      if (row + step < a.rows) fetch(row + step, next_res, next_y, next_gate);
+    } else {
+      fetch(row, res, y, gate);
+    }
     float r[N];
-    R::load(a.res, row, cols, tid, r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = R::at(res, i);
     if (a.y) {
-      float p[N];
-      R::load(a.y, row, cols, tid, p);
+      float rs = 1.f;
       if (a.w_post) {
-        float w[N], ss[1] = {0.f};
-        R::load(a.w_post, 0, cols, tid, w);
+        float ss[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss[0] += p[i] * p[i];
+        for (int i = 0; i < N; ++i) ss[0] += R::at(y, i) * R::at(y, i);
         row_reduce<WPR, 1>(ss, slots, wave, phase);
-        const float rs = rstd_of(ss[0], cols, a.eps);
-#pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = p[i] * rs * w[i];
+        rs = rstd_of(ss[0], cols, a.eps);
       }
-      if (a.gate_kind == kGateToken) {
-        const float g = a.alpha * Elem<T>::up(static_cast<const typename R::S*>(a.gate)[row]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] += g * p[i];
-      } else if (a.gate_kind == kGateNone) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] += a.alpha * p[i];
-      } else {
-        float g[N];
-        R::load(a.gate, a.gate_kind == kGateElement ? row : 0, cols, tid, g);
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] += a.alpha * (g[i] * p[i]);
-      }
+      for (int i = 0; i < N; ++i) r[i] += a.alpha * (R::at(gate, i) * (R::at(y, i) * rs * R::at(w_post, i)));
       R::store(r_out, row, cols, tid, r);
     }
     if (a.w_pre) {
-      float w[N], ss[1] = {0.f};
-      R::load(a.w_pre, 0, cols, tid, w);
+      float ss[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < N; ++i) ss[0] += r[i] * r[i];
       row_reduce<WPR, 1>(ss, slots, wave, phase);
       const float rs = rstd_of(ss[0], cols, a.eps);
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = r[i] * rs * w[i];
+      for (int i = 0; i < N; ++i) r[i] = r[i] * rs * R::at(w_pre, i);
       if (q_out) {
         // per-token INT8 codes of the unrounded n, by the rule of act_quant_int8
         // (a row with a NaN or an infinity, which no code holds, gets codes 0 and a NaN scale)
@@ -236,27 +285,28 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>()) k_block_norm_fwd(BlockN
         row_reduce<WPR, 1, true>(mx, slots, wave, phase);
         const bool finite = mx[0] < __builtin_inff();
         const float s = mx[0] / 127.0f;
-        float q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          q[i] = finite && s > 0.f ? fminf(fmaxf(rintf(r[i] / s), -128.f), 127.f) : 0.f;
-        R::store_codes(q_out, row, cols, tid, q);
+          r[i] = finite && s > 0.f ? fminf(fmaxf(rintf(r[i] / s), -128.f), 127.f) : 0.f;
+        R::store_codes(q_out, row, cols, tid, r);
         if (tid == 0) s_out[row] = finite ? s : __builtin_nanf("");
       } else {
         R::store(n_out, row, cols, tid, r);
       }
     }
+    if constexpr (AHEAD) res = next_res, y = next_y, gate = next_gate;
   }
 }
 
-// Every workgroup walks rows base, base + step, ... and adds their contributions to the
-// weight (and channel gate) gradients in registers; partial [groups][3][cols] holds one
-// set per row group, which k_norm_grad_sum adds in order.
+// As the forward kernel; the contributions to the weight (and channel gate) gradients are
+// added in registers, and partial [workgroups][3][cols] gets one set per workgroup, which
+// k_norm_grad_sum adds in order.
 template <typename T, int WPR, int NV, bool VEC>
 __global__ void __launch_bounds__(threads_per_wg<WPR>())
     k_block_norm_bwd(BlockNormArgs a, const void* dr, const void* dn, void* dres, void* dy, void* dgate,
                      float* partial) {
   typedef Row<T, 64 * WPR, NV, VEC> R;
+  typedef typename R::Raw Raw;
   constexpr int N = R::N;
   __shared__ float slots[2 * 2 * 16];
   const int wave = threadIdx.x >> 6;
@@ -267,51 +317,57 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>())
 #pragma unroll
   for (int i = 0; i < N; ++i) dw_pre[i] = dw_post[i] = dg_ch[i] = 0.f;
   const int64_t step = int64_t(gridDim.x) * rows_per_wg<WPR>();
-  for (int64_t base = int64_t(blockIdx.x) * rows_per_wg<WPR>(); base < a.rows; base += step) {
-    const int64_t row = base + threadIdx.x / (64 * WPR);
-    if constexpr (rows_per_wg<WPR>() > 1)
-      if (row >= a.rows) break;   // one wave per row: no barrier below
-    float r[N], yv[N], g[N];
-    float rs_y = 1.f, gt = 1.f;
-    R::load(a.res, row, cols, tid, r);
+  const int64_t group = int64_t(blockIdx.x) * rows_per_wg<WPR>() + threadIdx.x / (64 * WPR);
+  const Raw ones = R::fill(Elem<T>::down(1.f));
+  Raw w_post = ones, w_pre = ones, gate = ones, res = ones, y = ones, dnv = ones, drv = R::fill(0);
+  if (a.w_post) w_post = R::fetch(a.w_post, 0, cols, tid);
+  if (a.w_pre) w_pre = R::fetch(a.w_pre, 0, cols, tid);
+  if (a.gate_kind == kGateChannel) gate = R::fetch(a.gate, 0, cols, tid);
+  auto fetch = [&](int64_t row, Raw& res, Raw& y, Raw& dnv, Raw& drv, Raw& gate) {
+    res = R::fetch(a.res, row, cols, tid);
+    if (a.y) y = R::fetch(a.y, row, cols, tid);
+    if (a.w_pre) dnv = R::fetch(dn, row, cols, tid);
+    if (dr) drv = R::fetch(dr, row, cols, tid);
+    if (a.gate_kind == kGateElement) gate = R::fetch(a.gate, row, cols, tid);
+    if (a.gate_kind == kGateToken) gate = R::fill(static_cast<const typename R::S*>(a.gate)[row]);
+  };
+  constexpr bool AHEAD = fetch_ahead<WPR, VEC>();
+  if (AHEAD && group < a.rows) fetch(group, res, y, dnv, drv, gate);
+  for (int64_t row = group; row < a.rows; row += step) {   // (the same trip count for a row's waves)
+    Raw n_res, n_y, n_dn, n_dr, n_gate;
+    if constexpr (AHEAD) {
+      n_res = res, n_y = y, n_dn = dnv, n_dr = drv, n_gate = gate;
+      if (row + step < a.rows) fetch(row + step, n_res, n_y, n_dn, n_dr, n_gate);
+    } else {
+      fetch(row, res, y, dnv, drv, gate);
+    }
+    float r[N], yh[N];
+    float rs_y = 1.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = R::at(res, i);
     if (a.y) {
-      R::load(a.y, row, cols, tid, yv);
       if (a.w_post) {
         float ss[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss[0] += yv[i] * yv[i];
+        for (int i = 0; i < N; ++i) ss[0] += R::at(y, i) * R::at(y, i);
         row_reduce<WPR, 1>(ss, slots, wave, phase);
         rs_y = rstd_of(ss[0], cols, a.eps);
       }
-      if (a.gate_kind == kGateToken) {
-        gt = Elem<T>::up(static_cast<const typename R::S*>(a.gate)[row]);
-      } else if (a.gate_kind != kGateNone) {
-        R::load(a.gate, a.gate_kind == kGateElement ? row : 0, cols, tid, g);
-      }
-      float w[N];
-      if (a.w_post) R::load(a.w_post, 0, cols, tid, w);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        yv[i] *= rs_y;   // yh
-        const float p = a.w_post ? yv[i] * w[i] : yv[i];
-        r[i] += a.alpha * ((a.gate_kind == kGateChannel || a.gate_kind == kGateElement ? g[i] : gt) * p);
+        yh[i] = R::at(y, i) * rs_y;
+        r[i] += a.alpha * (R::at(gate, i) * (yh[i] * R::at(w_post, i)));
       }
     }
     float d[N];
-    if (dr) {
-      R::load(dr, row, cols, tid, d);
-    } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = 0.f;
-    }
+    for (int i = 0; i < N; ++i) d[i] = R::at(drv, i);   // zeros without dr
     if (a.w_pre) {
-      float dnv[N], w[N], red[2] = {0.f, 0.f};
-      R::load(dn, row, cols, tid, dnv);
-      R::load(a.w_pre, 0, cols, tid, w);
+      float red[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         red[0] += r[i] * r[i];
-        red[1] += w[i] * dnv[i] * r[i];
+        red[1] += R::at(w_pre, i) * R::at(dnv, i) * r[i];
       }
       row_reduce<WPR, 2>(red, slots, wave, phase);
       const float rs = rstd_of(red[0], cols, a.eps);
@@ -319,50 +375,61 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>())
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float rh = r[i] * rs;
-        d[i] += rs * (w[i] * dnv[i] - rh * c);
-        dw_pre[i] += dnv[i] * rh;
+        d[i] += rs * (R::at(w_pre, i) * R::at(dnv, i) - rh * c);
+        dw_pre[i] += R::at(dnv, i) * rh;
       }
     }
     R::store(dres, row, cols, tid, d);
     if (a.y) {
-      float w[N], red[2] = {0.f, 0.f};
-      if (a.w_post) R::load(a.w_post, 0, cols, tid, w);
+      float red[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float e = a.alpha * d[i];
-        const float ep = e * (a.w_post ? yv[i] * w[i] : yv[i]);
-        if (a.gate_kind == kGateChannel || a.gate_kind == kGateElement) {
-          d[i] = e * g[i];   // dp
-          if (a.gate_kind == kGateChannel) dg_ch[i] += ep;
-          else g[i] = ep;
-        } else {
-          d[i] = e * gt;
-          red[1] += ep;
-        }
-        if (a.w_post) {
-          red[0] += d[i] * w[i] * yv[i];
-          dw_post[i] += d[i] * yv[i];
-        }
+        r[i] = e * (yh[i] * R::at(w_post, i));   // e p, the gate's gradient before its sum
+        dg_ch[i] += r[i];
+        red[1] += r[i];
+        d[i] = e * R::at(gate, i);               // dp
+        const float dy = d[i] * yh[i];
+        dw_post[i] += dy;
+        red[0] += dy * R::at(w_post, i);
       }
-      if (a.gate_kind == kGateElement) R::store(dgate, row, cols, tid, g);
+      if (a.gate_kind == kGateElement) R::store(dgate, row, cols, tid, r);
       if (a.w_post || a.gate_kind == kGateToken) row_reduce<WPR, 2>(red, slots, wave, phase);
       if (a.gate_kind == kGateToken && tid == 0) static_cast<float*>(dgate)[row] = red[1];
       if (a.w_post) {
         const float c = red[0] / float(cols);
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = rs_y * (d[i] * w[i] - yv[i] * c);
+        for (int i = 0; i < N; ++i) d[i] = rs_y * (d[i] * R::at(w_post, i) - yh[i] * c);
       }
       R::store(dy, row, cols, tid, d);
     }
+    if constexpr (AHEAD) res = n_res, y = n_y, dnv = n_dn, drv = n_dr, gate = n_gate;
   }
-  const int64_t group = int64_t(blockIdx.x) * rows_per_wg<WPR>() + threadIdx.x / (64 * WPR);
-  float* out = partial + group * kGradSlots * cols;
-  if (a.w_pre) R::store_f32(out, cols, tid, dw_pre);
-  if (a.w_post) R::store_f32(out + cols, cols, tid, dw_post);
-  if (a.gate_kind == kGateChannel) R::store_f32(out + 2 * cols, cols, tid, dg_ch);
+  // one set of sums per workgroup: its row groups' sums join through LDS in group order
+  float* out = partial + int64_t(blockIdx.x) * kGradSlots * cols;
+  auto put = [&](float* to, const float v[N]) {
+    if constexpr (rows_per_wg<WPR>() == 1) {
+      R::store_f32(to, cols, tid, v);
+    } else {
+      constexpr int G = rows_per_wg<WPR>();
+      __shared__ __align__(16) float sums[G][64 * WPR * N];
+      R::store_f32(sums[threadIdx.x / (64 * WPR)], cols, tid, v);
+      __syncthreads();
+      for (int c = threadIdx.x; c < cols; c += threads_per_wg<WPR>()) {
+        float acc = sums[0][c];
+#pragma unroll
+        for (int k = 1; k < G; ++k) acc += sums[k][c];
+        to[c] = acc;
+      }
+      __syncthreads();
+    }
+  };
+  if (a.w_pre) put(out, dw_pre);
+  if (a.w_post) put(out + cols, dw_post);
+  if (a.gate_kind == kGateChannel) put(out + 2 * cols, dg_ch);
 }
 
-// out[slot][c] = sum over the row groups of partial[group][slot][c]: a workgroup owns 64
+// out[slot][c] = sum over the workgroups of partial[group][slot][c]: a workgroup owns 64
 // columns of one slot, its 16 waves take every 16th group, and wave 0 adds the 16 sums in
 // wave order (a fixed order: equal inputs give equal bits).
 __global__ void __launch_bounds__(1024) k_norm_grad_sum(const float* __restrict__ partial, int groups, int cols,
@@ -387,34 +454,56 @@ __global__ void __launch_bounds__(1024) k_norm_grad_sum(const float* __restrict_
   }
 }
 
-// Workgroups of the backward pass: each keeps its sums over several rows, so that the
-// partial sums (3 rows of fp32 per row group) stay small beside the rows themselves.
-int bwd_groups(int64_t rows, int rpw) {
-  const int64_t wgs = std::min<int64_t>((rows + rpw - 1) / rpw, 512);
-  return int(wgs);
+// Workgroups of a pass over the rows: as many as are on the chip at once (16 waves per CU in
+// the forward pass, 8 in the backward one, which holds twice as much per thread and writes
+// three partial rows of fp32 per workgroup).
+int64_t pass_wgs(int64_t rows, int wpr, bool backward) {
+  const int rpw = wpr >= 4 ? 1 : 4 / wpr;
+  const int64_t fill = 256 * std::max(1, (backward ? kBwdWaves : 16) / (wpr * rpw));
+  return std::min<int64_t>((rows + rpw - 1) / rpw, fill);
 }
 
-// Rows of up to 512 columns take one wave with one vector of 8 per lane; wider rows two
-// vectors per lane and as many waves as that takes.
-int waves_per_row(int64_t cols) { return cols <= 1024 ? 1 : cols <= 4096 ? 4 : cols <= 8192 ? 8 : 16; }
+// Waves per row: two vectors of 8 columns per lane at most, one where that still leaves few
+// waves (or single columns, which take a register each).
+int waves_per_row(int64_t cols) {
+  const bool vec = cols % 8 == 0;
+  if (cols <= 512 || (vec && cols <= 1024)) return 1;
+  if (cols <= 2048 || (vec && cols <= 4096)) return 4;
+  if (cols <= 4096 || (vec && cols <= 8192)) return 8;
+  return 16;
+}
 
-template <typename T, bool VEC, typename F>
+template <bool VEC, typename F>
 hipError_t with_shape(int64_t cols, F&& f) {
-  if (cols <= 512) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-  if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-  if (cols <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-  if (cols <= 8192) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+  typedef std::integral_constant<int, 1> one;
+  typedef std::integral_constant<int, 2> two;
+  const int w = waves_per_row(cols);
+  const bool nv1 = cols <= int64_t(w) * 512;
+  if (w == 1) {
+    if constexpr (VEC)
+      if (!nv1) return f(one{}, two{});
+    return f(one{}, one{});
+  }
+  if (w == 4) {
+    if constexpr (VEC)
+      if (!nv1) return f(std::integral_constant<int, 4>{}, two{});
+    return f(std::integral_constant<int, 4>{}, one{});
+  }
+  if (w == 8) {
+    if constexpr (VEC) return f(std::integral_constant<int, 8>{}, two{});
+    else return f(std::integral_constant<int, 8>{}, one{});
+  }
+  if constexpr (!VEC)
+    if (nv1) return f(std::integral_constant<int, 16>{}, one{});
+  return f(std::integral_constant<int, 16>{}, two{});
 }
 
 template <typename F>
 hipError_t with_type(int dtype, int64_t cols, F&& f) {
   const bool vec = cols % 8 == 0;
   auto go = [&](auto t, auto v) {
-    typedef decltype(t) T;
     constexpr bool VEC = decltype(v)::value;
-    return with_shape<T, VEC>(cols, [&](auto wpr, auto nv) { return f(t, v, wpr, nv); });
+    return with_shape<VEC>(cols, [&](auto wpr, auto nv) { return f(t, v, wpr, nv); });
   };
   if (dtype == 0) return vec ? go(NF32{}, std::true_type{}) : go(NF32{}, std::false_type{});
   if (dtype == 1) return vec ? go(NF16{}, std::true_type{}) : go(NF16{}, std::false_type{});
@@ -430,8 +519,7 @@ hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, void* r_out, voi
   return with_type(dtype, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
     typedef decltype(t) T;
     constexpr int WPR = decltype(wpr)::value;
-    constexpr int RPW = rows_per_wg<WPR>();
-    const unsigned grid = unsigned(std::min<int64_t>((a.rows + RPW - 1) / RPW, int64_t(1) << 20));
+    const unsigned grid = unsigned(pass_wgs(a.rows, WPR, false));
     hipLaunchKernelGGL((k_block_norm_fwd<T, WPR, decltype(nv)::value, decltype(v)::value>), dim3(grid),
                        dim3(threads_per_wg<WPR>()), 0, st, a, r_out, n_out, q_out, s_out);
     return hipGetLastError();
@@ -439,9 +527,7 @@ hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, void* r_out, voi
 }
 
 int64_t block_norm_bwd_workspace(int64_t rows, int64_t cols) {
-  const int wpr = waves_per_row(cols);
-  const int rpw = wpr >= 4 ? 1 : 4 / wpr;
-  return int64_t(bwd_groups(rows, rpw)) * rpw * kGradSlots * cols * 4;
+  return pass_wgs(rows, waves_per_row(cols), true) * kGradSlots * cols * 4;
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, const void* dr, const void* dn, void* dres,
@@ -452,8 +538,8 @@ hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, const void* 
     const hipError_t e = with_type(dtype, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
       typedef decltype(t) T;
       constexpr int WPR = decltype(wpr)::value;
-      const int wgs = bwd_groups(a.rows, rows_per_wg<WPR>());
-      groups = wgs * rows_per_wg<WPR>();
+      const int64_t wgs = pass_wgs(a.rows, WPR, true);
+      groups = int(wgs);
       hipLaunchKernelGGL((k_block_norm_bwd<T, WPR, decltype(nv)::value, decltype(v)::value>), dim3(unsigned(wgs)),
                          dim3(threads_per_wg<WPR>()), 0, st, a, dr, dn, dres, dy, dgate, partial);
       return hipGetLastError();
