@@ -621,8 +621,8 @@ Q4_API int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64
  * (the first half of the FFN that moe_int4_ffn_forward computes from INT4 weights).
  *  x        device [t][h]; w_gate, w_up device [i][h]; h_out device [t][i]; dtype Q4_BF16
  *           or Q4_F16 for all of them; products accumulate in fp32.
- *  gu_out   device [t][2][i] or NULL: g and u rounded to dtype, which the backward pass
- *           reads (a serving call passes NULL).
+ *  gu_out   device [t][2][i] fp32 or NULL: g and u, which the backward pass reads (a
+ *           serving call passes NULL).
  * Backward, given dh [t][i]:
  *   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh silu(g)   (rounded to dtype: operands)
  *   dx = dg w_gate + du w_up,   dw_gate = dg^T x,   dw_up = du^T x
@@ -635,10 +635,10 @@ Q4_API int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64
  */
 Q4_API size_t swiglu_linear_workspace_bytes(int64_t t, int64_t h, int64_t i);
 Q4_API int swiglu_linear_forward(const void* x, const void* w_gate, const void* w_up, int64_t t, int64_t h, int64_t i,
-                                 int dtype, void* h_out, void* gu_out, void* workspace, size_t ws_bytes,
+                                 int dtype, void* h_out, float* gu_out, void* workspace, size_t ws_bytes,
                                  hipStream_t stream);
 Q4_API size_t swiglu_linear_backward_workspace_bytes(int64_t t, int64_t h, int64_t i);
-Q4_API int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gu,
+Q4_API int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const float* gu,
                                   int64_t t, int64_t h, int64_t i, int dtype, void* dx, void* dw_gate, void* dw_up,
                                   void* workspace, size_t ws_bytes, hipStream_t stream);
 

@@ -825,11 +825,11 @@ def _swiglu_args(x, w_gate, w_up):
 
 def swiglu_linear_forward(x, w_gate, w_up, save=False):
     """h [t, i] = silu(x w_gate^T) * (x w_up^T) for x [t, h] and weights [i, h] (fp16 or bf16).
-    With ``save`` -> (h, gu): gu [t, 2, i] holds the two products for the backward pass."""
+    With ``save`` -> (h, gu): gu [t, 2, i] holds the two products in fp32 for the backward pass."""
     t, h, i, dev = _swiglu_args(x, w_gate, w_up)
     dtype, device = x.dtype, x.device
     out = torch.empty((t, i), dtype=dtype, device=device)
-    gu = torch.empty((t, 2, i), dtype=dtype, device=device) if save else None
+    gu = torch.empty((t, 2, i), dtype=torch.float32, device=device) if save else None
     nbytes = _lib.swiglu_linear_workspace_bytes(t, h, i)
     ws = _scratch(nbytes, device)
     _call("swiglu_linear_forward", _lib.swiglu_linear_forward, dev, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
@@ -841,7 +841,7 @@ def swiglu_linear_backward(dh, x, w_gate, w_up, gu):
     """Gradients (dx, dw_gate, dw_up) of swiglu_linear_forward for dh [t, i] and the saved gu."""
     t, h, i, dev = _swiglu_args(x, w_gate, w_up)
     _arg(dh, "dh", x.dtype, (t, i), dev)
-    _arg(gu, "gu", x.dtype, (t, 2, i), dev)
+    _arg(gu, "gu", torch.float32, (t, 2, i), dev)
     dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
     nbytes = _lib.swiglu_linear_backward_workspace_bytes(t, h, i)
     ws = _scratch(nbytes, x.device)

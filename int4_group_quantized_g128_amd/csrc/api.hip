@@ -1190,7 +1190,7 @@ size_t swiglu_linear_backward_workspace_bytes(int64_t t, int64_t h, int64_t i) {
 }
 
 int swiglu_linear_forward(const void* x, const void* w_gate, const void* w_up, int64_t t, int64_t h, int64_t i,
-                          int dtype, void* h_out, void* gu_out, void* workspace, size_t ws_bytes, hipStream_t stream) {
+                          int dtype, void* h_out, float* gu_out, void* workspace, size_t ws_bytes, hipStream_t stream) {
   g_last_error.clear();
   Q4_REQUIRE(dtype == Q4_F16 || dtype == Q4_BF16, Q4_ERR_DTYPE, "dtype must be Q4_F16 or Q4_BF16");
   Q4_REQUIRE(swiglu_shape(t, h, i), Q4_ERR_SHAPE, "need 0 <= t <= 2^24, h and i positive multiples of 8 up to 2^20");
@@ -1206,7 +1206,7 @@ int swiglu_linear_forward(const void* x, const void* w_gate, const void* w_up, i
                    "swiglu linear launch");
 }
 
-int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gu,
+int swiglu_linear_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const float* gu,
                            int64_t t, int64_t h, int64_t i, int dtype, void* dx, void* dw_gate, void* dw_up,
                            void* workspace, size_t ws_bytes, hipStream_t stream) {
   g_last_error.clear();

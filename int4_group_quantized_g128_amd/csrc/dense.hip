@@ -56,7 +56,7 @@ struct DenseArgs {
   const float* s_row;       // int8: token scales
   const float* s_col;       // int8: channel scales
   const float* bias;        // int8: or NULL
-  void* gu;                 // swiglu: [M][2][N] products, or NULL
+  float* gu;                // swiglu: [M][2][N] products, or NULL
   void* part;               // ksplit > 1: [ksplit][batches][panels][M][N] fp32 / int32 sums
 };
 
@@ -138,8 +138,8 @@ Q4_DEVICE void finish4(const DenseArgs& g, int z, int m, int n, typename Num<A>:
   if constexpr (EPI == EPI_SWIGLU) {
     if (g.gu) {
       const int64_t at = int64_t(m) * 2 * g.ldc + n;
-      store4(g.gu, g.c_dtype, at, v, count, vec);
-      store4(g.gu, g.c_dtype, at + g.ldc, v2, count, vec);
+      store4(g.gu, 0, at, v, count, vec);
+      store4(g.gu, 0, at + g.ldc, v2, count, vec);
     }
   }
 }
@@ -187,8 +187,8 @@ Q4_DEVICE void finish_pair(const DenseArgs& g, int z, int m, int nb, int q, bool
   if constexpr (EPI == EPI_SWIGLU) {
     if (g.gu) {
       const int64_t at = int64_t(m) * 2 * g.ldc + nb;
-      store_pair(g.gu, g.c_dtype, at, q, v0, v1, in);
-      store_pair(g.gu, g.c_dtype, at + g.ldc, q, w0, w1, in);
+      store_pair(g.gu, 0, at, q, v0, v1, in);
+      store_pair(g.gu, 0, at + g.ldc, q, w0, w1, in);
     }
   }
 }
@@ -724,24 +724,29 @@ __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
 }
 
 // ---------------------------------------------------------------- element-wise kernels
-// dg and du of 8 elements: bound by memory (3 reads, 2 writes of 2 bytes per element).
-// dg and du are rounded to 16 bits: they are matrix-core operands next.
+// dg and du of 8 elements: bound by memory (g, u in fp32 and dh in, dg and du out: 14 bytes
+// per element).  g and u are kept in fp32: rounding them to 16 bits as well made the bf16
+// gradients 1.8 times as far from the 64-bit ones as one rounding of the result does, fp32
+// 1.4 times (dg and du are rounded, being matrix-core operands next).
 template <bool F16>
-__global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu,
+__global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict__ dh, const float* __restrict__ gu,
                                                      int64_t t, int64_t inter, uint16_t* __restrict__ dg,
                                                      uint16_t* __restrict__ du) {
   const int64_t vecs = inter / 8;
   const int64_t step = int64_t(gridDim.x) * 256;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < t * vecs; i += step) {
     const int64_t row = i / vecs, c = (i - row * vecs) * 8;
+    f32x4_t g[2], u[2];
     uint16_t a[8], b[8], d[8];
-    *reinterpret_cast<uint4*>(a) = load16(gu + row * 2 * inter + c);
-    *reinterpret_cast<uint4*>(b) = load16(gu + row * 2 * inter + inter + c);
-    *reinterpret_cast<uint4*>(d) = load16(dh + row * inter + c);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      g[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + c + 4 * j));
+      u[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + inter + c + 4 * j));
+    }
+    *reinterpret_cast<uint4*>(d) = load16_stream(dh + row * inter + c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float gv = F16 ? f16_bits_to_f32(a[e]) : bf16_to_f32(a[e]);
-      const float uv = F16 ? f16_bits_to_f32(b[e]) : bf16_to_f32(b[e]);
+      const float gv = g[e / 4][e % 4], uv = u[e / 4][e % 4];
       const float dv = F16 ? f16_bits_to_f32(d[e]) : bf16_to_f32(d[e]);
       const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-gv));
       a[e] = to16(dv * uv * sig * (1.0f + gv * (1.0f - sig)), F16 ? 1 : 2);
@@ -908,7 +913,7 @@ int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i) {
 }
 
 hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, int64_t t, int64_t h, int64_t i, int f16,
-                                void* out, void* gu, void* work, hipStream_t st) {
+                                void* out, float* gu, void* work, hipStream_t st) {
   DenseArgs g{};
   g.a[0] = g.a[1] = x;
   g.b[0] = wg, g.b[1] = wu;
@@ -935,7 +940,7 @@ int64_t swiglu_linear_bwd_workspace(int64_t t, int64_t h, int64_t i) {
   return 2 * align256(t * i * 2) + std::max(dx, dw);
 }
 
-hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* gu,
+hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const float* gu,
                                     int64_t t, int64_t h, int64_t i, int f16, void* dx, void* dwg, void* dwu,
                                     void* work, hipStream_t st) {
   uint16_t* dg = static_cast<uint16_t*>(work);
@@ -944,9 +949,8 @@ hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* w
   if (t > 0) {
     const unsigned grid = unsigned(std::min<int64_t>(ceil_div(t * (i / 8), 256), 4096));
     const auto* d = static_cast<const uint16_t*>(dh);
-    const auto* p = static_cast<const uint16_t*>(gu);
-    if (f16) hipLaunchKernelGGL(k_swiglu_grad<true>, dim3(grid), dim3(256), 0, st, d, p, t, i, dg, du);
-    else hipLaunchKernelGGL(k_swiglu_grad<false>, dim3(grid), dim3(256), 0, st, d, p, t, i, dg, du);
+    if (f16) hipLaunchKernelGGL(k_swiglu_grad<true>, dim3(grid), dim3(256), 0, st, d, gu, t, i, dg, du);
+    else hipLaunchKernelGGL(k_swiglu_grad<false>, dim3(grid), dim3(256), 0, st, d, gu, t, i, dg, du);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

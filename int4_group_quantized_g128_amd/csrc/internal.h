@@ -185,12 +185,12 @@ hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k,
 int64_t int8_linear_workspace(int64_t t, int64_t k, int64_t n);
 hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* wq, const float* ws,
                               int64_t n, const float* bias, int y_dtype, void* y, void* work, hipStream_t st);
-// h = silu(x wg^T) * (x wu^T); gu (optional) [t][2][i] the two products.  f16: fp16, else bf16.
+// h = silu(x wg^T) * (x wu^T); gu (optional) fp32 [t][2][i] the two products.  f16: fp16, else bf16.
 int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i);
 hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, int64_t t, int64_t h, int64_t i, int f16,
-                                void* out, void* gu, void* work, hipStream_t st);
+                                void* out, float* gu, void* work, hipStream_t st);
 int64_t swiglu_linear_bwd_workspace(int64_t t, int64_t h, int64_t i);
-hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const void* gu,
+hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const float* gu,
                                     int64_t t, int64_t h, int64_t i, int f16, void* dx, void* dwg, void* dwu,
                                     void* work, hipStream_t st);
 

@@ -146,8 +146,8 @@ def test_swiglu_linear_forward(lib, t, h, i, dt):
     g, u = xd @ gd.T, xd @ ud.T
     dg, du = 2 * h * U * (xd.abs() @ gd.abs().T), 2 * h * U * (xd.abs() @ ud.abs().T)
     hs = half_step(dt)
-    within(gu[:, 0], g, dg + hs * (g.abs() + dg) + tiny(dt), "g")
-    within(gu[:, 1], u, du + hs * (u.abs() + du) + tiny(dt), "u")
+    within(gu[:, 0], g, dg, "g")
+    within(gu[:, 1], u, du, "u")
     sig = torch.sigmoid(g)
     ref = g * sig * u
     # |silu'| < 1.1; e^-g through exp2: (|g| + 4) roundings, then 4 more operations
@@ -166,7 +166,7 @@ def swiglu_grads(dh, x, wg, wu, g, u):
 @pytest.mark.parametrize("t,h,i", SWIGLU_SHAPES)
 def test_swiglu_linear_backward(lib, t, h, i, dt):
     x, wg, wu, dh = swiglu_inputs(t, h, i, dt, 1)
-    gu = torch.stack((randn(gen_of(7), t, i), randn(gen_of(8), t, i)), 1).to(dt)
+    gu = torch.stack((randn(gen_of(7), t, i), randn(gen_of(8), t, i)), 1)
     dx, dwg, dwu = lib.swiglu_linear_backward(dh, x, wg, wu, gu)
     xd, gd, ud, d = x.double(), wg.double(), wu.double(), dh.double()
     g, u = gu[:, 0].double(), gu[:, 1].double()
@@ -186,9 +186,8 @@ def test_swiglu_linear_backward(lib, t, h, i, dt):
 @pytest.mark.parametrize("dt", TYPES)
 def test_swiglu_linear_gradient_against_differences(lib, dt):
     """<grad, d> against (L(p + e d) - L(p - e d)) / 2e of the 64-bit loss L = sum dh h, for a
-    direction in each of x, w_gate and w_up.  The gradients carry roundings of g, u, dg, du
-    and of the result: 3 half steps (and the curvature in g, at most 1.6 |dg| per |g|),
-    taken at full size against the absolute values of the sum."""
+    direction in each of x, w_gate and w_up.  The gradients carry roundings of dg, du and of
+    the result: 2 half steps, taken at full size against the absolute values of the sum."""
     t, h, i = 70, 136, 72
     x, wg, wu, dh = swiglu_inputs(t, h, i, dt, 2)
     _, gu = lib.swiglu_linear_forward(x, wg, wu, save=True)
@@ -209,7 +208,7 @@ def test_swiglu_linear_gradient_against_differences(lib, dt):
         plus, minus = [list(p), list(p)]
         plus[j], minus[j] = p[j] + e * v, p[j] - e * v
         diff = (loss(*plus) - loss(*minus)) / (2 * e)
-        tol = 5 * half_step(dt) * mags[j].sum() + 1e-6 * mags[j].sum()
+        tol = 2.1 * half_step(dt) * mags[j].sum() + 1e-6 * mags[j].sum()
         assert abs((grads[j] * v).sum() - diff) <= tol
 
 
@@ -506,7 +505,7 @@ def test_int8_block(lib, t, dt):
 def test_training_block(lib, dt):
     """Norm -> gated projection -> down projection -> norm, gate, residual scale, with every
     gradient, against 64-bit automatic differentiation.  Each stored tensor on the way (n, h,
-    g, u, y, dy, dh, dg, du, dn and the result) is rounded once: at most 11 half steps, and
+    y, dy, dh, dg, du, dn and the result) is rounded once: at most 9 half steps, and
     as much again for what the norms' Jacobians (norm at most 2 here) make of them."""
     t, c, i = 130, 264, 520
     g = gen_of(3)
@@ -533,7 +532,7 @@ def test_training_block(lib, dt):
     yy = (gg * torch.sigmoid(gg) * (nn @ W.T)) @ wd.double().T
     rr = R + 0.5 * K * (yy * rstd64(yy, 1e-6) * B)
     rr.backward(dr.double())
-    tol = 22 * half_step(dt)
+    tol = 18 * half_step(dt)
     for got, ref in ((r, rr.detach()), (g1["res"], R.grad), (g1["w_pre"], A.grad), (dwg, G.grad), (dwu, W.grad),
                      (g2["w_post"], B.grad), (g2["gate"], K.grad)):
         assert (got.double() - ref).norm() <= tol * ref.norm()
