@@ -7,6 +7,7 @@ kernels; there is no fallback: if the library is missing, importing this module
 raises.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -744,6 +745,19 @@ _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
+# Workspace sizes depend on the sizes alone (a library call per size, not per use).
+_int8_linear_ws = functools.lru_cache(4096)(_lib.int8_linear_workspace_bytes)
+_swiglu_linear_ws = functools.lru_cache(4096)(_lib.swiglu_linear_workspace_bytes)
+_swiglu_linear_bwd_ws = functools.lru_cache(4096)(_lib.swiglu_linear_backward_workspace_bytes)
+
+
+def _first(t, dtypes, name):
+    """A call's first tensor: 2-D, contiguous, on a GPU; -> (its shape, its GPU)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous() and t.is_cuda):
+        _need(t, dtypes, name, 2)
+    return t.shape, t.get_device()
+
+
 def _arg(t, name, dtype, shape, dev):
     """t must be a contiguous tensor of this dtype and shape on GPU `dev`."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
@@ -791,11 +805,8 @@ def quantize_int8_channel(w, flags=None):
 def int8_linear_forward(q, s, w_q, w_s, bias=None, out_dtype=torch.bfloat16):
     """y [t, n] = (q w_q^T) * (s[:, None] * w_s) (+ bias) for token codes q [t, k] with scales
     s [t] and weight codes w_q [n, k] with scales w_s [n]; exact INT32 sums, y of out_dtype."""
-    _need(q, torch.int8, "q", 2)
-    _need(w_q, torch.int8, "w_q", 2)
-    t, k = q.shape
-    n = w_q.shape[0]
-    dev = q.get_device()
+    (t, k), dev = _first(q, (torch.int8,), "q")
+    n = _first(w_q, (torch.int8,), "w_q")[0][0]
     _arg(w_q, "w_q", torch.int8, (n, k), dev)
     _arg(s, "s", torch.float32, (t,), dev)
     _arg(w_s, "w_s", torch.float32, (n,), dev)
@@ -805,7 +816,7 @@ def int8_linear_forward(q, s, w_q, w_s, bias=None, out_dtype=torch.bfloat16):
         raise TypeError(f"out_dtype {out_dtype} is not fp32, fp16 or bf16")
     device = q.device
     y = torch.empty((t, n), dtype=out_dtype, device=device)
-    nbytes = _lib.int8_linear_workspace_bytes(t, k, n)
+    nbytes = _int8_linear_ws(t, k, n)
     ws = _scratch(nbytes, device)
     _call("int8_linear_forward", _lib.int8_linear_forward, dev, q.data_ptr(), s.data_ptr(), t, k, w_q.data_ptr(),
           w_s.data_ptr(), n, _dp(bias), _DT[out_dtype], y.data_ptr(), _dp(ws), nbytes)
@@ -813,11 +824,8 @@ def int8_linear_forward(q, s, w_q, w_s, bias=None, out_dtype=torch.bfloat16):
 
 
 def _swiglu_args(x, w_gate, w_up):
-    _need(x, _16BIT, "x", 2)
-    _need(w_gate, x.dtype, "w_gate", 2)
-    t, h = x.shape
-    i = w_gate.shape[0]
-    dev = x.get_device()
+    (t, h), dev = _first(x, _16BIT, "x")
+    i = _first(w_gate, _16BIT, "w_gate")[0][0]
     _arg(w_gate, "w_gate", x.dtype, (i, h), dev)
     _arg(w_up, "w_up", x.dtype, (i, h), dev)
     return t, h, i, dev
@@ -830,7 +838,7 @@ def swiglu_linear_forward(x, w_gate, w_up, save=False):
     dtype, device = x.dtype, x.device
     out = torch.empty((t, i), dtype=dtype, device=device)
     gu = torch.empty((t, 2, i), dtype=torch.float32, device=device) if save else None
-    nbytes = _lib.swiglu_linear_workspace_bytes(t, h, i)
+    nbytes = _swiglu_linear_ws(t, h, i)
     ws = _scratch(nbytes, device)
     _call("swiglu_linear_forward", _lib.swiglu_linear_forward, dev, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
           t, h, i, _DT[dtype], out.data_ptr(), _dp(gu), _dp(ws), nbytes)
@@ -843,7 +851,7 @@ def swiglu_linear_backward(dh, x, w_gate, w_up, gu):
     _arg(dh, "dh", x.dtype, (t, i), dev)
     _arg(gu, "gu", torch.float32, (t, 2, i), dev)
     dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
-    nbytes = _lib.swiglu_linear_backward_workspace_bytes(t, h, i)
+    nbytes = _swiglu_linear_bwd_ws(t, h, i)
     ws = _scratch(nbytes, x.device)
     _call("swiglu_linear_backward", _lib.swiglu_linear_backward, dev, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
           w_up.data_ptr(), gu.data_ptr(), t, h, i, _DT[x.dtype], dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
@@ -852,8 +860,8 @@ def swiglu_linear_backward(dh, x, w_gate, w_up, gu):
 
 
 def _norm_desc(res, y, w_post, gate, alpha, w_pre, eps):
-    _need(res, _FLOATS, "res", 2)
-    dtype, shape, dev = res.dtype, res.shape, res.get_device()
+    shape, dev = _first(res, _FLOATS, "res")
+    dtype = res.dtype
     rows, cols = shape
     if y is None and w_pre is None:
         raise ValueError("y or w_pre is required")
