@@ -793,22 +793,31 @@ struct Plan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The products by how their panels lie, which decides what a step costs.
+enum Kind { NT = 0 /* forward, KC x KC */, DX = 1 /* KC x MC */, DW = 2 /* MC x MC */ };
+
 // Estimated time (us) of a product of `steps` 128-byte K steps with square tiles of `bm` and
-// K in `ks` slices.  Per tile size: workgroups a CU holds, time of a step when it is alone
-// on its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
-// workgroup), time of a workgroup's start and end.  The figures are fitted to 75 shapes of
-// both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three tiles and
-// up to 8 splits: the plan below then lies within 2 % of the fastest of them on every one
-// (a rule that only counted workgroups lost up to 70 %).
-double plan_us(int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
+// K in `ks` slices.  Per kind and tile size: time of a step when the workgroup is alone on
+// its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
+// workgroup), time of a workgroup's start and end.  The forward figures are fitted to 75
+// shapes of both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three
+// tiles and up to 8 splits: the plan below then lies within 2 % of the fastest of them on
+// every one (a rule that only counted workgroups lost up to 70 %).  The backward figures are
+// fitted to 6 shapes with 15 plans each (64 to 2048 tokens; rms error of an estimate 12 % for
+// dx, 7 % for dW).
+double plan_us(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
-  static const int held[3] = {3, 2, 1};
-  static const double alone[3] = {0.27, 0.55, 0.62}, full[3] = {0.21, 0.45, 1.23}, ends[3] = {1.9, 8.0, 4.0};
+  static const int held[3] = {3, 2, 1};   // workgroups a CU holds
+  static const double alone[3][3] = {{0.27, 0.55, 0.62}, {0.35, 0.66, 1.27}, {0.17, 0.39, 1.53}};
+  static const double full[3][3] = {{0.21, 0.45, 1.23}, {0.22, 0.65, 1.27}, {0.20, 0.54, 1.53}};
+  static const double ends[3][3] = {{1.9, 8.0, 4.0}, {2.9, 5.1, 13.5}, {2.0, 4.1, 9.3}};
   const int64_t per = ceil_div(steps, ks);
   const int64_t wgs = ceil_div(m, bm) * ceil_div(n * panels, bm) * batches * ceil_div(steps, per);
   const int64_t rounds = ceil_div(wgs, 256 * held[t]);
   const int64_t last = std::min<int64_t>(held[t], ceil_div(wgs - (rounds - 1) * 256 * held[t], 256));
-  const auto slice = [&](int64_t on_cu) { return ends[t] + per * std::max(alone[t], full[t] * on_cu); };
+  const auto slice = [&](int64_t on_cu) {
+    return ends[kind][t] + per * std::max(alone[kind][t], full[kind][t] * on_cu);
+  };
   double us = (rounds - 1) * slice(held[t]) + slice(last);
   // the join: a launch, a chain of reads, and the slices' bytes at 4.5 TB/s
   if (ks > 1) us += 2.9 + 0.5 * ks + double(ks) * m * n * panels * batches * 4 / 4.5e6;
@@ -816,14 +825,14 @@ double plan_us(int64_t m, int64_t n, int panels, int64_t steps, int batches, int
 }
 
 // Tile and K split with the least estimated time.
-Plan plan_of(int64_t m, int64_t n, int panels, int64_t steps, int batches) {
+Plan plan_of(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches) {
   Plan best{64, 64, 1};
   if (steps == 0) return best;   // no tokens: the weight gradients are zero
-  double us = plan_us(m, n, panels, steps, batches, 64, 1);
+  double us = plan_us(kind, m, n, panels, steps, batches, 64, 1);
   for (const int bm : {64, 128, 256})
     for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (ks > 1 && steps / ks < 2) break;
-      const double u = plan_us(m, n, panels, steps, batches, bm, ks);
+      const double u = plan_us(kind, m, n, panels, steps, batches, bm, ks);
       if (u < us) us = u, best = Plan{bm, bm, int(ceil_div(steps, ceil_div(steps, ks)))};
     }
   return best;
@@ -885,7 +894,7 @@ hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k,
 
 int64_t int8_linear_workspace(int64_t t, int64_t k, int64_t n) {
   if (t == 0 || few_rows(t)) return 0;
-  return part_bytes(plan_of(t, n, 1, ceil_div(k, kStepBytes), 1), t, n, 1, 1);
+  return part_bytes(plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), t, n, 1, 1);
 }
 
 hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* wq, const float* ws,
@@ -904,12 +913,12 @@ hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_
   g.bias = bias;
   g.part = work;
   if (few_rows(t)) return launch_rows<Act::I8, EPI_INT8>(g, st);
-  return launch_tiles<Act::I8, false, false, EPI_INT8>(g, plan_of(t, n, 1, ceil_div(k, kStepBytes), 1), st);
+  return launch_tiles<Act::I8, false, false, EPI_INT8>(g, plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), st);
 }
 
 int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i) {
   if (t == 0 || few_rows(t)) return 0;
-  return part_bytes(plan_of(t, i, 2, ceil_div(h, 64), 1), t, i, 2, 1);
+  return part_bytes(plan_of(NT, t, i, 2, ceil_div(h, 64), 1), t, i, 2, 1);
 }
 
 hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, int64_t t, int64_t h, int64_t i, int f16,
@@ -927,7 +936,7 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
   g.part = work;
   if (few_rows(t))
     return f16 ? launch_rows<Act::F16, EPI_SWIGLU>(g, st) : launch_rows<Act::BF16, EPI_SWIGLU>(g, st);
-  const Plan p = plan_of(t, i, 2, ceil_div(h, 64), 1);
+  const Plan p = plan_of(NT, t, i, 2, ceil_div(h, 64), 1);
   return f16 ? launch_tiles<Act::F16, false, false, EPI_SWIGLU>(g, p, st)
              : launch_tiles<Act::BF16, false, false, EPI_SWIGLU>(g, p, st);
 }
@@ -935,8 +944,8 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
 // Workspace: dg and du [t][i] each, then the K slices of whichever product splits K.
 int64_t swiglu_linear_bwd_workspace(int64_t t, int64_t h, int64_t i) {
   if (t == 0) return 0;
-  const int64_t dx = part_bytes(plan_of(t, h, 1, 2 * ceil_div(i, 64), 1), t, h, 1, 1);
-  const int64_t dw = part_bytes(plan_of(i, h, 1, ceil_div(t, 64), 2), i, h, 1, 2);
+  const int64_t dx = part_bytes(plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1), t, h, 1, 1);
+  const int64_t dw = part_bytes(plan_of(DW, i, h, 1, ceil_div(t, 64), 2), i, h, 1, 2);
   return 2 * align256(t * i * 2) + std::max(dx, dw);
 }
 
@@ -967,7 +976,7 @@ hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* w
     g.M = int32_t(t), g.K = int32_t(i);
     g.batches = 1;
     g.c[0] = g.c[1] = dx;
-    const Plan p = plan_of(t, h, 1, 2 * ceil_div(i, 64), 1);
+    const Plan p = plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1);
     const hipError_t e = f16 ? launch_tiles<Act::F16, false, true, EPI_STORE>(g, p, st)
                              : launch_tiles<Act::BF16, false, true, EPI_STORE>(g, p, st);
     if (e != hipSuccess) return e;
@@ -979,7 +988,7 @@ hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* w
   g.M = int32_t(i), g.K = int32_t(t);
   g.batches = 2;
   g.c[0] = dwg, g.c[1] = dwu;
-  const Plan p = plan_of(i, h, 1, ceil_div(t, 64), 2);
+  const Plan p = plan_of(DW, i, h, 1, ceil_div(t, 64), 2);
   return f16 ? launch_tiles<Act::F16, true, true, EPI_STORE>(g, p, st)
              : launch_tiles<Act::BF16, true, true, EPI_STORE>(g, p, st);
 }
