@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
 // reading); the 8 waves of a workgroup own NF fragments' rows, take the 128-byte K steps in
 // turn and feed the matrix core straight from global memory (16 bytes per lane, two loads
 // cover a step's whole lines), four steps in flight, then add their sums through LDS in wave
-// order.  2048 / 8192 gated projection, one row: 14.5 us, 4.6 TB/s.
+// order.  2048 / 8192 gated projection, one row: 14.0 us, 4.8 TB/s
+// (non-temporal weight loads: 14.6; the second load of a line then misses again).
 template <Act A, int EPI, int W, int NF>
 __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
   typedef Num<A> T;
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
         const int64_t at = int64_t(s + u * W) * kStepBytes + h * 64;
 #pragma unroll
         for (int f = 0; f < NF; ++f)
-          w[u][h][f] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp[f] + at));
+          w[u][h][f] = *reinterpret_cast<const u32x4_t*>(wp[f] + at);
         x[u][h] = *reinterpret_cast<const u32x4_t*>(xp + at);
       }
 #pragma unroll
