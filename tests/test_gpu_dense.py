@@ -648,3 +648,161 @@ def test_binding_refusals(lib):
         lib.block_norm_backward(x, None, x, w_pre=wv)
     with pytest.raises(lib.Q4Error):
         lib.block_norm_forward(x, w_pre=wv, eps=0.0)
+
+
+# ------------------------------------------------------------------ buffers
+class Guarded:
+    """Buffers between filled guard regions; check() finds a write outside any of them."""
+    PAD = 4096
+
+    def __init__(self):
+        self.bufs = []
+
+    def new(self, *shape, dtype):
+        n = 1
+        for d in shape:
+            n *= d
+        nbytes = n * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((nbytes + 2 * self.PAD,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.bufs.append((raw, nbytes))
+        return raw[self.PAD:self.PAD + nbytes].view(dtype).view(*shape)
+
+    def check(self):
+        for raw, nbytes in self.bufs:
+            assert (raw[:self.PAD] == 0xA5).all() and (raw[self.PAD + nbytes:] == 0xA5).all()
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("t,k,n", [(5, 48, 33), (70, 1040, 1001), (333, 272, 130), (3500, 80, 4101)])
+def test_int8_linear_writes_only_its_output(lib, t, k, n):
+    r = lib._lib.raw
+    g = gen_of(t)
+    q, wq = codes(g, t, k), codes(g, n, k)
+    s, ws = torch.rand(t, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    for dt in ALL_TYPES:
+        b = Guarded()
+        y = b.new(t, n, dtype=dt)
+        nbytes = r.int8_linear_workspace_bytes(t, k, n)
+        work = b.new(nbytes, dtype=torch.uint8) if nbytes else None
+        assert r.int8_linear_forward(ptr(q), ptr(s), t, k, ptr(wq), ptr(ws), n, None, lib._lib._DT[dt], ptr(y),
+                                     ptr(work), nbytes, stream()) == 0
+        b.check()
+        assert torch.equal(y, lib.int8_linear_forward(q, s, wq, ws, out_dtype=dt))
+
+
+@pytest.mark.parametrize("t,h,i", [(5, 40, 24), (70, 1000, 136), (300, 264, 520), (1300, 72, 4360), (200, 2568, 2560)])
+def test_swiglu_linear_writes_only_its_outputs(lib, t, h, i):
+    r, dt = lib._lib.raw, torch.bfloat16
+    code = lib._lib._DT[dt]
+    x, wg, wu, dh = swiglu_inputs(t, h, i, dt, 4)
+    b = Guarded()
+    out, gu = b.new(t, i, dtype=dt), b.new(t, 2, i, dtype=torch.float32)
+    nbytes = r.swiglu_linear_workspace_bytes(t, h, i)
+    work = b.new(nbytes, dtype=torch.uint8) if nbytes else None
+    assert r.swiglu_linear_forward(ptr(x), ptr(wg), ptr(wu), t, h, i, code, ptr(out), ptr(gu), ptr(work), nbytes,
+                                   stream()) == 0
+    dx, dwg, dwu = b.new(t, h, dtype=dt), b.new(i, h, dtype=dt), b.new(i, h, dtype=dt)
+    nbytes = r.swiglu_linear_backward_workspace_bytes(t, h, i)
+    work = b.new(nbytes, dtype=torch.uint8)
+    assert r.swiglu_linear_backward(ptr(dh), ptr(x), ptr(wg), ptr(wu), ptr(gu), t, h, i, code, ptr(dx), ptr(dwg),
+                                    ptr(dwu), ptr(work), nbytes, stream()) == 0
+    b.check()
+    ref, gu_ref = lib.swiglu_linear_forward(x, wg, wu, save=True)
+    assert torch.equal(out, ref) and torch.equal(gu, gu_ref)
+    for a, c in zip((dx, dwg, dwu), lib.swiglu_linear_backward(dh, x, wg, wu, gu)):
+        assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("t,c", [(3, 7), (5, 1000), (70, 1001), (33, 4104), (9, 9000)])
+def test_block_norm_writes_only_its_outputs(lib, t, c):
+    import ctypes
+    L = lib._lib
+    for dt in ALL_TYPES:
+        kw = norm_inputs(t, c, dt, "channel", 8)
+        d = L._norm_desc(kw["res"], kw["y"], kw["w_post"], kw["gate"], 0.5, kw["w_pre"], 1e-6)
+        b = Guarded()
+        rr, n, q, s = b.new(t, c, dtype=dt), b.new(t, c, dtype=dt), b.new(t, c, dtype=torch.int8), b.new(t, dtype=torch.float32)
+        assert L.raw.block_norm_forward(ctypes.byref(d), ptr(rr), ptr(n), None, None, stream()) == 0
+        assert L.raw.block_norm_forward(ctypes.byref(d), ptr(rr), None, ptr(q), ptr(s), stream()) == 0
+        dres, dy = b.new(t, c, dtype=dt), b.new(t, c, dtype=dt)
+        dwo, dwi, dg = (b.new(c, dtype=torch.float32) for _ in range(3))
+        nbytes = L.raw.block_norm_workspace_bytes(ctypes.byref(d))
+        work = b.new(nbytes, dtype=torch.uint8)
+        assert L.raw.block_norm_backward(ctypes.byref(d), ptr(kw["y"]), ptr(kw["res"]), ptr(dres), ptr(dy), ptr(dwo),
+                                         ptr(dg), ptr(dwi), ptr(work), nbytes, stream()) == 0
+        b.check()
+        got = lib.block_norm_backward(kw["y"], kw["res"], alpha=0.5, **kw)
+        for a, name in ((dres, "res"), (dy, "y"), (dwo, "w_post"), (dwi, "w_pre"), (dg, "gate")):
+            assert torch.equal(a, got[name]), name
+
+
+def test_two_streams_at_once(lib):
+    """The same operators on two streams with work of their own in flight together."""
+    x, wg, wu, dh = swiglu_inputs(300, 1000, 520, torch.bfloat16, 6)
+    kw = norm_inputs(700, 2048, torch.bfloat16, "channel")
+
+    def work():
+        h, gu = lib.swiglu_linear_forward(x, wg, wu, save=True)
+        g = lib.block_norm_backward(kw["y"], kw["res"], **kw)
+        return (h,) + lib.swiglu_linear_backward(dh, x, wg, wu, gu) + tuple(g[k] for k in sorted(g))
+
+    ref = work()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(work())
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, ref))
+
+
+def test_offsets_past_32_bits(lib):
+    """Outputs of more than 2^31 elements: the last rows against a call on them alone."""
+    bf = torch.bfloat16
+    g = gen_of(12)
+    t, n, tail = 200000, 12288, 100
+    q, wq = codes(g, t, 16), codes(g, n, 16)
+    s, ws = torch.rand(t, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    y = lib.int8_linear_forward(q, s, wq, ws)
+    assert torch.equal(y[-tail:], lib.int8_linear_forward(q[-tail:].contiguous(), s[-tail:].contiguous(), wq, ws))
+    del y
+    t, h, i = 150000, 8, 8192
+    x, wg, wu = randn(g, t, h).to(bf), randn(g, i, h).to(bf), randn(g, i, h).to(bf)
+    out, gu = lib.swiglu_linear_forward(x, wg, wu, save=True)
+    xt = x[-tail:].double()
+    gd, ud = xt @ wg.double().T, xt @ wu.double().T
+    within(gu[-tail:, 0], gd, 2 * h * U * (xt.abs() @ wg.double().abs().T), "g")
+    within(gu[-tail:, 1], ud, 2 * h * U * (xt.abs() @ wu.double().abs().T), "u")
+    dx, dwg, dwu = lib.swiglu_linear_backward(out, x, wg, wu, gu)
+    dh = out[-tail:].double()
+    dg, du, rx, _, _ = swiglu_grads(dh, xt, wg.double(), wu.double(), gu[-tail:, 0].double(), gu[-tail:, 1].double())
+    hs = half_step(bf)
+    ag, au = dg.abs() @ wg.double().abs(), du.abs() @ wu.double().abs()
+    u_abs, g_abs = gu[-tail:, 1].double().abs(), gu[-tail:, 0].double().abs()
+    # dg, du: 32 fp32 roundings on terms up to |dh u| (1 + |g|), one to bf16; the sums; the result
+    tol = (1 + 1e-3) * hs * (ag + au) + 32 * U * (((dh.abs() * u_abs * (1 + g_abs)) @ wg.double().abs())
+                                                  + ((dh.abs() * g_abs) @ wu.double().abs())) \
+        + 5 * i * U * (ag + au)
+    within(dx[-tail:], rx, tol + hs * (rx.abs() + tol), "dx")
+    del out, gu, dx, dwg, dwu
+    t, c = 300000, 8192
+    res = torch.zeros(t, c, dtype=bf, device="cuda")
+    res[-tail:] = randn(g, tail, c).to(bf)
+    w = torch.ones(c, dtype=bf, device="cuda")
+    last = res[-tail:].contiguous()
+    want, n_want = lib.block_norm_forward(last, y=last, w_pre=w, w_post=w)
+    got, n_got = lib.block_norm_forward(res, y=res, w_pre=w, w_post=w)
+    assert torch.equal(got[-tail:], want) and torch.equal(n_got[-tail:], n_want)
+    gb = lib.block_norm_backward(got, n_got, res, y=res, w_pre=w, w_post=w)
+    ref = lib.block_norm_backward(want, n_want, last, y=last, w_pre=w, w_post=w)
+    assert torch.equal(gb["res"][-tail:], ref["res"]) and torch.equal(gb["y"][-tail:], ref["y"])
