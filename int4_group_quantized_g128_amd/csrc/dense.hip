@@ -144,96 +144,9 @@ Q4_DEVICE void finish4(const DenseArgs& g, int z, int m, int n, typename Num<A>:
   }
 }
 
-// Stores row values of two adjacent 16-column blocks, columns 4 q .. 4 q + 3 of each in
-// quarter q = lane / 16: 16-bit values are first swapped between neighbouring quarters so
-// that each lane holds 8 consecutive columns, i.e. whole 16-byte stores and 64-byte row
-// segments (8-byte stores ran the 2048 x 2048 x 16384 INT8 product at 103 us).
-Q4_DEVICE void store_pair(void* c, int dtype, int64_t at, int q, f32x4_t y0, f32x4_t y1, bool in) {
-  if (dtype == 0) {
-    if (in) {
-      float* p = static_cast<float*>(c) + at + 4 * q;
-      *reinterpret_cast<f32x4_t*>(p) = y0;
-      *reinterpret_cast<f32x4_t*>(p + 16) = y1;
-    }
-  } else {
-    u32x4_t o;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint32_t a = to16(y0[2 * w], dtype) | uint32_t(to16(y0[2 * w + 1], dtype)) << 16;
-      const uint32_t b = to16(y1[2 * w], dtype) | uint32_t(to16(y1[2 * w + 1], dtype)) << 16;
-      // odd quarters of a <-> even quarters of b
-      const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-      o[w] = r[0];
-      o[2 + w] = r[1];
-    }
-    if (in) *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c) + at + 16 * (q & 1) + 8 * (q >> 1)) = o;
-  }
-}
-
-// Results of row m in the adjacent blocks nb and nb + 16 (the wave's 16 rows together: every
-// lane calls).  `whole`: both blocks inside the matrix, rows of whole 16-byte stores.
-template <Act A, int EPI>
-Q4_DEVICE void finish_pair(const DenseArgs& g, int z, int m, int nb, int q, bool whole, typename Num<A>::acc_t v0,
-                           typename Num<A>::acc_t v1, typename Num<A>::acc_t w0, typename Num<A>::acc_t w1, float sm,
-                           const ColScales& cs0, const ColScales& cs1) {
-  if (!whole) {
-    finish4<A, EPI>(g, z, m, nb + 4 * q, v0, w0, sm, cs0);
-    finish4<A, EPI>(g, z, m, nb + 16 + 4 * q, v1, w1, sm, cs1);
-    return;
-  }
-  const bool in = m < g.M;
-  store_pair(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + nb, q, result4<A, EPI>(v0, w0, sm, cs0),
-             result4<A, EPI>(v1, w1, sm, cs1), in);
-  if constexpr (EPI == EPI_SWIGLU) {
-    if (g.gu) {
-      const int64_t at = int64_t(m) * 2 * g.ldc + nb;
-      store_pair(g.gu, 0, at, q, v0, v1, in);
-      store_pair(g.gu, 0, at + g.ldc, q, w0, w1, in);
-    }
-  }
-}
-
-// Store of 16 rows of a wave in whole 128-byte lines, turned through the wave's own LDS (16
-// rows of kTurnStride bytes): 32 fp32 columns, as two fragments hold them, or 64 16-bit
-// columns, as four do.  The lines are written past the caches' reuse order: they are not read
-// again soon, and whole lines need no merging in L2 (g and u of a 4096 x 2048 x 8192 forward:
-// 300 -> 279 us; the same with 64-byte segments: 340 us).
-constexpr int kTurnStride = 128 + 16;   // the gap spreads the rows over the banks
-Q4_DEVICE void store_turned(void* c, int64_t row_bytes, int m0, int M, uint32_t lds, int lane) {
-  typedef __attribute__((address_space(3))) u32x4_t* lptr;
-  __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 8 * h + (lane >> 3);
-    const u32x4_t v = *(lptr)(uintptr_t)(lds + r * kTurnStride + (lane & 7) * 16);
-    if (m0 + r < M)
-      __builtin_nontemporal_store(
-          v, reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(c) + (m0 + r) * row_bytes + (lane & 7) * 16));
-  }
-  __builtin_amdgcn_wave_barrier();
-}
-Q4_DEVICE void store_lines(float* c, int64_t ld, int m0, int M, uint32_t lds, int lane, f32x4_t y0, f32x4_t y1) {
-  typedef __attribute__((address_space(3))) f32x4_t* lptr;
-  const uint32_t at = lds + (lane & 15) * kTurnStride + (lane >> 4) * 16;
-  *(lptr)(uintptr_t)at = y0;
-  *(lptr)(uintptr_t)(at + 64) = y1;
-  store_turned(c, ld * 4, m0, M, lds, lane);
-}
-Q4_DEVICE void store_lines16(uint16_t* c, int64_t ld, int dtype, int m0, int M, uint32_t lds, int lane,
-                             const f32x4_t y[4]) {
-  typedef __attribute__((address_space(3))) u32x2_t* lptr;
-  const uint32_t at = lds + (lane & 15) * kTurnStride + (lane >> 4) * 8;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *(lptr)(uintptr_t)(at + 32 * j) = u32x2_t{to16(y[j][0], dtype) | uint32_t(to16(y[j][1], dtype)) << 16,
-                                              to16(y[j][2], dtype) | uint32_t(to16(y[j][3], dtype)) << 16};
-  store_turned(c, ld * 2, m0, M, lds, lane);
-}
-
-// Raw sums of a K slice.
+// Raw sums of a K slice, columns n .. n + 3.
 template <typename V>
 Q4_DEVICE void store_part(const DenseArgs& g, int64_t panel, int m, int n, V v) {
-  if (m >= g.M) return;
   uint32_t* o = static_cast<uint32_t*>(g.part) + (panel * g.M + m) * g.N + n;
   const u32x4_t w = bitcast<u32x4_t>(v);
   if (n + 4 <= g.N && (g.N & 3) == 0) {
@@ -242,6 +155,80 @@ Q4_DEVICE void store_part(const DenseArgs& g, int64_t panel, int m, int n, V v) 
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (n + e < g.N) o[e] = w[e];
+  }
+}
+
+// Eight consecutive 16-bit values of a row (8 lanes: a whole 128-byte line).  NT: written past
+// the caches' reuse order, which whole lines of gradients and of g and u gain from (forward with
+// g and u 300 -> 279 us at 4096 x 2048 x 8192; 64-byte segments lose, 340 us) and INT8 results
+// do not (76.0 -> 78.5 us at 2048 x 2048 x 16384).
+template <bool NT>
+Q4_DEVICE void store8(void* c, int dtype, int64_t idx, f32x4_t y0, f32x4_t y1, int count, int64_t ld) {
+  if (dtype != 0 && count >= 8 && (ld & 7) == 0) {
+    u32x4_t o;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      o[w] = to16(y0[2 * w], dtype) | uint32_t(to16(y0[2 * w + 1], dtype)) << 16;
+      o[2 + w] = to16(y1[2 * w], dtype) | uint32_t(to16(y1[2 * w + 1], dtype)) << 16;
+    }
+    u32x4_t* p = reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(c) + idx);
+    if constexpr (NT) __builtin_nontemporal_store(o, p);
+    else *p = o;
+  } else {
+    const bool vec = (ld & 3) == 0;
+    store4(c, dtype, idx, y0, count, vec);
+    store4(c, dtype, idx + 4, y1, count - 4, vec);
+  }
+}
+
+// The end of a tile: a wave's sums go through its own part of LDS (free once every wave's
+// copies are done), 64 fp32 columns (or 32) per row, so that a lane holds 8 consecutive
+// columns of one row, or 4 of both projections, stores are whole lines, and the code that
+// turns sums into results stands in one short loop (stored from the accumulators it was 30 KB
+// of code, at the same speed).
+// 16-byte chunk c of row r lies at c ^ (r % chunks of a row), against bank conflicts.
+template <int COLS, typename V>
+Q4_DEVICE void turn_in(uint32_t lds, int row, int chunk, V v) {
+  typedef __attribute__((address_space(3))) V* lptr;
+  constexpr int CH = COLS / 4;
+  *(lptr)(uintptr_t)(lds + row * (COLS * 4) + ((chunk ^ (row & (CH - 1))) << 4)) = v;
+}
+
+template <Act A, int EPI, int COLS>
+Q4_DEVICE void turn_out(const DenseArgs& g, int z, int64_t slice, uint32_t lds, int lane, int rows, int m0, int n0,
+                        const float* s_row) {
+  typedef typename Num<A>::acc_t acc_t;
+  typedef __attribute__((address_space(3))) const acc_t* lptr;
+  constexpr bool DUAL = EPI == EPI_SWIGLU;
+  constexpr int CH = COLS / 4, LPR = COLS / 8;   // chunks and lanes per row
+  const int c = lane % LPR, n = n0 + (DUAL ? 4 : 8) * c;
+  const int ca = DUAL ? c : 2 * c, cb = DUAL ? CH / 2 + c : 2 * c + 1;
+  const ColScales cs0 = col_scales<EPI>(g, n), cs1 = col_scales<EPI>(g, n + 4);
+#pragma unroll 2
+  for (int r = lane / LPR; r < rows; r += 64 / LPR) {
+    const acc_t a = *(lptr)(uintptr_t)(lds + r * (COLS * 4) + ((ca ^ (r & (CH - 1))) << 4));
+    const acc_t b = *(lptr)(uintptr_t)(lds + r * (COLS * 4) + ((cb ^ (r & (CH - 1))) << 4));
+    const int m = m0 + r;
+    if (m >= g.M || n >= g.N) continue;
+    if (g.ksplit > 1) {
+      store_part(g, DUAL ? 2 * slice : slice, m, n, a);
+      if (DUAL) store_part(g, 2 * slice + 1, m, n, b);
+      else if (n + 4 < g.N) store_part(g, slice, m, n + 4, b);
+      continue;
+    }
+    if constexpr (DUAL) {
+      const int64_t at = int64_t(m) * g.ldc + n;   // (ldc is a multiple of 8: whole quads)
+      store4(g.c[0], g.c_dtype, at, result4<A, EPI>(a, b, 0.f, cs0), 4, true);
+      if (g.gu) {
+        f32x4_t* p = reinterpret_cast<f32x4_t*>(g.gu + at + int64_t(m) * g.ldc);
+        __builtin_nontemporal_store(a, p);
+        __builtin_nontemporal_store(b, p + g.ldc / 4);
+      }
+    } else {
+      const float sm = EPI == EPI_INT8 ? s_row[r] : 0.f;
+      store8<EPI == EPI_STORE>(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + n, result4<A, EPI>(a, a, sm, cs0),
+             result4<A, EPI>(b, b, sm, cs1), g.N - n, g.ldc);
+    }
   }
 }
 
@@ -474,40 +461,22 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
 #pragma unroll
           for (int j = 0; j < NB; ++j) acc[p][i][j] = T::mfma(fb[sub][p][j], fa[sub][i], acc[p][i][j]);
   }
-  wait_barrier<0>();   // no copy may land after the workgroup's end
-
-  // lane: row m = lane % 16 of its block, columns 4 (lane / 16) .. + 3
-  const int q = lane >> 4;
-  const int nw = n0 + wn * (BP / 2);
-  if (g.ksplit > 1) {
+  __shared__ float s_row[EPI == EPI_INT8 ? BM : 1];
+  if constexpr (EPI == EPI_INT8)
+    if (threadIdx.x < BM) s_row[threadIdx.x] = row_scale<EPI>(g, m0 + threadIdx.x);
+  wait_barrier<0>();   // every wave's copies and reads are done: LDS is free
+  // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3
+  constexpr int COLS = NP * BP / 2;
+  const uint32_t turn = lds0 + wid * (BM / 2 * COLS * 4);
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-          store_part(g, (int64_t(it.ks) * g.batches + it.z) * NP + p, m0 + wm * (BM / 2) + 16 * i + (lane & 15),
-                     nw + 16 * j + 4 * q, acc[p][i][j]);
-    return;
-  }
-  float sm[MB];
-  ColScales cs[NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) sm[i] = row_scale<EPI>(g, m0 + wm * (BM / 2) + 16 * i + (lane & 15));
-#pragma unroll
-  for (int j = 0; j < NB; ++j) cs[j] = col_scales<EPI>(g, nw + 16 * j + 4 * q);
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = m0 + wm * (BM / 2) + 16 * i + (lane & 15);
-    if constexpr (NB == 1) {
-      finish4<A, EPI>(g, it.z, m, nw + 4 * q, acc[0][i][0], acc[NP - 1][i][0], sm[i], cs[0]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NB; j += 2)
-        finish_pair<A, EPI>(g, it.z, m, nw + 16 * j, q, (g.ldc & 7) == 0 && nw + 16 * j + 32 <= g.N, acc[0][i][j],
-                            acc[0][i][j + 1], acc[NP - 1][i][j], acc[NP - 1][i][j + 1], sm[i], cs[j], cs[j + 1]);
-    }
-  }
+        turn_in<COLS>(turn, 16 * i + (lane & 15), 4 * (p * NB + j) + (lane >> 4), acc[p][i][j]);
+  turn_out<A, EPI, COLS>(g, it.z, int64_t(it.ks) * g.batches + it.z, turn, lane, BM / 2, m0 + wm * (BM / 2),
+                         n0 + wn * (BP / 2), s_row + wm * (BM / 2));
 }
 
 // ---------------------------------------------------------------- large tile kernel
@@ -609,65 +578,21 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
     fence();
   }
   if (wid < 4) asm volatile("s_barrier" ::: "memory");
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
-
-  const int q = lane >> 4;
-  const int mw = m0 + wm * 128 + (lane & 15);
-  const int nw = n0 + wn * (DUAL ? 32 : 64);
-  if (g.ksplit > 1) {
+  __shared__ float s_row[EPI == EPI_INT8 ? 256 : 1];
+  if constexpr (EPI == EPI_INT8)
+    if (threadIdx.x < 256) s_row[threadIdx.x] = row_scale<EPI>(g, m0 + threadIdx.x);
+  wait_barrier<0>();   // every wave's copies and reads are done: LDS is free
+  // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3; 64 rows at a time
+  const uint32_t turn = lds0 + wid * (64 * 64 * 4);
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int64_t zs = int64_t(it.ks) * g.batches + it.z;
-        if constexpr (DUAL) store_part(g, 2 * zs + j / 2, mw + 16 * i, nw + 16 * (j % 2) + 4 * q, acc[i][j]);
-        else store_part(g, zs, mw + 16 * i, nw + 16 * j + 4 * q, acc[i][j]);
-      }
-    return;
-  }
-  ColScales cs[NB];
+    for (int i = 0; i < MB / 2; ++i)
 #pragma unroll
-  for (int j = 0; j < NB; ++j) cs[j] = col_scales<EPI>(g, nw + 16 * j + 4 * q);
-  float sm[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) sm[i] = row_scale<EPI>(g, mw + 16 * i);
-  // whole lines where the wave's columns are inside and rows of whole 16 bytes; g and u (half
-  // of what a training forward writes) first, h in 64-byte segments
-  const bool lines = (g.ldc & 7) == 0 && nw + (DUAL ? 32 : 64) <= g.N;
-  const uint32_t turn = lds0 + wid * 4096;
-  asm volatile("s_barrier" ::: "memory");   // every wave's copies are done: LDS is free
-  if constexpr (DUAL) {
-    if (lines && g.gu) {
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const int m = m0 + wm * 128 + 16 * i;
-        store_lines(g.gu + nw, 2 * g.ldc, m, g.M, turn, lane, acc[i][0], acc[i][1]);
-        store_lines(g.gu + g.ldc + nw, 2 * g.ldc, m, g.M, turn, lane, acc[i][2], acc[i][3]);
-      }
-      g.gu = nullptr;
-    }
-  } else if (EPI == EPI_STORE && lines) {   // (INT8: no gain, 76.0 -> 78.5 us at 2048 x 2048 x 16384)
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      f32x4_t y[NB];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) y[j] = result4<A, EPI>(acc[i][j], acc[i][j], sm[i], cs[j]);
-      store_lines16(static_cast<uint16_t*>(it.z ? g.c[1] : g.c[0]) + nw, g.ldc, g.c_dtype, m0 + wm * 128 + 16 * i, g.M,
-                    turn, lane, y);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    if constexpr (DUAL) {
-      finish_pair<A, EPI>(g, it.z, mw + 16 * i, nw, q, (g.ldc & 7) == 0 && nw + 32 <= g.N, acc[i][0], acc[i][1],
-                          acc[i][2], acc[i][3], sm[i], cs[0], cs[1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NB; j += 2)
-        finish_pair<A, EPI>(g, it.z, mw + 16 * i, nw + 16 * j, q, (g.ldc & 7) == 0 && nw + 16 * j + 32 <= g.N,
-                            acc[i][j], acc[i][j + 1], acc[i][j], acc[i][j + 1], sm[i], cs[j], cs[j + 1]);
-    }
+      for (int j = 0; j < NB; ++j)
+        turn_in<64>(turn, 16 * i + (lane & 15), 4 * j + (lane >> 4), acc[h * (MB / 2) + i][j]);
+    turn_out<A, EPI, 64>(g, it.z, int64_t(it.ks) * g.batches + it.z, turn, lane, 64, m0 + wm * 128 + h * 64,
+                         n0 + wn * (DUAL ? 32 : 64), s_row + wm * 128 + h * 64);
   }
 }
 
