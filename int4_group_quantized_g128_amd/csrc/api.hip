@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/q4moe.h"
+#include "dense.h"
 #include "internal.h"
 
 using namespace q4;

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "dense.h"
 #include "internal.h"
 #include "lds_copy.h"
 
@@ -320,7 +321,7 @@ Q4_DEVICE void copies(const u32x4_t& rs, uint32_t at, int first, int lane, int64
     copy2_to_lds(rs, at + first * 1024, P::offset(first, lane, ld, left), P::offset(first + 1, lane, ld, left));
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) copy_to_lds<16>(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left), 0u);
+    for (int j = 0; j < N; ++j) copy_to_lds(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left));
   }
 }
 

@@ -15,10 +15,11 @@
 // written once; the row statistics are recomputed in the backward pass from the rows it
 // reads anyway, so nothing but the inputs is kept between the passes.  All sums are fp32;
 // n and the gradients are formed from the unrounded r, and each output is rounded once.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
-#include "internal.h"
+#include "dense.h"
 
 namespace q4 {
 
