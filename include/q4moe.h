@@ -654,7 +654,8 @@ Q4_API int swiglu_linear_backward(const void* dh, const void* x, const void* w_g
  *           [rows] or Q4_GATE_ELEMENT [rows][cols].
  *  w_pre    device [cols]: weight of the norm before the next block, or NULL (no n).
  *  All of dtype Q4_F32, Q4_F16 or Q4_BF16; w_post and gate need y; y or w_pre is required.
- *  Sums and statistics are fp32; n is formed from the unrounded r.
+ *  Sums and statistics are fp32 (a row's sum of squares has to stay within its range); n is
+ *  formed from the unrounded r.
  * Forward outputs:
  *  r_out    device [rows][cols] (required with y; NULL without): may be res or y itself.
  *  n_out    device [rows][cols], or q_out device [rows][cols] int8 and s_out device [rows]
