@@ -205,6 +205,7 @@ Q4_DEVICE void turn_out(const DenseArgs& g, int z, int64_t slice, uint32_t lds, 
   const int c = lane % LPR, n = n0 + (DUAL ? 4 : 8) * c;
   const int ca = DUAL ? c : 2 * c, cb = DUAL ? CH / 2 + c : 2 * c + 1;
   const ColScales cs0 = col_scales<EPI>(g, n), cs1 = col_scales<EPI>(g, n + 4);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // other lanes' turn_in before these reads
 #pragma unroll 2
   for (int r = lane / LPR; r < rows; r += 64 / LPR) {
     const acc_t a = *(lptr)(uintptr_t)(lds + r * (COLS * 4) + ((ca ^ (r & (CH - 1))) << 4));
@@ -231,6 +232,7 @@ Q4_DEVICE void turn_out(const DenseArgs& g, int z, int64_t slice, uint32_t lds, 
              result4<A, EPI>(b, b, sm, cs1), g.N - n, g.ldc);
     }
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // these reads before the next turn_in
 }
 
 // ---------------------------------------------------------------- panels in LDS
@@ -342,20 +344,20 @@ constexpr int segments(bool amc, bool bmc) { return !amc && bmc ? 2 : 1; }
 struct Item {
   int z, ks, mt, nt;
 };
-Q4_DEVICE Item item_of(int64_t b, int64_t total, int batches, int mtiles, int ntiles) {
-  const int64_t xcd = b % 8, per = total / 8, rest = total % 8;
-  int64_t i = xcd * per + (xcd < rest ? xcd : rest) + b / 8;
+Q4_DEVICE Item item_of(uint32_t b, uint32_t total, uint32_t batches, uint32_t mtiles, uint32_t ntiles) {
+  const uint32_t xcd = b % 8, per = total / 8, rest = total % 8;
+  uint32_t i = xcd * per + (xcd < rest ? xcd : rest) + b / 8;
   Item it;
-  const int64_t tiles = int64_t(mtiles) * ntiles;
+  const uint32_t tiles = mtiles * ntiles;   // (total, and so every product here, is below 2^31)
   it.ks = int(i / (tiles * batches));
   i -= it.ks * tiles * batches;
   it.z = int(i / tiles);
   i -= it.z * tiles;
-  constexpr int GM = 8;
-  const int64_t band = i / (int64_t(GM) * ntiles);
-  const int m0 = int(band) * GM, gm = mtiles - m0 < GM ? mtiles - m0 : GM;
+  constexpr uint32_t GM = 8;
+  const uint32_t band = i / (GM * ntiles);
+  const uint32_t m0 = band * GM, gm = mtiles - m0 < GM ? mtiles - m0 : GM;
   i -= band * GM * ntiles;
-  it.mt = m0 + int(i % gm);
+  it.mt = int(m0 + i % gm);
   it.nt = int(i / gm);
   return it;
 }
@@ -603,12 +605,11 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
   typedef typename Num<A>::acc_t acc_t;
   typedef typename std::conditional<A == Act::I8, int32_t, float>::type S;
   constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
-  const int quads = (g.N + 3) / 4;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= int64_t(g.batches) * g.M * quads) return;
-  const int n = int(i % quads) * 4;
-  const int64_t zm = i / quads;
-  const int z = int(zm / g.M), m = int(zm % g.M);
+  const uint32_t quads = (g.N + 3) / 4, i = blockIdx.x * 256 + threadIdx.x;   // (plan_us: below 2^32)
+  const uint32_t zm = i / quads;
+  if (zm >= uint32_t(g.batches) * g.M) return;
+  const int n = int(i - zm * quads) * 4;
+  const int z = zm >= uint32_t(g.M), m = int(zm) - z * g.M;   // (one batch or two)
   const int count = g.N - n < 4 ? g.N - n : 4;
   const bool vec = count == 4 && (g.N & 3) == 0;
   acc_t v[2];
@@ -635,8 +636,8 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
 // reading); the 8 waves of a workgroup own NF fragments' rows, take the 128-byte K steps in
 // turn and feed the matrix core straight from global memory (16 bytes per lane, two loads
 // cover a step's whole lines), four steps in flight, then add their sums through LDS in wave
-// order.  2048 / 8192 gated projection, one row: 14.0 us, 4.8 TB/s
-// (non-temporal weight loads: 14.6; the second load of a line then misses again).
+// order.  2048 / 8192 gated projection, one row: 12.2 us, 5.5 TB/s (with non-temporal weight
+// loads the second load of a line misses again: 14.6 against 14.0 us on another card).
 template <Act A, int EPI, int W, int NF>
 __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
   typedef Num<A> T;
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(256) k_quantize8_rows(const void* __restrict__
 
 // ---------------------------------------------------------------- launches
 struct Plan {
-  int bm, bn, ksplit;   // bm == 0: the few-rows kernel
+  int tile, ksplit;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -803,6 +804,8 @@ double plan_us(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int b
   static const double ends[3][3] = {{1.9, 8.0, 4.0}, {2.9, 5.1, 13.5}, {2.0, 4.1, 9.3}};
   const int64_t per = ceil_div(steps, ks);
   const int64_t wgs = ceil_div(m, bm) * ceil_div(n * panels, bm) * batches * ceil_div(steps, per);
+  // the grid stays below 2^31 workgroups, a join below 2^32 threads
+  if (wgs >= int64_t(1) << 31 || (ks > 1 && m * batches * ceil_div(n, 4) >= int64_t(1) << 32)) return 1e300;
   const int64_t rounds = ceil_div(wgs, 256 * held[t]);
   const int64_t last = std::min<int64_t>(held[t], ceil_div(wgs - (rounds - 1) * 256 * held[t], 256));
   const auto slice = [&](int64_t on_cu) {
@@ -816,14 +819,14 @@ double plan_us(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int b
 
 // Tile and K split with the least estimated time.
 Plan plan_of(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches) {
-  Plan best{64, 64, 1};
+  Plan best{64, 1};
   if (steps == 0) return best;   // no tokens: the weight gradients are zero
   double us = plan_us(kind, m, n, panels, steps, batches, 64, 1);
   for (const int bm : {64, 128, 256})
     for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (ks > 1 && steps / ks < 2) break;
       const double u = plan_us(kind, m, n, panels, steps, batches, bm, ks);
-      if (u < us) us = u, best = Plan{bm, bm, int(ceil_div(steps, ceil_div(steps, ks)))};
+      if (u < us) us = u, best = Plan{bm, int(ceil_div(steps, ceil_div(steps, ks)))};
     }
   return best;
 }
@@ -836,11 +839,11 @@ template <Act A, bool AMC, bool BMC, int EPI>
 hipError_t launch_tiles(DenseArgs g, const Plan& p, hipStream_t st) {
   constexpr int NP = EPI == EPI_SWIGLU ? 2 : 1;
   g.ksplit = p.ksplit;
-  const int mt = int(ceil_div(g.M, p.bm)), nt = int(ceil_div(int64_t(g.N) * NP, p.bn));
+  const int mt = int(ceil_div(g.M, p.tile)), nt = int(ceil_div(int64_t(g.N) * NP, p.tile));
   const unsigned grid = unsigned(int64_t(mt) * nt * g.batches * p.ksplit);
-  if (p.bm == 256)
+  if (p.tile == 256)
     hipLaunchKernelGGL((k_dense_big<A, AMC, BMC, EPI>), dim3(grid), dim3(512), 0, st, g, mt, nt);
-  else if (p.bm == 128)
+  else if (p.tile == 128)
     hipLaunchKernelGGL((k_dense<A, AMC, BMC, 128, 128, 64, 4, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else
     hipLaunchKernelGGL((k_dense<A, AMC, BMC, 64, 64, 128, 3, EPI>), dim3(grid), dim3(256), 0, st, g, mt, nt);
@@ -859,17 +862,21 @@ hipError_t launch_rows_as(const DenseArgs& g, hipStream_t st) {
 }
 
 // Two fragments per wave halve the reads of x, which count from a few rows on, as long as
-// enough workgroups are left: 7168 x 7168 INT8, 16 rows, 18.8 -> 16.3 us (one row 13.8 ->
-// 13.1); but 8192 x 2048, 64 workgroups instead of 128, 10.5 -> 15.1 us.
+// enough workgroups are left (both measured with non-temporal weight loads): 7168 x 7168
+// INT8, 16 rows, 18.8 -> 16.3 us (one row 13.8 -> 13.1); but 8192 x 2048, 64 workgroups
+// instead of 128, 10.5 -> 15.1 us.
 template <Act A, int EPI>
 hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
   const int64_t wgs = ceil_div(g.N, EPI == EPI_SWIGLU ? 16 : 32);
   return g.M > 4 && wgs >= 192 ? launch_rows_as<A, EPI, 8, 2>(g, st) : launch_rows_as<A, EPI, 8, 1>(g, st);
 }
 
-// Beyond 16 rows the tiles with split K are faster (7168 / 2048 gated projection, 16 rows:
-// 19.8 us against 19.0; 2048 x 2048 INT8: 4.1 us against 7.5).
-bool few_rows(int64_t t) { return t <= 16; }
+// The few-rows kernel up to 16 rows (16 rows, gated 2048 / 2048: 6.4 us against 10.1 in tiles;
+// INT8 8192 x 2048: 9.6 against 10.9), but tiles from 8 rows on where the columns fill the chip
+// with them, since they read x once per 64 columns and not per 8 or 16 (gated 7168 / 7168, 8
+// rows: 50.2 against 41.2 us, 16 rows: 56.5 against 41.8; 2048 / 8192, 16 rows: 16.2 / 15.4).
+// cols: columns of all B panels.
+bool few_rows(int64_t t, int64_t cols) { return t < 8 || (t <= 16 && ceil_div(cols, 64) < 224); }
 
 }  // namespace
 
@@ -883,7 +890,7 @@ hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k,
 }
 
 int64_t int8_linear_workspace(int64_t t, int64_t k, int64_t n) {
-  if (t == 0 || few_rows(t)) return 0;
+  if (t == 0 || few_rows(t, n)) return 0;
   return part_bytes(plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), t, n, 1, 1);
 }
 
@@ -902,12 +909,12 @@ hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_
   g.s_col = ws;
   g.bias = bias;
   g.part = work;
-  if (few_rows(t)) return launch_rows<Act::I8, EPI_INT8>(g, st);
+  if (few_rows(t, n)) return launch_rows<Act::I8, EPI_INT8>(g, st);
   return launch_tiles<Act::I8, false, false, EPI_INT8>(g, plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), st);
 }
 
 int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i) {
-  if (t == 0 || few_rows(t)) return 0;
+  if (t == 0 || few_rows(t, 2 * i)) return 0;
   return part_bytes(plan_of(NT, t, i, 2, ceil_div(h, 64), 1), t, i, 2, 1);
 }
 
@@ -924,7 +931,7 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
   g.c_dtype = f16 ? 1 : 2;
   g.gu = gu;
   g.part = work;
-  if (few_rows(t))
+  if (few_rows(t, 2 * i))
     return f16 ? launch_rows<Act::F16, EPI_SWIGLU>(g, st) : launch_rows<Act::BF16, EPI_SWIGLU>(g, st);
   const Plan p = plan_of(NT, t, i, 2, ceil_div(h, 64), 1);
   return f16 ? launch_tiles<Act::F16, false, false, EPI_SWIGLU>(g, p, st)

@@ -60,7 +60,8 @@ def int8_ref(q, s, wq, ws, bias):
 
 @pytest.mark.parametrize("t,k,n", [(1, 16, 1), (1, 2048, 2048), (3, 144, 33), (16, 1040, 130), (17, 272, 64),
                                    (40, 4096, 100), (64, 512, 17), (65, 2048, 96), (130, 48, 257), (333, 1040, 1001),
-                                   (1000, 640, 2050), (2100, 384, 1100), (3500, 272, 4100), (3500, 400, 4101)])
+                                   (1000, 640, 2050), (2100, 384, 1100), (3500, 272, 4100), (3500, 400, 4101), (7, 80, 14400), (8, 80, 14400),
+                                   (16, 144, 14401)])
 @pytest.mark.parametrize("dt", ALL_TYPES)
 def test_int8_linear(lib, t, k, n, dt):
     g = gen_of(t + k + n)
@@ -127,7 +128,8 @@ def test_quantize_int8_channel(lib, dt, n, k):
 # ------------------------------------------------------------------ gated projection
 SWIGLU_SHAPES = [(1, 8, 8), (1, 2048, 1024), (5, 72, 40), (16, 1000, 136), (17, 64, 24), (33, 512, 200),
                  (64, 136, 72), (65, 72, 264), (130, 1000, 136), (300, 264, 520), (1030, 136, 1288),
-                 (1300, 72, 4360), (3600, 3592, 264), (200, 2568, 2560)]   # the large tiles: forward, dx, dw
+                 (1300, 72, 4360), (3600, 3592, 264), (200, 2568, 2560),   # the large tiles: forward, dx, dw
+                 (7, 72, 7200), (9, 72, 7200)]   # rows and tiles of a wide projection
 
 
 def swiglu_inputs(t, h, i, dt, seed=0):
