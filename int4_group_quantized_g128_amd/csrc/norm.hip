@@ -207,8 +207,8 @@ Q4_DEVICE void row_reduce(float v[K], float* slots, int wave, int& phase) {
 
 Q4_DEVICE float rstd_of(float sumsq, int cols, float eps) { return 1.0f / sqrtf(sumsq / float(cols) + eps); }
 
-// Rows per workgroup: four waves' worth of row groups, or one row over WPR > 4 waves.
-template <int WPR> constexpr int rows_per_wg() { return WPR >= 4 ? 1 : 4 / WPR; }
+// Rows of a workgroup at a time: one, or four where a row is one wave's (no barriers).
+template <int WPR> constexpr int rows_per_wg() { return WPR == 1 ? 4 : 1; }
 template <int WPR> constexpr int threads_per_wg() { return 64 * WPR * rows_per_wg<WPR>(); }
 
 // Whether the next row is fetched ahead (16 waves of 128 registers, or single columns, have
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>()) __attribute__((amdgpu_w
   int phase = 0;
   const int64_t step = int64_t(gridDim.x) * rows_per_wg<WPR>();
   int64_t row = int64_t(blockIdx.x) * rows_per_wg<WPR>() + threadIdx.x / (64 * WPR);
-  if (row >= a.rows) return;   // whole waves, and with WPR >= 4 the whole workgroup
+  if (row >= a.rows) return;   // whole waves, and with WPR > 1 the whole workgroup
   const Raw ones = R::fill(Elem<T>::down(1.f));
   Raw w_post = ones, w_pre = ones, gate = ones, res = ones, y = ones;
   if (a.w_post) w_post = R::fetch(a.w_post, 0, cols, tid);
@@ -459,52 +459,46 @@ __global__ void __launch_bounds__(1024) k_norm_grad_sum(const float* __restrict_
 // the forward pass, 8 in the backward one, which holds twice as much per thread and writes
 // three partial rows of fp32 per workgroup).
 int64_t pass_wgs(int64_t rows, int wpr, bool backward) {
-  const int rpw = wpr >= 4 ? 1 : 4 / wpr;
+  const int rpw = wpr == 1 ? 4 : 1;
   const int64_t fill = 256 * std::max(1, (backward ? kBwdWaves : 16) / (wpr * rpw));
   return std::min<int64_t>((rows + rpw - 1) / rpw, fill);
 }
 
-// Waves per row: two vectors of 8 columns per lane at most, one where that still leaves few
-// waves (or single columns, which take a register each).
-int waves_per_row(int64_t cols) {
-  const bool vec = cols % 8 == 0;
-  if (cols <= 512 || (vec && cols <= 1024)) return 1;
-  if (cols <= 2048 || (vec && cols <= 4096)) return 4;
-  if (cols <= 4096 || (vec && cols <= 8192)) return 8;
-  return 16;
+// Waves per row: two vectors of 8 columns per lane (one to 512 columns), or 8 single columns,
+// which take a register each (16 of them beyond 8192).  Up to 2048 columns few rows take four
+// waves of one vector each, whose chain is shorter (one row to INT8 codes: 4.0 us against 4.5), many
+// rows two waves (4096 x 2048: forward 14.8 -> 13.9 us, with INT8 codes 13.4 -> 11.7).
+int waves_per_row(int64_t rows, int64_t cols) {
+  if (cols % 8 != 0) return cols <= 512 ? 1 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16;
+  if (cols <= 1024) return 1;
+  if (cols <= 2048) return rows >= 1024 ? 2 : 4;
+  return cols <= 4096 ? 4 : cols <= 8192 ? 8 : 16;
 }
 
 template <bool VEC, typename F>
-hipError_t with_shape(int64_t cols, F&& f) {
+hipError_t with_shape(int64_t rows, int64_t cols, F&& f) {
   typedef std::integral_constant<int, 1> one;
   typedef std::integral_constant<int, 2> two;
-  const int w = waves_per_row(cols);
-  const bool nv1 = cols <= int64_t(w) * 512;
-  if (w == 1) {
-    if constexpr (VEC)
-      if (!nv1) return f(one{}, two{});
-    return f(one{}, one{});
+  typedef std::integral_constant<int, 4> four;
+  typedef std::integral_constant<int, 8> eight;
+  typedef std::integral_constant<int, 16> sixteen;
+  const int w = waves_per_row(rows, cols);
+  if constexpr (VEC) {
+    if (w == 1) return cols <= 512 ? f(one{}, one{}) : f(one{}, two{});
+    if (w == 4) return cols <= 2048 ? f(four{}, one{}) : f(four{}, two{});
+    return w == 2 ? f(two{}, two{}) : w == 8 ? f(eight{}, two{}) : f(sixteen{}, two{});
+  } else {
+    if (w == 16) return cols <= 8192 ? f(sixteen{}, one{}) : f(sixteen{}, two{});
+    return w == 1 ? f(one{}, one{}) : w == 4 ? f(four{}, one{}) : f(eight{}, one{});
   }
-  if (w == 4) {
-    if constexpr (VEC)
-      if (!nv1) return f(std::integral_constant<int, 4>{}, two{});
-    return f(std::integral_constant<int, 4>{}, one{});
-  }
-  if (w == 8) {
-    if constexpr (VEC) return f(std::integral_constant<int, 8>{}, two{});
-    else return f(std::integral_constant<int, 8>{}, one{});
-  }
-  if constexpr (!VEC)
-    if (nv1) return f(std::integral_constant<int, 16>{}, one{});
-  return f(std::integral_constant<int, 16>{}, two{});
 }
 
 template <typename F>
-hipError_t with_type(int dtype, int64_t cols, F&& f) {
+hipError_t with_type(int dtype, int64_t rows, int64_t cols, F&& f) {
   const bool vec = cols % 8 == 0;
   auto go = [&](auto t, auto v) {
     constexpr bool VEC = decltype(v)::value;
-    return with_shape<VEC>(cols, [&](auto wpr, auto nv) { return f(t, v, wpr, nv); });
+    return with_shape<VEC>(rows, cols, [&](auto wpr, auto nv) { return f(t, v, wpr, nv); });
   };
   if (dtype == 0) return vec ? go(NF32{}, std::true_type{}) : go(NF32{}, std::false_type{});
   if (dtype == 1) return vec ? go(NF16{}, std::true_type{}) : go(NF16{}, std::false_type{});
@@ -517,7 +511,7 @@ int block_norm_max_cols() { return kMaxCols; }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, void* r_out, void* n_out, int8_t* q_out, float* s_out,
                              hipStream_t st) {
-  return with_type(dtype, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
+  return with_type(dtype, a.rows, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
     typedef decltype(t) T;
     constexpr int WPR = decltype(wpr)::value;
     const unsigned grid = unsigned(pass_wgs(a.rows, WPR, false));
@@ -528,7 +522,7 @@ hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, void* r_out, voi
 }
 
 int64_t block_norm_bwd_workspace(int64_t rows, int64_t cols) {
-  return pass_wgs(rows, waves_per_row(cols), true) * kGradSlots * cols * 4;
+  return pass_wgs(rows, waves_per_row(rows, cols), true) * kGradSlots * cols * 4;
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, const void* dr, const void* dn, void* dres,
@@ -536,7 +530,7 @@ hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int dtype, const void* 
                                  hipStream_t st) {
   int groups = 0;
   if (a.rows > 0) {
-    const hipError_t e = with_type(dtype, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
+    const hipError_t e = with_type(dtype, a.rows, a.cols, [&](auto t, auto v, auto wpr, auto nv) {
       typedef decltype(t) T;
       constexpr int WPR = decltype(wpr)::value;
       const int64_t wgs = pass_wgs(a.rows, WPR, true);

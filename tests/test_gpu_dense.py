@@ -298,7 +298,8 @@ def norm_check(lib, kw, alpha=0.75, eps=1e-6):
 
 
 NORM_SHAPES = [(1, 1), (3, 7), (1, 2048), (5, 129), (4, 512), (7, 520), (9, 1024), (2, 1537), (6, 2048), (3, 4096),
-               (2, 4104), (3, 7168), (2, 8191), (2, 16384), (600, 64), (1100, 2056)]
+               (2, 4104), (3, 7168), (2, 8191), (2, 16384), (600, 64), (1100, 2056), (1023, 1032),
+               (1025, 1032)]
 
 
 @pytest.mark.parametrize("dt", ALL_TYPES)
