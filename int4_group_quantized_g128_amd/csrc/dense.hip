@@ -160,9 +160,8 @@ Q4_DEVICE void store_part(const DenseArgs& g, int64_t panel, int m, int n, V v) 
 }
 
 // Eight consecutive 16-bit values of a row (8 lanes: a whole 128-byte line).  NT: written past
-// the caches' reuse order, which whole lines of gradients and of g and u gain from (forward with
-// g and u 300 -> 279 us at 4096 x 2048 x 8192; 64-byte segments lose, 340 us) and INT8 results
-// do not (76.0 -> 78.5 us at 2048 x 2048 x 16384).
+// the caches' reuse order, which the gradients gain from (backward 524 -> 513 us at 4096 x 2048 x
+// 8192) and INT8 results do not (76.0 -> 78.5 us at 2048 x 2048 x 16384).
 template <bool NT>
 Q4_DEVICE void store8(void* c, int dtype, int64_t idx, f32x4_t y0, f32x4_t y1, int count, int64_t ld) {
   if (dtype != 0 && count >= 8 && (ld & 7) == 0) {
@@ -222,9 +221,11 @@ Q4_DEVICE void turn_out(const DenseArgs& g, int z, int64_t slice, uint32_t lds, 
       const int64_t at = int64_t(m) * g.ldc + n;   // (ldc is a multiple of 8: whole quads)
       store4(g.c[0], g.c_dtype, at, result4<A, EPI>(a, b, 0.f, cs0), 4, true);
       if (g.gu) {
+        // (past the caches a forward alone gains 20 us of 300 at 4096 x 2048 x 8192, but a backward
+        // pass that follows it at once loses 57: 796 -> 833 us for both)
         f32x4_t* p = reinterpret_cast<f32x4_t*>(g.gu + at + int64_t(m) * g.ldc);
-        __builtin_nontemporal_store(a, p);
-        __builtin_nontemporal_store(b, p + g.ldc / 4);
+        *p = a;
+        *(p + g.ldc / 4) = b;
       }
     } else {
       const float sm = EPI == EPI_INT8 ? s_row[r] : 0.f;
