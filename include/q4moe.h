@@ -624,7 +624,9 @@ Q4_API int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64
  *  gu_out   device [t][2][i] fp32 or NULL: g and u, which the backward pass reads (a
  *           serving call passes NULL).
  * Backward, given dh [t][i]:
- *   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh silu(g)   (rounded to dtype: operands)
+ *   dg = dh u sig(g) (1 + g (1 - sig(g))),  du = dh silu(g)   (rounded to dtype: operands;
+ *   in fp16 first scaled by a power of two per token for dx and per column for dw_gate and
+ *   dw_up, undone in the fp32 sums, so that they may lie outside fp16's range)
  *   dx = dg w_gate + du w_up,   dw_gate = dg^T x,   dw_up = du^T x
  *  dx       device [t][h];  dw_gate, dw_up device [i][h] (overwritten, not accumulated).
  *  workspace device buffers of swiglu_linear_workspace_bytes / swiglu_linear_backward_

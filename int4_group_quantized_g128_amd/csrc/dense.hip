@@ -32,7 +32,9 @@ namespace {
 constexpr int kStepBytes = 128;
 constexpr uint32_t kNoByte = 0x80000000u;   // a byte offset past every descriptor's range
 
-enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_INT8 = 2 };
+// SCALED: as STORE, each row times its own power of two.
+enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_INT8 = 2, EPI_SCALED = 3 };
+constexpr bool row_scaled(int epi) { return epi == EPI_INT8 || epi == EPI_SCALED; }
 
 template <Act A> struct Num {
   static constexpr int ESZ = A == Act::I8 ? 1 : 2;
@@ -54,7 +56,7 @@ struct DenseArgs {
   void* c[2];
   int64_t ldc;
   int32_t c_dtype;          // 0 fp32, 1 fp16, 2 bf16
-  const float* s_row;       // int8: token scales
+  const float* s_row;       // int8: token scales; scaled: [batches][M]
   const float* s_col;       // int8: channel scales
   const float* bias;        // int8: or NULL
   float* gu;                // swiglu: [M][2][N] products, or NULL
@@ -109,8 +111,8 @@ Q4_DEVICE ColScales col_scales(const DenseArgs& g, int n) {
   return r;
 }
 template <int EPI>
-Q4_DEVICE float row_scale(const DenseArgs& g, int m) {
-  if constexpr (EPI == EPI_INT8) return g.s_row[min(m, g.M - 1)];
+Q4_DEVICE float row_scale(const DenseArgs& g, int z, int m) {
+  if constexpr (row_scaled(EPI)) return g.s_row[(EPI == EPI_SCALED ? int64_t(z) * g.M : 0) + min(m, g.M - 1)];
   return 0.f;
 }
 
@@ -123,6 +125,7 @@ Q4_DEVICE f32x4_t result4(typename Num<A>::acc_t v, typename Num<A>::acc_t v2, f
     // int8: the INT32 sum becomes fp32 (24 bits), then one product of the scales, one with it
     if constexpr (EPI == EPI_INT8) y[i] = float(v[i]) * (sm * cs.s[i]) + cs.b[i];
     else if constexpr (EPI == EPI_SWIGLU) y[i] = swiglu(v[i], v2[i]);
+    else if constexpr (EPI == EPI_SCALED) y[i] = v[i] * sm;
     else y[i] = v[i];
   }
   return y;
@@ -228,8 +231,8 @@ Q4_DEVICE void turn_out(const DenseArgs& g, int z, int64_t slice, uint32_t lds, 
         *(p + g.ldc / 4) = b;
       }
     } else {
-      const float sm = EPI == EPI_INT8 ? s_row[r] : 0.f;
-      store8<EPI == EPI_STORE>(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + n, result4<A, EPI>(a, a, sm, cs0),
+      const float sm = row_scaled(EPI) ? s_row[r] : 0.f;
+      store8<EPI != EPI_INT8>(z ? g.c[1] : g.c[0], g.c_dtype, int64_t(m) * g.ldc + n, result4<A, EPI>(a, a, sm, cs0),
              result4<A, EPI>(b, b, sm, cs1), g.N - n, g.ldc);
     }
   }
@@ -465,9 +468,9 @@ __global__ void __launch_bounds__(256) k_dense(DenseArgs g, int mtiles, int ntil
 #pragma unroll
           for (int j = 0; j < NB; ++j) acc[p][i][j] = T::mfma(fb[sub][p][j], fa[sub][i], acc[p][i][j]);
   }
-  __shared__ float s_row[EPI == EPI_INT8 ? BM : 1];
-  if constexpr (EPI == EPI_INT8)
-    if (threadIdx.x < BM) s_row[threadIdx.x] = row_scale<EPI>(g, m0 + threadIdx.x);
+  __shared__ float s_row[row_scaled(EPI) ? BM : 1];
+  if constexpr (row_scaled(EPI))
+    if (threadIdx.x < BM) s_row[threadIdx.x] = row_scale<EPI>(g, it.z, m0 + threadIdx.x);
   wait_barrier<0>();   // every wave's copies and reads are done: LDS is free
   // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3
   constexpr int COLS = NP * BP / 2;
@@ -582,9 +585,9 @@ __global__ void __launch_bounds__(512, 1) k_dense_big(DenseArgs g, int mtiles, i
     fence();
   }
   if (wid < 4) asm volatile("s_barrier" ::: "memory");
-  __shared__ float s_row[EPI == EPI_INT8 ? 256 : 1];
-  if constexpr (EPI == EPI_INT8)
-    if (threadIdx.x < 256) s_row[threadIdx.x] = row_scale<EPI>(g, m0 + threadIdx.x);
+  __shared__ float s_row[row_scaled(EPI) ? 256 : 1];
+  if constexpr (row_scaled(EPI))
+    if (threadIdx.x < 256) s_row[threadIdx.x] = row_scale<EPI>(g, it.z, m0 + threadIdx.x);
   wait_barrier<0>();   // every wave's copies and reads are done: LDS is free
   // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3; 64 rows at a time
   const uint32_t turn = lds0 + wid * (64 * 64 * 4);
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
       }
     }
   }
-  finish4<A, EPI>(g, z, m, n, v[0], v[NP - 1], row_scale<EPI>(g, m), col_scales<EPI>(g, n));
+  finish4<A, EPI>(g, z, m, n, v[0], v[NP - 1], row_scale<EPI>(g, z, m), col_scales<EPI>(g, n));
 }
 
 // ---------------------------------------------------------------- few rows
@@ -711,16 +714,40 @@ __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
     for (int i = 0; i < 4; ++i) up[i] = __shfl_xor(v[i], 32, 64);
     if (lane < 32) finish4<A, EPI>(g, 0, m, n, v, up, 0.f, col_scales<EPI>(g, n));
   } else {
-    finish4<A, EPI>(g, 0, m, n, v, v, row_scale<EPI>(g, m), col_scales<EPI>(g, n));
+    finish4<A, EPI>(g, 0, m, n, v, v, row_scale<EPI>(g, 0, m), col_scales<EPI>(g, n));
   }
 }
 
 // ---------------------------------------------------------------- element-wise kernels
-// dg and du of 8 elements: bound by memory (g, u in fp32 and dh in, dg and du out: 14 bytes
-// per element).  g and u are kept in fp32: rounding them to 16 bits as well made the bf16
-// gradients 1.8 times as far from the 64-bit ones as one rounding of the result does, fp32
-// 1.4 times (dg and du are rounded, being matrix-core operands next).
+// dg and du of 8 elements, columns c .. c + 7 of a token's row.
 template <bool F16>
+Q4_DEVICE void swiglu_grad8(const uint16_t* __restrict__ dh, const float* __restrict__ gu, int64_t row, int64_t inter,
+                            int64_t c, float a[8], float b[8]) {
+  f32x4_t g[2], u[2];
+  uint16_t d[8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    g[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + c + 4 * j));
+    u[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + inter + c + 4 * j));
+  }
+  *reinterpret_cast<uint4*>(d) = load16_stream(dh + row * inter + c);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float gv = g[e / 4][e % 4], uv = u[e / 4][e % 4];
+    const float dv = F16 ? f16_bits_to_f32(d[e]) : bf16_to_f32(d[e]);
+    const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-gv));
+    a[e] = dv * uv * sig * (1.0f + gv * (1.0f - sig));
+    b[e] = dv * gv * sig;
+  }
+}
+
+// dg and du in bf16: bound by memory (g, u in fp32 and dh in, dg and du out: 14 bytes per
+// element).  g and u are kept in fp32: rounding them to 16 bits as well made the bf16
+// gradients 1.8 times as far from the 64-bit ones as one rounding of the result does, fp32
+// 1.4 times.  The rest is the rounding of dg and du themselves: as matrix-core operands they
+// have the type of x and the weights, and a second operand for what a rounding leaves would
+// double the work of all three products (8 T H I operations more, 0.38 ms at 4096 x 2048 x
+// 8192 and this card's 1437 TFLOP/s).
 __global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict__ dh, const float* __restrict__ gu,
                                                      int64_t t, int64_t inter, uint16_t* __restrict__ dg,
                                                      uint16_t* __restrict__ du) {
@@ -728,24 +755,139 @@ __global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict_
   const int64_t step = int64_t(gridDim.x) * 256;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < t * vecs; i += step) {
     const int64_t row = i / vecs, c = (i - row * vecs) * 8;
-    f32x4_t g[2], u[2];
-    uint16_t a[8], b[8], d[8];
+    float va[8], vb[8];
+    swiglu_grad8<false>(dh, gu, row, inter, c, va, vb);
+    uint16_t a[8], b[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      g[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + c + 4 * j));
-      u[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(gu + row * 2 * inter + inter + c + 4 * j));
-    }
-    *reinterpret_cast<uint4*>(d) = load16_stream(dh + row * inter + c);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float gv = g[e / 4][e % 4], uv = u[e / 4][e % 4];
-      const float dv = F16 ? f16_bits_to_f32(d[e]) : bf16_to_f32(d[e]);
-      const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-gv));
-      a[e] = to16(dv * uv * sig * (1.0f + gv * (1.0f - sig)), F16 ? 1 : 2);
-      b[e] = to16(dv * gv * sig, F16 ? 1 : 2);
-    }
+    for (int e = 0; e < 8; ++e) a[e] = to16(va[e], 2), b[e] = to16(vb[e], 2);
     *reinterpret_cast<uint4*>(dg + row * inter + c) = *reinterpret_cast<const uint4*>(a);
     *reinterpret_cast<uint4*>(du + row * inter + c) = *reinterpret_cast<const uint4*>(b);
+  }
+}
+
+// dg and du in fp16.  The type holds 2^-24 to 2^16 and the fp32 values can lie outside it where
+// the gradients do not (dh of 2^12 and u of 2^8, times weights of 2^-12), so each operand takes
+// powers of two along the axis that the product keeps: dx keeps the tokens, dw the columns.
+//   dx  = 2^r_t (2^-r_t dg Wg + 2^-r_t du Wu),   dWg = 2^c_i ((2^-c_i dg)^T x),  dWu likewise
+// which takes the largest finite magnitude of each row and column first, a pass of its own over
+// g, u and dh (10 bytes per element), and two sets of operands (8 bytes written, not 4): the
+// backward pass of 777 x 1000 x 2728 takes 75 us, unscaled 57.
+// Scaled, that magnitude lies in [2^14, 2^15): nothing overflows, and an element loses bits
+// only below 2^-28 of it.
+constexpr int kMaxGroup = 512;   // columns of a wave's row maximum
+
+// Rows per partial column maximum: 32, more where that made over 2048 workgroups.
+int64_t grad_rows(int64_t t, int64_t inter) {
+  const int64_t groups = (inter + kMaxGroup - 1) / kMaxGroup;
+  const int64_t chunks = std::max<int64_t>(1, 2048 / groups);
+  return std::max<int64_t>(32, (t + chunks - 1) / chunks);
+}
+
+// rmax [t][groups]: of a token's dg and du over 512 columns; cmax [chunks][2][inter]: of dg and
+// of du over the chunk's rows.
+__global__ void __launch_bounds__(256) k_swiglu_grad_max(const uint16_t* __restrict__ dh, const float* __restrict__ gu,
+                                                         int64_t t, int64_t inter, int64_t rows, uint32_t groups,
+                                                         float* __restrict__ rmax, float* __restrict__ cmax) {
+  __shared__ float s[4][2][kMaxGroup];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t group = blockIdx.x % groups, chunk = blockIdx.x / groups;
+  const int64_t c = int64_t(group) * kMaxGroup + lane * 8;
+  const int64_t end = int64_t(chunk + 1) * rows < t ? int64_t(chunk + 1) * rows : t;
+  float ca[8], cb[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ca[e] = cb[e] = 0.f;
+  for (int64_t row = int64_t(chunk) * rows + wave; row < end; row += 4) {
+    float m = 0.f;
+    if (c < inter) {
+      float a[8], b[8];
+      swiglu_grad8<true>(dh, gu, row, inter, c, a, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // (infinities and NaN stay what they are at any scale)
+        const float fa = fabsf(a[e]) < __builtin_inff() ? fabsf(a[e]) : 0.f;
+        const float fb = fabsf(b[e]) < __builtin_inff() ? fabsf(b[e]) : 0.f;
+        ca[e] = fmaxf(ca[e], fa), cb[e] = fmaxf(cb[e], fb);
+        m = fmaxf(m, fmaxf(fa, fb));
+      }
+    }
+    m = wave_max(m);
+    if (lane == 0) rmax[row * groups + group] = m;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[wave][0][lane * 8 + e] = ca[e], s[wave][1][lane * 8 + e] = cb[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kMaxGroup; i += 256) {
+    const int p = i / kMaxGroup, k = i % kMaxGroup;
+    const int64_t col = int64_t(group) * kMaxGroup + k;
+    if (col < inter)
+      cmax[(int64_t(chunk) * 2 + p) * inter + col] = fmaxf(fmaxf(s[0][p][k], s[1][p][k]), fmaxf(s[2][p][k], s[3][p][k]));
+  }
+}
+
+// The power of two s with m / s in [2^14, 2^15), within [2^-100, 2^113]: what is smaller than
+// 2^-86 to begin with vanishes in any fp16 gradient.
+Q4_DEVICE float pow2_scale(float m) {
+  const int e = int(__float_as_uint(m) >> 23) - 127 - 14;
+  return m > 0.f ? __uint_as_float(uint32_t(max(e, -100) + 127) << 23) : 1.f;
+}
+// 1 / s of a power of two.
+Q4_DEVICE float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// Scales from the maxima: cscale [2][inter] (workgroups of 64 columns by 16 waves, which take
+// every 16th chunk), then rscale [t] (a wave per token).
+__global__ void __launch_bounds__(1024) k_swiglu_grad_scales(const float* __restrict__ rmax,
+                                                             const float* __restrict__ cmax, int64_t t, int64_t inter,
+                                                             int chunks, uint32_t groups, uint32_t col_wgs,
+                                                             float* __restrict__ rscale, float* __restrict__ cscale) {
+  __shared__ float s[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float m = 0.f;
+  if (blockIdx.x < col_wgs) {
+    const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+    if (c < 2 * inter)
+#pragma unroll 4
+      for (int k = wave; k < chunks; k += 16) m = fmaxf(m, cmax[int64_t(k) * 2 * inter + c]);
+    s[wave][lane] = m;
+    __syncthreads();
+    if (wave != 0 || c >= 2 * inter) return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w) m = fmaxf(m, s[w][lane]);
+    cscale[c] = pow2_scale(m);
+  } else {
+    const int64_t row = int64_t(blockIdx.x - col_wgs) * 16 + wave;
+    if (row >= t) return;
+    for (uint32_t k = lane; k < groups; k += 64) m = fmaxf(m, rmax[row * groups + k]);
+    m = wave_max(m);
+    if (lane == 0) rscale[row] = pow2_scale(m);
+  }
+}
+
+// dg and du scaled by row (row_g, row_u: dx) and by column (col_g, col_u: dw).
+__global__ void __launch_bounds__(256) k_swiglu_grad_scaled(const uint16_t* __restrict__ dh,
+                                                            const float* __restrict__ gu, int64_t t, int64_t inter,
+                                                            const float* __restrict__ rscale,
+                                                            const float* __restrict__ cscale,
+                                                            uint16_t* __restrict__ row_g, uint16_t* __restrict__ row_u,
+                                                            uint16_t* __restrict__ col_g,
+                                                            uint16_t* __restrict__ col_u) {
+  const int64_t vecs = inter / 8;
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < t * vecs; i += step) {
+    const int64_t row = i / vecs, c = (i - row * vecs) * 8;
+    float va[8], vb[8];
+    swiglu_grad8<true>(dh, gu, row, inter, c, va, vb);
+    const float r = pow2_inverse(rscale[row]);
+    uint16_t a[8], b[8], ca[8], cb[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = to16(va[e] * r, 1), b[e] = to16(vb[e] * r, 1);
+      ca[e] = to16(va[e] * pow2_inverse(cscale[c + e]), 1);
+      cb[e] = to16(vb[e] * pow2_inverse(cscale[inter + c + e]), 1);
+    }
+    *reinterpret_cast<uint4*>(row_g + row * inter + c) = *reinterpret_cast<const uint4*>(a);
+    *reinterpret_cast<uint4*>(row_u + row * inter + c) = *reinterpret_cast<const uint4*>(b);
+    *reinterpret_cast<uint4*>(col_g + row * inter + c) = *reinterpret_cast<const uint4*>(ca);
+    *reinterpret_cast<uint4*>(col_u + row * inter + c) = *reinterpret_cast<const uint4*>(cb);
   }
 }
 
@@ -939,56 +1081,88 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
              : launch_tiles<Act::BF16, false, false, EPI_SWIGLU>(g, p, st);
 }
 
-// Workspace: dg and du [t][i] each, then the K slices of whichever product splits K.
+// Workspace of the gradients: the K slices of whichever product splits K, dg and du [t][i]
+// (in fp16 scaled by row, and once more scaled by column, with the scales and the maxima that
+// they come from).  One size for both types.
+struct GradWork {
+  Plan dx, dw;
+  void* part;
+  uint16_t *g, *u, *col_g, *col_u;
+  float *rscale, *cscale, *rmax, *cmax;
+  int64_t bytes;
+};
+GradWork grad_work(void* base, int64_t t, int64_t h, int64_t i) {
+  const int64_t groups = ceil_div(i, kMaxGroup);
+  GradWork w{};
+  w.dx = plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1);
+  w.dw = plan_of(DW, i, h, 1, ceil_div(t, 64), 2);
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = static_cast<uint8_t*>(base) + w.bytes;
+    w.bytes += align256(bytes);
+    return static_cast<void*>(p);
+  };
+  auto half = [&] { return static_cast<uint16_t*>(take(t * i * 2)); };
+  auto floats = [&](int64_t n) { return static_cast<float*>(take(n * 4)); };
+  w.part = take(std::max(part_bytes(w.dx, t, h, 1, 1), part_bytes(w.dw, i, h, 1, 2)));
+  w.g = half(), w.u = half(), w.col_g = half(), w.col_u = half();
+  w.rscale = floats(t), w.cscale = floats(2 * i);
+  w.rmax = floats(t * groups), w.cmax = floats(ceil_div(t, grad_rows(t, i)) * 2 * i);
+  return w;
+}
 int64_t swiglu_linear_bwd_workspace(int64_t t, int64_t h, int64_t i) {
-  if (t == 0) return 0;
-  const int64_t dx = part_bytes(plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1), t, h, 1, 1);
-  const int64_t dw = part_bytes(plan_of(DW, i, h, 1, ceil_div(t, 64), 2), i, h, 1, 2);
-  return 2 * align256(t * i * 2) + std::max(dx, dw);
+  return t == 0 ? 0 : grad_work(nullptr, t, h, i).bytes;
 }
 
 hipError_t launch_swiglu_linear_bwd(const void* dh, const void* x, const void* wg, const void* wu, const float* gu,
                                     int64_t t, int64_t h, int64_t i, int f16, void* dx, void* dwg, void* dwu,
                                     void* work, hipStream_t st) {
-  uint16_t* dg = static_cast<uint16_t*>(work);
-  uint16_t* du = dg + align256(t * i * 2) / 2;
-  void* part = reinterpret_cast<uint8_t*>(work) + 2 * align256(t * i * 2);
+  const GradWork w = grad_work(work, t, h, i);
   if (t > 0) {
     const unsigned grid = unsigned(std::min<int64_t>(ceil_div(t * (i / 8), 256), 4096));
     const auto* d = static_cast<const uint16_t*>(dh);
-    if (f16) hipLaunchKernelGGL(k_swiglu_grad<true>, dim3(grid), dim3(256), 0, st, d, gu, t, i, dg, du);
-    else hipLaunchKernelGGL(k_swiglu_grad<false>, dim3(grid), dim3(256), 0, st, d, gu, t, i, dg, du);
+    if (f16) {
+      const int64_t rows = grad_rows(t, i), chunks = ceil_div(t, rows);
+      const unsigned groups = unsigned(ceil_div(i, kMaxGroup)), col_wgs = unsigned(ceil_div(2 * i, 64));
+      hipLaunchKernelGGL(k_swiglu_grad_max, dim3(unsigned(groups * chunks)), dim3(256), 0, st, d, gu, t, i, rows, groups,
+                         w.rmax, w.cmax);
+      hipLaunchKernelGGL(k_swiglu_grad_scales, dim3(unsigned(col_wgs + ceil_div(t, 16))), dim3(1024), 0, st, w.rmax,
+                         w.cmax, t, i, int(chunks), groups, col_wgs, w.rscale, w.cscale);
+      hipLaunchKernelGGL(k_swiglu_grad_scaled, dim3(grid), dim3(256), 0, st, d, gu, t, i, w.rscale, w.cscale, w.g, w.u,
+                         w.col_g, w.col_u);
+    } else {
+      hipLaunchKernelGGL(k_swiglu_grad, dim3(grid), dim3(256), 0, st, d, gu, t, i, w.g, w.u);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   DenseArgs g{};
   g.c_dtype = f16 ? 1 : 2;
   g.ksplit = 1;
-  g.part = part;
+  g.part = w.part;
   g.ldc = h;
   g.N = int32_t(h);
   if (t > 0) {   // dx = dg Wg + du Wu: K runs over the gate rows, then the up rows
-    g.a[0] = dg, g.a[1] = du;
+    g.a[0] = w.g, g.a[1] = w.u;
     g.b[0] = wg, g.b[1] = wu;
     g.lda = i, g.ldb = h;
     g.M = int32_t(t), g.K = int32_t(i);
     g.batches = 1;
     g.c[0] = g.c[1] = dx;
-    const Plan p = plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1);
-    const hipError_t e = f16 ? launch_tiles<Act::F16, false, true, EPI_STORE>(g, p, st)
-                             : launch_tiles<Act::BF16, false, true, EPI_STORE>(g, p, st);
+    g.s_row = w.rscale;
+    const hipError_t e = f16 ? launch_tiles<Act::F16, false, true, EPI_SCALED>(g, w.dx, st)
+                             : launch_tiles<Act::BF16, false, true, EPI_STORE>(g, w.dx, st);
     if (e != hipSuccess) return e;
   }
   // dWg = dg^T x and dWu = du^T x as two batches (t == 0: no K step, zeros)
-  g.a[0] = dg, g.a[1] = du;
+  g.a[0] = f16 ? w.col_g : w.g, g.a[1] = f16 ? w.col_u : w.u;
   g.b[0] = g.b[1] = x;
   g.lda = i, g.ldb = h;
   g.M = int32_t(i), g.K = int32_t(t);
   g.batches = 2;
   g.c[0] = dwg, g.c[1] = dwu;
-  const Plan p = plan_of(DW, i, h, 1, ceil_div(t, 64), 2);
-  return f16 ? launch_tiles<Act::F16, true, true, EPI_STORE>(g, p, st)
-             : launch_tiles<Act::BF16, true, true, EPI_STORE>(g, p, st);
+  g.s_row = w.cscale;
+  return f16 && t > 0 ? launch_tiles<Act::F16, true, true, EPI_SCALED>(g, w.dw, st)
+                      : launch_tiles<Act::BF16, true, true, EPI_STORE>(g, w.dw, st);
 }
 
 }  // namespace q4
