@@ -739,10 +739,18 @@ def int4_w4a8_group_acc(q, w_dev, n, asymmetric=False):
 
 # ------------------------------------------------------------------ dense operators
 # These run at a few microseconds per call for one token, so their checks take one pass per
-# tensor and the stream comes as a raw handle.
+# tensor and the stream comes as a raw handle (through torch's public calls where a torch
+# lacks the direct ones).
 _16BIT = (torch.float16, torch.bfloat16)
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _public_raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 
 # Workspace sizes depend on the sizes alone (a library call per size, not per use).
