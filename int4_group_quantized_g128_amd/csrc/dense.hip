@@ -22,6 +22,7 @@
 
 #include "common.h"
 #include "dense.h"
+#include "dense_plan.h"
 #include "internal.h"
 #include "lds_copy.h"
 
@@ -921,59 +922,6 @@ __global__ void __launch_bounds__(256) k_quantize8_rows(const void* __restrict__
 }
 
 // ---------------------------------------------------------------- launches
-struct Plan {
-  int tile, ksplit;
-};
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// The products by how their panels lie, which decides what a step costs.
-enum Kind { NT = 0 /* forward, KC x KC */, DX = 1 /* KC x MC */, DW = 2 /* MC x MC */ };
-
-// Estimated time (us) of a product of `steps` 128-byte K steps with square tiles of `bm` and
-// K in `ks` slices.  Per kind and tile size: time of a step when the workgroup is alone on
-// its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
-// workgroup), time of a workgroup's start and end.  The forward figures are fitted to 75
-// shapes of both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three
-// tiles and up to 8 splits: the plan below then lies within 2 % of the fastest of them on
-// every one (a rule that only counted workgroups lost up to 70 %).  The backward figures are
-// fitted to 6 shapes with 15 plans each (64 to 2048 tokens; rms error of an estimate 12 % for
-// dx, 7 % for dW).
-double plan_us(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
-  const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
-  static const int held[3] = {3, 2, 1};   // workgroups a CU holds
-  static const double alone[3][3] = {{0.27, 0.55, 0.62}, {0.35, 0.66, 1.27}, {0.17, 0.39, 1.53}};
-  static const double full[3][3] = {{0.21, 0.45, 1.23}, {0.22, 0.65, 1.27}, {0.20, 0.54, 1.53}};
-  static const double ends[3][3] = {{1.9, 8.0, 4.0}, {2.9, 5.1, 13.5}, {2.0, 4.1, 9.3}};
-  const int64_t per = ceil_div(steps, ks);
-  const int64_t wgs = ceil_div(m, bm) * ceil_div(n * panels, bm) * batches * ceil_div(steps, per);
-  // the grid stays below 2^31 workgroups, a join below 2^32 threads
-  if (wgs >= int64_t(1) << 31 || (ks > 1 && m * batches * ceil_div(n, 4) >= int64_t(1) << 32)) return 1e300;
-  const int64_t rounds = ceil_div(wgs, 256 * held[t]);
-  const int64_t last = std::min<int64_t>(held[t], ceil_div(wgs - (rounds - 1) * 256 * held[t], 256));
-  const auto slice = [&](int64_t on_cu) {
-    return ends[kind][t] + per * std::max(alone[kind][t], full[kind][t] * on_cu);
-  };
-  double us = (rounds - 1) * slice(held[t]) + slice(last);
-  // the join: a launch, a chain of reads, and the slices' bytes at 4.5 TB/s
-  if (ks > 1) us += 2.9 + 0.5 * ks + double(ks) * m * n * panels * batches * 4 / 4.5e6;
-  return us;
-}
-
-// Tile and K split with the least estimated time.
-Plan plan_of(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches) {
-  Plan best{64, 1};
-  if (steps == 0) return best;   // no tokens: the weight gradients are zero
-  double us = plan_us(kind, m, n, panels, steps, batches, 64, 1);
-  for (const int bm : {64, 128, 256})
-    for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (ks > 1 && steps / ks < 2) break;
-      const double u = plan_us(kind, m, n, panels, steps, batches, bm, ks);
-      if (u < us) us = u, best = Plan{bm, int(ceil_div(steps, ceil_div(steps, ks)))};
-    }
-  return best;
-}
-
 int64_t part_bytes(const Plan& p, int64_t m, int64_t n, int panels, int batches) {
   return p.ksplit > 1 ? int64_t(p.ksplit) * batches * panels * m * n * 4 : 0;
 }
@@ -1014,13 +962,6 @@ hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
   return g.M > 4 && wgs >= 192 ? launch_rows_as<A, EPI, 8, 2>(g, st) : launch_rows_as<A, EPI, 8, 1>(g, st);
 }
 
-// The few-rows kernel up to 16 rows (16 rows, gated 2048 / 2048: 6.4 us against 10.1 in tiles;
-// INT8 8192 x 2048: 9.6 against 10.9), but tiles from 8 rows on where the columns fill the chip
-// with them, since they read x once per 64 columns and not per 8 or 16 (gated 7168 / 7168, 8
-// rows: 50.2 against 41.2 us, 16 rows: 56.5 against 41.8; 2048 / 8192, 16 rows: 16.2 / 15.4).
-// cols: columns of all B panels.
-bool few_rows(int64_t t, int64_t cols) { return t < 8 || (t <= 16 && ceil_div(cols, 64) < 224); }
-
 }  // namespace
 
 hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k, int8_t* q, float* s, int32_t* flags,
@@ -1033,8 +974,7 @@ hipError_t launch_quantize8_rows(const void* w, int dtype, int64_t n, int64_t k,
 }
 
 int64_t int8_linear_workspace(int64_t t, int64_t k, int64_t n) {
-  if (t == 0 || few_rows(t, n)) return 0;
-  return part_bytes(plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), t, n, 1, 1);
+  return t == 0 ? 0 : part_bytes(int8_plan(t, k, n), t, n, 1, 1);
 }
 
 hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_t k, const int8_t* wq, const float* ws,
@@ -1052,13 +992,12 @@ hipError_t launch_int8_linear(const int8_t* q, const float* s, int64_t t, int64_
   g.s_col = ws;
   g.bias = bias;
   g.part = work;
-  if (few_rows(t, n)) return launch_rows<Act::I8, EPI_INT8>(g, st);
-  return launch_tiles<Act::I8, false, false, EPI_INT8>(g, plan_of(NT, t, n, 1, ceil_div(k, kStepBytes), 1), st);
+  const Plan p = int8_plan(t, k, n);
+  return p.tile == 0 ? launch_rows<Act::I8, EPI_INT8>(g, st) : launch_tiles<Act::I8, false, false, EPI_INT8>(g, p, st);
 }
 
 int64_t swiglu_linear_workspace(int64_t t, int64_t h, int64_t i) {
-  if (t == 0 || few_rows(t, 2 * i)) return 0;
-  return part_bytes(plan_of(NT, t, i, 2, ceil_div(h, 64), 1), t, i, 2, 1);
+  return t == 0 ? 0 : part_bytes(swiglu_plan(t, h, i), t, i, 2, 1);
 }
 
 hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, int64_t t, int64_t h, int64_t i, int f16,
@@ -1074,9 +1013,9 @@ hipError_t launch_swiglu_linear(const void* x, const void* wg, const void* wu, i
   g.c_dtype = f16 ? 1 : 2;
   g.gu = gu;
   g.part = work;
-  if (few_rows(t, 2 * i))
+  const Plan p = swiglu_plan(t, h, i);
+  if (p.tile == 0)
     return f16 ? launch_rows<Act::F16, EPI_SWIGLU>(g, st) : launch_rows<Act::BF16, EPI_SWIGLU>(g, st);
-  const Plan p = plan_of(NT, t, i, 2, ceil_div(h, 64), 1);
   return f16 ? launch_tiles<Act::F16, false, false, EPI_SWIGLU>(g, p, st)
              : launch_tiles<Act::BF16, false, false, EPI_SWIGLU>(g, p, st);
 }
@@ -1094,8 +1033,8 @@ struct GradWork {
 GradWork grad_work(void* base, int64_t t, int64_t h, int64_t i) {
   const int64_t groups = ceil_div(i, kMaxGroup);
   GradWork w{};
-  w.dx = plan_of(DX, t, h, 1, 2 * ceil_div(i, 64), 1);
-  w.dw = plan_of(DW, i, h, 1, ceil_div(t, 64), 2);
+  w.dx = dx_plan(t, h, i);
+  w.dw = dw_plan(t, h, i);
   auto take = [&](int64_t bytes) {
     uint8_t* p = static_cast<uint8_t*>(base) + w.bytes;
     w.bytes += align256(bytes);

@@ -1,0 +1,92 @@
+"""Every kernel, tile and K split of the dense products (test_dense_plan.py checks that the
+shapes below take them all) against 64 bits, repeated and guarded."""
+import pytest
+import torch
+
+import tests.test_gpu_dense as base
+from tests.helpers import require_gpu
+from tests.test_gpu_dense import ALL_TYPES, TYPES, U, codes, gen_of, half_step, randn, swiglu_inputs, tiny, within
+
+pytestmark = pytest.mark.gpu
+
+# t, k, n: few rows (one and two fragments a wave), then tiles of 64, 128 and 256, each with K whole and split
+INT8_SHAPES = [(5, 144, 33), (9, 208, 7001), (333, 1040, 1001), (20, 3328, 19), (204, 1664, 12738), (71, 8144, 8283),
+               (778, 64, 7681), (131, 7152, 5544), (5472, 6944, 133)]
+# t, h, i: forward 64 whole and split, 128 whole and split, 256 whole and split, ...
+SWIGLU_SHAPES = [(5, 72, 40), (9, 72, 3600), (21, 64, 72), (17, 1712, 72), (201, 792, 6848), (66, 3680, 4352),
+                 (471, 64, 6216), (146, 3968, 2936),
+                 # ... dx 128 whole and split, 256 whole (and dw 128 split), 256 split,
+                 (464, 6168, 64), (70, 6168, 2392), (2761, 4392, 72), (130, 5912, 3464),
+                 # ... dw 64 split, 256 whole and split
+                 (2241, 72, 64), (65, 6472, 920), (2626, 2336, 848)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    require_gpu()
+    import int4_group_quantized_g128_amd as lib
+    return lib
+
+
+@pytest.mark.parametrize("dt", ALL_TYPES)
+@pytest.mark.parametrize("t,k,n", INT8_SHAPES)
+def test_int8_linear(lib, t, k, n, dt):
+    base.test_int8_linear(lib, t, k, n, dt)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("t,h,i", SWIGLU_SHAPES)
+def test_swiglu_linear_forward(lib, t, h, i, dt):
+    base.test_swiglu_linear_forward(lib, t, h, i, dt)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("t,h,i", SWIGLU_SHAPES)
+def test_swiglu_linear_backward(lib, t, h, i, dt):
+    base.test_swiglu_linear_backward(lib, t, h, i, dt)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("t,h,i", [(17, 1712, 72), (66, 3680, 4352), (146, 3968, 2936), (70, 6168, 2392),
+                                   (130, 5912, 3464), (2241, 72, 64), (2761, 4392, 72), (2626, 2336, 848)])
+def test_split_products_repeat_and_write_only_their_outputs(lib, t, h, i, dt):
+    r, code = lib._lib.raw, lib._lib._DT[dt]
+    x, wg, wu, dh = swiglu_inputs(t, h, i, dt, 4)
+    ptr, stream = base.ptr, base.stream
+    ref, gu_ref = lib.swiglu_linear_forward(x, wg, wu, save=True)
+    grads = lib.swiglu_linear_backward(dh, x, wg, wu, gu_ref)
+    for fill in (0, 0xFF):   # a workspace of zeros and of NaN
+        b = base.Guarded()
+        out, gu = b.new(t, i, dtype=dt), b.new(t, 2, i, dtype=torch.float32)
+        nbytes = r.swiglu_linear_workspace_bytes(t, h, i)
+        work = b.new(max(nbytes, 16), dtype=torch.uint8).fill_(fill)
+        assert r.swiglu_linear_forward(ptr(x), ptr(wg), ptr(wu), t, h, i, code, ptr(out), ptr(gu), ptr(work), nbytes,
+                                       stream()) == 0
+        dx, dwg, dwu = b.new(t, h, dtype=dt), b.new(i, h, dtype=dt), b.new(i, h, dtype=dt)
+        nbytes = r.swiglu_linear_backward_workspace_bytes(t, h, i)
+        work = b.new(nbytes, dtype=torch.uint8).fill_(fill)
+        assert r.swiglu_linear_backward(ptr(dh), ptr(x), ptr(wg), ptr(wu), ptr(gu), t, h, i, code, ptr(dx), ptr(dwg),
+                                        ptr(dwu), ptr(work), nbytes, stream()) == 0
+        b.check()
+        assert torch.equal(out, ref) and torch.equal(gu, gu_ref)
+        assert all(torch.equal(a, c) for a, c in zip((dx, dwg, dwu), grads))
+
+
+@pytest.mark.parametrize("t,k,n", [(20, 3328, 19), (71, 8144, 8283), (131, 7152, 5544)])
+def test_split_int8_products_repeat_and_write_only_their_output(lib, t, k, n):
+    r = lib._lib.raw
+    g = gen_of(t + n)
+    q, wq = codes(g, t, k), codes(g, n, k)
+    s, ws = torch.rand(t, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    for dt in ALL_TYPES:
+        ref = lib.int8_linear_forward(q, s, wq, ws, out_dtype=dt)
+        for fill in (0, 0xFF):
+            b = base.Guarded()
+            y = b.new(t, n, dtype=dt)
+            nbytes = r.int8_linear_workspace_bytes(t, k, n)
+            assert nbytes > 0
+            work = b.new(nbytes, dtype=torch.uint8).fill_(fill)
+            assert r.int8_linear_forward(base.ptr(q), base.ptr(s), t, k, base.ptr(wq), base.ptr(ws), n, None,
+                                         lib._lib._DT[dt], base.ptr(y), base.ptr(work), nbytes, base.stream()) == 0
+            b.check()
+            assert torch.equal(y, ref)
