@@ -90,3 +90,48 @@ def test_split_int8_products_repeat_and_write_only_their_output(lib, t, k, n):
                                          lib._lib._DT[dt], base.ptr(y), base.ptr(work), nbytes, base.stream()) == 0
             b.check()
             assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("t,h,i", [(70, 136, 72), (130, 264, 520), (17, 1712, 72)])
+def test_swiglu_linear_gradient_along_itself(lib, t, h, i, dt):
+    """Forward and backward pass against differences of the 64-bit loss sum(dh h) along the sign
+    of its own gradient (by automatic differentiation), where the difference is the sum of the
+    gradient's magnitudes, and against that gradient element by element.
+
+    A gradient entry carries one rounding of the result (half a step of it), one of dg and du
+    (half a step of every term of its sum) and fp32 sums of h, then of i or t terms:
+    |dg| <= 1.1 |dh u|, |du| <= |dh g|."""
+    x, wg, wu, dh = swiglu_inputs(t, h, i, dt, 2)
+    _, gu = lib.swiglu_linear_forward(x, wg, wu, save=True)
+    grads = [v.double() for v in lib.swiglu_linear_backward(dh, x, wg, wu, gu)]
+    p = [v.double().requires_grad_() for v in (x, wg, wu)]
+    d = dh.double()
+
+    def loss(x, wg, wu):
+        g = x @ wg.T
+        return (d * (g * torch.sigmoid(g)) * (x @ wu.T)).sum()
+
+    auto = torch.autograd.grad(loss(*p), p)
+    p = [v.detach() for v in p]
+    xa, ga, ua = (v.abs() for v in p)
+    # g and u carry 2 h u of their sums' magnitudes, so do dg and du of theirs (|sig''| < 1)
+    eg, eu = 2 * h * U * (xa @ ga.T), 2 * h * U * (xa @ ua.T)
+    g, u = (p[0] @ p[1].T).abs(), (p[0] @ p[2].T).abs()
+    ag, au = 1.1 * d.abs() * u, d.abs() * g
+    hs = half_step(dt)
+    fg = hs * ag + d.abs() * (1.1 * eu + u * eg) + 32 * U * d.abs() * u * (1 + g) + tiny(dt)
+    fu = hs * au + d.abs() * 1.1 * eg + 32 * U * au + tiny(dt)
+    n = max(i, t) * 4 * U
+    tols = [(fg + n * ag) @ ga + (fu + n * au) @ ua, (fg + n * ag).T @ xa, (fu + n * au).T @ xa]
+    e = 1e-5
+    for j, name in enumerate(("dx", "dw_gate", "dw_up")):
+        tol = 1.01 * (tols[j] + hs * (auto[j].abs() + tols[j])) + tiny(dt)
+        within(grads[j], auto[j], tol, name)
+        v = torch.sign(auto[j])
+        plus, minus = list(p), list(p)
+        plus[j], minus[j] = p[j] + e * v, p[j] - e * v
+        diff = (loss(*plus) - loss(*minus)) / (2 * e)
+        assert tol.sum() < 0.25 * diff, "the tolerance is well below what it measures"
+        # (the differences' own error: e^2 and 2^-53 / e of the loss's terms)
+        assert abs((grads[j] * v).sum() - diff) <= tol.sum() + 1e-6 * diff, name
