@@ -601,7 +601,8 @@ Q4_API int quantize_int8_channel(const void* w, int w_dtype, int64_t n, int64_t 
  *           (quantize_int8_channel), row-major as they are.
  *  bias     device [n] fp32 or NULL.
  *  y        device [t][n] of dtype y_dtype (Q4_F32, Q4_F16, Q4_BF16):
- *           float(acc) * (s[t] * w_s[n]) + bias[n] in fp32, rounded once to y_dtype.
+ *           float(acc) * (s[t] * w_s[n]) + bias[n] in fp32 (the outer product and the sum
+ *           in one fma), rounded once to y_dtype.
  *  workspace device buffer of int8_linear_workspace_bytes(t, k, n) bytes (may be 0): INT32
  *           sums of the K slices where a product has few output tiles.
  *  The INT32 sums are exact, so equal inputs give equal bits on every path.  A NaN scale

@@ -123,8 +123,9 @@ Q4_DEVICE f32x4_t result4(typename Num<A>::acc_t v, typename Num<A>::acc_t v2, f
   f32x4_t y;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // int8: the INT32 sum becomes fp32 (24 bits), then one product of the scales, one with it
-    if constexpr (EPI == EPI_INT8) y[i] = float(v[i]) * (sm * cs.s[i]) + cs.b[i];
+    // int8: the INT32 sum becomes fp32 (24 bits), the scales' product is rounded, and one fma
+    // joins them and the bias (spelt out, so that every kernel rounds alike)
+    if constexpr (EPI == EPI_INT8) y[i] = __builtin_fmaf(float(v[i]), sm * cs.s[i], cs.b[i]);
     else if constexpr (EPI == EPI_SWIGLU) y[i] = swiglu(v[i], v2[i]);
     else if constexpr (EPI == EPI_SCALED) y[i] = v[i] * sm;
     else y[i] = v[i];

@@ -64,3 +64,9 @@ def test_gpu_shapes_take_every_plan(plan, product):
     assert len(reachable) >= 6
     tested = {plan(product, *s) for s in (INT8_SHAPES if product == "int8" else SWIGLU_SHAPES)}
     assert reachable <= tested, sorted(reachable - tested)
+
+
+def test_equal_bits_shapes_take_every_plan(plan):
+    from tests.test_gpu_dense_paths import EQUAL_BITS
+    taken = {plan("int8", t, k, n) for rows, k, n in EQUAL_BITS for t in rows}
+    assert taken == {(0, False)} | {(tile, split) for tile in (64, 128, 256) for split in (False, True)}

@@ -1,5 +1,5 @@
 """Every kernel, tile and K split of the dense products (test_dense_plan.py checks that the
-shapes below take them all) against 64 bits, repeated and guarded."""
+shapes below take them all) against 64 bits, for equal bits, repeated and guarded."""
 import pytest
 import torch
 
@@ -19,6 +19,8 @@ SWIGLU_SHAPES = [(5, 72, 40), (9, 72, 3600), (21, 64, 72), (17, 1712, 72), (201,
                  (464, 6168, 64), (70, 6168, 2392), (2761, 4392, 72), (130, 5912, 3464),
                  # ... dw 64 split, 256 whole and split
                  (2241, 72, 64), (65, 6472, 920), (2626, 2336, 848)]
+# row counts that take every plan at one k, n (odd; a multiple of 8)
+EQUAL_BITS = [((1, 5, 17, 130, 200, 400, 700, 1700), 7264, 4835), ((1, 17, 130, 200, 400, 700, 1700), 7264, 4840)]
 
 
 @pytest.fixture(scope="module")
@@ -44,6 +46,34 @@ def test_swiglu_linear_forward(lib, t, h, i, dt):
 @pytest.mark.parametrize("t,h,i", SWIGLU_SHAPES)
 def test_swiglu_linear_backward(lib, t, h, i, dt):
     base.test_swiglu_linear_backward(lib, t, h, i, dt)
+
+
+@pytest.mark.parametrize("dt", ALL_TYPES)
+@pytest.mark.parametrize("rows,k,n", EQUAL_BITS)
+def test_int8_linear_equal_bits_on_every_plan(lib, rows, k, n, dt):
+    """A row's result does not depend on the rows beside it, with and without a bias, and is
+    what the definition gives in fp32: one rounding of the INT32 sum, one of the scales'
+    product, one of the product of both with the bias added."""
+    g = gen_of(k + n)
+    q, wq = codes(g, max(rows), k), codes(g, n, k)
+    s, ws = torch.rand(max(rows), generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    acc = q.double() @ wq.double().T   # exact: below 2^53
+    for bias in (None, randn(g, n, std=1e4)):
+        full = lib.int8_linear_forward(q, s, wq, ws, bias=bias, out_dtype=dt)
+        # sum and scales' product have 24 bits each, so their product is exact in fp64; adding the
+        # bias there rounds once more before fp32 does, which is off by one step at most
+        want = acc.float().double() * (s[:, None] * ws).double() + (0 if bias is None else bias.double())
+        exact = want.float()
+        if bias is None:
+            assert torch.equal(full, exact.to(dt))
+        else:
+            same = full == exact.to(dt)   # (infinities of fp16 among them)
+            off = (full.double() - exact.to(dt).double()).abs()
+            assert (same | (off <= torch.finfo(dt).eps * want.abs() * (1 + 2.0 ** -7) + tiny(dt))).all()
+            assert same.double().mean() > 0.999
+        for t in rows:
+            got = lib.int8_linear_forward(q[:t], s[:t], wq, ws, bias=bias, out_dtype=dt)
+            assert torch.equal(got, full[:t]), (t, bias is not None)
 
 
 @pytest.mark.parametrize("dt", TYPES)
