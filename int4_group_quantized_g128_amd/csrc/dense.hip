@@ -181,8 +181,8 @@ Q4_DEVICE void store8(void* c, int dtype, int64_t idx, f32x4_t y0, f32x4_t y1, i
     else *p = o;
   } else {
     const bool vec = (ld & 3) == 0;
-    store4(c, dtype, idx, y0, count, vec);
-    store4(c, dtype, idx + 4, y1, count - 4, vec);
+    store4(c, dtype, idx, y0, min(count, 4), vec);
+    store4(c, dtype, idx + 4, y1, min(count - 4, 4), vec);
   }
 }
 

@@ -76,6 +76,27 @@ def test_int8_linear_equal_bits_on_every_plan(lib, rows, k, n, dt):
             assert torch.equal(got, full[:t]), (t, bias is not None)
 
 
+@pytest.mark.parametrize("t,k,n", [(130, 144, 257 + e) for e in range(8)] +
+                         [(778, 64, 7680 + e) for e in (0, 4, 1)] + [(204, 1664, 12736 + e) for e in (0, 4, 2)])
+def test_int8_linear_every_row_end(lib, t, k, n):
+    """Rows that end anywhere in a lane's eight columns, stored in vectors of 8 and 4 or singly as
+    the row length allows, between guards."""
+    r = lib._lib.raw
+    g = gen_of(n)
+    q, wq = codes(g, t, k), codes(g, n, k)
+    s, ws = torch.rand(t, generator=g, device="cuda") * 1e-3, torch.rand(n, generator=g, device="cuda") * 1e-3
+    want = ((q.double() @ wq.double().T).float().double() * (s[:, None] * ws).double()).float()
+    for dt in ALL_TYPES:
+        b = base.Guarded()
+        y = b.new(t, n, dtype=dt)
+        nbytes = r.int8_linear_workspace_bytes(t, k, n)
+        work = b.new(max(nbytes, 16), dtype=torch.uint8)
+        assert r.int8_linear_forward(base.ptr(q), base.ptr(s), t, k, base.ptr(wq), base.ptr(ws), n, None,
+                                     lib._lib._DT[dt], base.ptr(y), base.ptr(work), nbytes, base.stream()) == 0
+        b.check()
+        assert torch.equal(y, want.to(dt))
+
+
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("t,h,i", [(17, 1712, 72), (66, 3680, 4352), (146, 3968, 2936), (70, 6168, 2392),
                                    (130, 5912, 3464), (2241, 72, 64), (2761, 4392, 72), (2626, 2336, 848)])
