@@ -883,6 +883,8 @@ def _norm_desc(res, y, w_post, gate, alpha, w_pre, eps):
         _arg(y, "y", dtype, shape, dev)
     kind = Q4_GATE_NONE
     if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a tensor")
         g = tuple(gate.shape)
         kind = {(rows, cols): Q4_GATE_ELEMENT, (rows, 1): Q4_GATE_TOKEN, (cols,): Q4_GATE_CHANNEL}.get(g)
         if kind is None:

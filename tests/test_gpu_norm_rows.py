@@ -65,3 +65,12 @@ def test_many_rows_codes_and_repeats(lib, t, c, dt):
     tail = {k: v[-3:].clone() if v.shape[0] == t else v for k, v in kw.items()}
     _, q3, s3 = lib.block_norm_forward(quantize=True, **tail)
     assert torch.equal(q[-3:], q3) and torch.equal(s[-3:], s3)
+
+
+def test_gate_that_is_no_tensor(lib):
+    x = torch.zeros(4, 64, device="cuda")
+    for gate in (0.5, [1.0] * 64):
+        with pytest.raises(TypeError):
+            lib.block_norm_forward(x, y=x, gate=gate)
+        with pytest.raises(TypeError):
+            lib.block_norm_backward(x, None, x, y=x, gate=gate)
