@@ -617,7 +617,8 @@ Q4_API int int8_linear_forward(const int8_t* q, const float* s, int64_t t, int64
 
 /*
  * swiglu_linear_forward / swiglu_linear_backward -- the gated projection of a SwiGLU FFN in
- * 16 bits, both products, the activation and their product in one launch:
+ * 16 bits, both products, the activation and their product in one launch (two where few
+ * tokens split K):
  *   h = silu(g) * u,   g = x w_gate^T,   u = x w_up^T,   silu(g) = g / (1 + e^-g)
  * (the first half of the FFN that moe_int4_ffn_forward computes from INT4 weights).
  *  x        device [t][h]; w_gate, w_up device [i][h]; h_out device [t][i]; dtype Q4_BF16
@@ -670,8 +671,10 @@ Q4_API int swiglu_linear_backward(const void* dh, const void* x, const void* w_g
  *  dw_post, dw_pre  device [cols] fp32 (with the weights).
  *  dgate    channel: fp32 [cols]; token: fp32 [rows]; element: dtype [rows][cols].
  *  workspace device buffer of block_norm_workspace_bytes bytes (partial weight gradients).
- *  Weight gradients are added in a fixed order: equal inputs give equal bits.  dres may be dr
- *  itself; other outputs may not alias inputs.
+ *  Weight gradients are added in a fixed order: equal inputs give equal bits.  (Rows of 1025 to
+ *  2048 columns, a multiple of 8, are summed in another order from 1024 rows on: the same row
+ *  may differ there in its last bits, and a code of n by one, from a call of fewer rows.)  dres
+ *  may be dr itself; other outputs may not alias inputs.
  *  Requires 1 <= cols <= 16384, rows >= 0, eps > 0, finite alpha.  rows == 0: the forward
  *  is a no-op, the backward sets the weight and channel gate gradients to zero.
  */

@@ -740,7 +740,8 @@ def int4_w4a8_group_acc(q, w_dev, n, asymmetric=False):
 # ------------------------------------------------------------------ dense operators
 # These run at a few microseconds per call for one token, so their checks take one pass per
 # tensor and the stream comes as a raw handle (through torch's public calls where a torch
-# lacks the direct ones).
+# lacks the direct ones).  Forward and backward passes are separate calls: no autograd graph
+# is recorded, also where an input requires a gradient.
 _16BIT = (torch.float16, torch.bfloat16)
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 
@@ -841,7 +842,8 @@ def _swiglu_args(x, w_gate, w_up):
 
 def swiglu_linear_forward(x, w_gate, w_up, save=False):
     """h [t, i] = silu(x w_gate^T) * (x w_up^T) for x [t, h] and weights [i, h] (fp16 or bf16).
-    With ``save`` -> (h, gu): gu [t, 2, i] holds the two products in fp32 for the backward pass."""
+    With ``save`` -> (h, gu): gu [t, 2, i] holds the two products in fp32 for the backward pass,
+    swiglu_linear_backward (a call of its own: the result carries no autograd graph)."""
     t, h, i, dev = _swiglu_args(x, w_gate, w_up)
     dtype, device = x.dtype, x.device
     out = torch.empty((t, i), dtype=dtype, device=device)
@@ -898,7 +900,8 @@ def block_norm_forward(res, y=None, w_post=None, gate=None, alpha=1.0, w_pre=Non
     """r = res + alpha * gate * N(y; w_post) and n = N(r; w_pre), N the RMS norm with a weight,
     gate one value per channel [cols], per token [rows, 1] or per element [rows, cols].
     -> (r, n), or (r, q, s) with ``quantize``: n as per-token INT8 codes and scales.  Without
-    y, r is res; without w_pre, n (and q, s) is None."""
+    y, r is res; without w_pre, n (and q, s) is None.  Gradients come from block_norm_backward
+    (a call of its own: the results carry no autograd graph)."""
     d = _norm_desc(res, y, w_post, gate, alpha, w_pre, eps)
     r = res if y is None else torch.empty_like(res)
     n = q = s = None

@@ -190,7 +190,7 @@ Q4_DEVICE void store8(void* c, int dtype, int64_t idx, f32x4_t y0, f32x4_t y1, i
 // copies are done), 64 fp32 columns (or 32) per row, so that a lane holds 8 consecutive
 // columns of one row, or 4 of both projections, stores are whole lines, and the code that
 // turns sums into results stands in one short loop (stored from the accumulators it was 30 KB
-// of code, at the same speed).
+// of code: forward with g and u 277 -> 270 us at 4096 x 2048 x 8192).
 // 16-byte chunk c of row r lies at c ^ (r % chunks of a row), against bank conflicts.
 template <int COLS, typename V>
 Q4_DEVICE void turn_in(uint32_t lds, int row, int chunk, V v) {
@@ -641,9 +641,11 @@ __global__ void __launch_bounds__(256) k_dense_join(DenseArgs g) {
 // columns of y; for swiglu 8 gate and 8 up rows, so that twice as many workgroups share the
 // reading); the 8 waves of a workgroup own NF fragments' rows, take the 128-byte K steps in
 // turn and feed the matrix core straight from global memory (16 bytes per lane, two loads
-// cover a step's whole lines), four steps in flight, then add their sums through LDS in wave
-// order.  2048 / 8192 gated projection, one row: 12.2 us, 5.5 TB/s (with non-temporal weight
-// loads the second load of a line misses again: 14.6 against 14.0 us on another card).
+// cover a step's whole lines), four steps per turn of the loop, then add their sums through LDS
+// in wave order.  The compiler spreads a turn's 16 loads (24 of NF = 2) over its products: 8 (6)
+// are in flight at a time, in 64 registers.  2048 / 8192 gated projection, one row: 12.2 us, 5.5
+// TB/s (with non-temporal weight loads the second load of a line misses again: 14.6 against
+// 14.0 us on another card).
 template <Act A, int EPI, int W, int NF>
 __global__ void __launch_bounds__(64 * W) k_dense_rows(DenseArgs g) {
   typedef Num<A> T;
@@ -747,9 +749,9 @@ Q4_DEVICE void swiglu_grad8(const uint16_t* __restrict__ dh, const float* __rest
 // element).  g and u are kept in fp32: rounding them to 16 bits as well made the bf16
 // gradients 1.8 times as far from the 64-bit ones as one rounding of the result does, fp32
 // 1.4 times.  The rest is the rounding of dg and du themselves: as matrix-core operands they
-// have the type of x and the weights, and a second operand for what a rounding leaves would
-// double the work of all three products (8 T H I operations more, 0.38 ms at 4096 x 2048 x
-// 8192 and this card's 1437 TFLOP/s).
+// have the type of x and the weights.  With a second operand for what that rounding leaves the
+// gradients are as near as one rounding (0.0017 instead of 0.0023 relative), but all three
+// products double: 524 -> 981 us backward at 4096 x 2048 x 8192.
 __global__ void __launch_bounds__(256) k_swiglu_grad(const uint16_t* __restrict__ dh, const float* __restrict__ gu,
                                                      int64_t t, int64_t inter, uint16_t* __restrict__ dg,
                                                      uint16_t* __restrict__ du) {
@@ -955,9 +957,10 @@ hipError_t launch_rows_as(const DenseArgs& g, hipStream_t st) {
 }
 
 // Two fragments per wave halve the reads of x, which count from a few rows on, as long as
-// enough workgroups are left (both measured with non-temporal weight loads): 7168 x 7168
-// INT8, 16 rows, 18.8 -> 16.3 us (one row 13.8 -> 13.1); but 8192 x 2048, 64 workgroups
-// instead of 128, 10.5 -> 15.1 us.
+// enough workgroups are left: 7168 x 7168 INT8 12.4 -> 11.1 us at 5 rows, 15.1 -> 12.3 at 16,
+// gated 2048 / 8192 13.4 -> 12.3 at 5; but INT8 8192 x 2048, 64 workgroups instead of 128, 9.6
+// -> 13.0 at 16, gated 7168 / 2048 15.1 -> 21.2.  (Where the rule takes two and K is long, a
+// gated projection can lose: 4096 / 6144 20.5 -> 23.0 at 5 rows, 24.9 -> 25.1 at 16.)
 template <Act A, int EPI>
 hipError_t launch_rows(const DenseArgs& g, hipStream_t st) {
   const int64_t wgs = ceil_div(g.N, EPI == EPI_SWIGLU ? 16 : 32);

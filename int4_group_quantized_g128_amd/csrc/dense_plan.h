@@ -17,12 +17,15 @@ enum Kind { NT = 0 /* forward, KC x KC */, DX = 1 /* KC x MC */, DW = 2 /* MC x 
 // Estimated time (us) of a product of `steps` 128-byte K steps with square tiles of `bm` and
 // K in `ks` slices.  Per kind and tile size: time of a step when the workgroup is alone on
 // its CU (a chain of copy, LDS and matrix-core latencies) and when the CU is full (per
-// workgroup), time of a workgroup's start and end.  The forward figures are fitted to 75
-// shapes of both forward products (17 to 2048 rows, K 512 to 16384), each timed with the three
-// tiles and up to 8 splits: the plan below then lies within 2 % of the fastest of them on
-// every one (a rule that only counted workgroups lost up to 70 %).  The backward figures are
-// fitted to 6 shapes with 15 plans each (64 to 2048 tokens; rms error of an estimate 12 % for
-// dx, 7 % for dW).
+// workgroup), time of a workgroup's start and end.  They were fitted to 75 forward shapes (17
+// to 2048 rows, K 512 to 16384) and 6 backward ones with an earlier end of a tile and rank plans
+// rather than predict times: the estimate leaves out the results' bytes (gated 4096 x 2048 x
+// 8192 with g and u 173 us against 274 measured, INT8 333 x 1040 x 1001 4.3 against 8.1).
+// Today's kernels, each of the three tiles with K in 1, 2, 4 and 8 slices against the plan: of 76
+// forward shapes (24 to 4096 rows, with and without g and u) 72 within 8 % of the fastest, the
+// worst INT8 333 x 7168 x 7168 (44 us, 64 / 1 36) and gated 2048 x 512 x 1408 with g and u (22.5,
+// 128 / 1 17); of 20 backward passes 19 within 5 %, the worst 2048 x 1000 x 2728 (105, dx by
+// 128 / 2 95).  (A rule that only counted workgroups lost up to 70 %.)
 inline double plan_us(Kind kind, int64_t m, int64_t n, int panels, int64_t steps, int batches, int bm, int64_t ks) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
   static const int held[3] = {3, 2, 1};   // workgroups a CU holds

@@ -216,8 +216,10 @@ template <int WPR> constexpr int threads_per_wg() { return 64 * WPR * rows_per_w
 template <int WPR, bool VEC> constexpr bool fetch_ahead() { return VEC && WPR < 16; }
 
 // Every workgroup walks rows base, base + step, ...: the weights stay in its registers, and
-// the next row is on its way while the current one is reduced.  Four waves per SIMD: 4096 x
-// 7168 bf16 with a channel gate, two workgroups per CU.
+// the next row is on its way while the current one is reduced.  16-bit rows of vectors run four
+// waves per SIMD (4096 x 7168 bf16 with a channel gate: two workgroups per CU, 41 us, 5.7 TB/s);
+// fp32 ones two or three, without loss (4096 x 7168 95 us, 4.9 TB/s).  Single columns are bound by
+// their accesses of one element: 4096 x 7167 bf16 121 us.
 template <typename T, int WPR, int NV, bool VEC>
 __global__ void __launch_bounds__(threads_per_wg<WPR>()) __attribute__((amdgpu_waves_per_eu(sizeof(typename Elem<T>::type) == 2 && VEC ? 4 : 1))) k_block_norm_fwd(BlockNormArgs a, void* r_out, void* n_out,
                                                                           int8_t* q_out, float* s_out) {
@@ -301,7 +303,11 @@ __global__ void __launch_bounds__(threads_per_wg<WPR>()) __attribute__((amdgpu_w
 
 // As the forward kernel; the contributions to the weight (and channel gate) gradients are
 // added in registers, and partial [workgroups][3][cols] gets one set per workgroup, which
-// k_norm_grad_sum adds in order.
+// k_norm_grad_sum adds in order.  One kernel for every combination of parts: up to 8192 columns
+// in 16 bits its 250 registers hold (4096 x 7168 bf16 85 us in all, 4.1 TB/s), fp32 rows of up
+// to 4096 take 297 (one wave per SIMD; 4096 x 4096 93 us, 4.3 TB/s).  Beyond that it spills:
+// fp32 rows of 4104 to 8192 columns 1140 bytes per lane (4096 x 7168 1680 us), rows above 8192
+// 336 to 460 in every type (2048 x 16384 bf16 383 us).
 template <typename T, int WPR, int NV, bool VEC>
 __global__ void __launch_bounds__(threads_per_wg<WPR>())
     k_block_norm_bwd(BlockNormArgs a, const void* dr, const void* dn, void* dres, void* dy, void* dgate,
@@ -455,9 +461,10 @@ __global__ void __launch_bounds__(1024) k_norm_grad_sum(const float* __restrict_
   }
 }
 
-// Workgroups of a pass over the rows: as many as are on the chip at once (16 waves per CU in
-// the forward pass, 8 in the backward one, which holds twice as much per thread and writes
-// three partial rows of fp32 per workgroup).
+// Workgroups of a pass over the rows: 16 waves per CU in the forward pass, 8 in the backward
+// one, which holds twice as much per thread and writes three partial rows of fp32 per workgroup.
+// That is what a CU holds at once of 16-bit rows with two vectors per lane; of fp32 ones it holds
+// 8 to 12 and 4, and the other workgroups start as these end.
 int64_t pass_wgs(int64_t rows, int wpr, bool backward) {
   const int rpw = wpr == 1 ? 4 : 1;
   const int64_t fill = 256 * std::max(1, (backward ? kBwdWaves : 16) / (wpr * rpw));
