@@ -133,3 +133,18 @@ def test_fp16_gradients_captured(lib):
         want = lib.swiglu_linear_backward(dh, x, wg, wu, gu)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), rep
+
+
+def test_fp16_gradients_offsets_past_32_bits(lib):
+    """More than 2^31 elements of dh, all rows but the last ones zero: the weight gradients are
+    those of the last rows, and so are their dx."""
+    t, h, i, tail = 270000, 8, 8192, 100
+    few = inputs(tail, h, i, "mixed")
+    dh, x, gu = (torch.zeros(t, *v.shape[1:], dtype=v.dtype, device="cuda") for v in (few[0], few[1], few[4]))
+    dh[-tail:], x[-tail:], gu[-tail:] = few[0], few[1], few[4]
+    _, _, ref = reference(*few)
+    dx, dwg, dwu = lib.swiglu_linear_backward(dh, x, few[2], few[3], gu)
+    assert not dx[:-tail].any()
+    # (the weight gradients' sums run over the zero rows too, which adds no rounding)
+    for v, (r, tol) in zip((dx[-tail:], dwg, dwu), ref):
+        within(v, r, tol)
