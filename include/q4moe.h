@@ -703,6 +703,109 @@ Q4_API int block_norm_backward(const q4_block_norm_t* norm, const void* dr, cons
                                hipStream_t stream);
 
 /*
+ * Tokens sorted by expert and back, with their weights, and the gradients of both: the steps
+ * around the experts' products (page "MoE推理优化实战：4bit存储+INT8计算的W4A8路线解析" §1: tokens are
+ * dispatched to their experts and the results combined afterwards), inside
+ * moe_int4_ffn_forward fused into its launches, here on their own for experts of any kind
+ * (fp8_linear_forward by expert).  Used together: moe_route_topk -> moe_dispatch_forward ->
+ * fp8_linear_forward -> quantize_fp8_tokens -> fp8_linear_forward -> moe_combine_forward.
+ * Rows are of h elements of dtype Q4_F32, Q4_F16 or Q4_BF16; slot s = t_idx k + j.
+ *
+ * moe_dispatch_forward -- sorts the slots by expert, in slot order within an expert, and
+ * writes each token's row once per held slot in that order.
+ *  x        device [t][h].
+ *  ids      device [t][k] int32: the experts; this call holds [first, first + e).  A slot of
+ *           another expert (any other value) is dropped.  An expert may come twice in a token.
+ *  out      device [t k][h]: out[inv[t][j]] = x[t]; or NULL and
+ *  q, s     device [t k][h] e4m3 codes and [ceil(h / 128)][t k] fp32 scales of these rows, by
+ *           quantize_fp8_tokens' rule along the row (h % 16 == 0).
+ *           Rows from offsets[e] on are left as they were.
+ *  offsets  device [e + 1] int32: the experts' first rows; offsets[e]: the held slots.
+ *  perm     device [t k] int32: row -> slot, -1 from offsets[e] on.
+ *  inv      device [t][k] int32: slot -> row, -1 for a dropped slot.
+ *  workspace device buffer of moe_dispatch_workspace_bytes(t, k, e) bytes (may be 0).
+ *  t == 0 sets offsets to 0.
+ * moe_dispatch_backward -- dx[t] = sum over its held slots of dxp[inv[t][j]].
+ * moe_combine_forward -- out[t] = sum_j weights[t][j] y[inv[t][j]] (+ add[t]); weights device
+ *  [t][k] fp32 or NULL (ones); add device [t][h] or NULL (the shared expert's output); out may be
+ *  add.  y device [t k][h].  A token without held slots gets 0 (+ add).
+ * moe_combine_backward -- dy[inv[t][j]] = weights[t][j] dout[t] and dw[t][j] = <dout[t],
+ *  y[inv[t][j]]> (fp32; 0 for a dropped slot).  Other rows of dy are left as they were.  Without
+ *  weights, dw is NULL and y may be.  (The gradient to add is dout.)
+ * Sums are fp32, in ascending j (dw: a fixed order), rounded once.  Values of inv outside
+ * [0, t k) count as dropped; rows that are not read may hold anything.  Outputs may not alias
+ * inputs except as stated.
+ *  Requires 0 <= t < 2^23, 1 <= k <= 4096, t k < 2^26, 1 <= h <= 2^20, 1 <= e <= 4096,
+ *  first >= 0.
+ */
+Q4_API size_t moe_dispatch_workspace_bytes(int64_t t, int32_t k, int32_t e);
+Q4_API int moe_dispatch_forward(const void* x, int dtype, int64_t t, int64_t h, const int32_t* ids, int32_t k,
+                                int32_t first, int32_t e, void* out, uint8_t* q, float* s, int32_t* offsets,
+                                int32_t* perm, int32_t* inv, void* workspace, size_t ws_bytes, hipStream_t stream);
+Q4_API int moe_dispatch_backward(const void* dxp, int dtype, int64_t t, int64_t h, const int32_t* inv, int32_t k,
+                                 void* dx, hipStream_t stream);
+Q4_API int moe_combine_forward(const void* y, int dtype, int64_t t, int64_t h, const int32_t* inv, const float* weights,
+                               const void* add, int32_t k, void* out, hipStream_t stream);
+Q4_API int moe_combine_backward(const void* dout, const void* y, int dtype, int64_t t, int64_t h, const int32_t* inv,
+                                const float* weights, int32_t k, void* dy, float* dw, hipStream_t stream);
+
+/*
+ * 8-bit floating point (e4m3, OCP: largest value 448) with a scale for each block of 128, for one
+ * matrix or for the experts of a layer: next to int8_linear_forward, whose one scale per token
+ * and channel a few large channels spoil.
+ *
+ * quantize_fp8_tokens -- codes of x in groups of 128: s = amax / 448 (IEEE fp32), q = e4m3(x / s)
+ * (IEEE fp32 quotient, half to even); a zero scale gives codes 0; a group with an infinity or a
+ * NaN gets codes 0 and the scale NaN (results that it enters are NaN).
+ *  x        device [t][k] of dtype Q4_F32, Q4_F16 or Q4_BF16; gated: [t][2 k], each row g | u, and
+ *           what is quantised is silu(g) u in fp32 (silu(g) = g / (1 + e^-g)).
+ *  q, s     along the row: device [t][k] codes and [ceil(k / 128)][t] fp32 scales, or NULL.
+ *  q_col, s_col  along the tokens (the weight gradient sums over them): device [t][k] codes and
+ *           [groups][k] fp32 scales, or NULL (not with gated).  Without offsets the groups are rows
+ *           128 g .. + 127, groups = ceil(t / 128); with offsets they start anew at each expert's
+ *           first row and are counted through in expert order (room: t / 128 + min(e, t) groups).
+ *  offsets  device [e + 1] int32 (moe_dispatch_forward's), or NULL: rows from offsets[e] on are
+ *           left out (their codes and scales stay as they were).
+ * quantize_fp8_blocks -- weights w device [e][n][k] by blocks of 128 x 128: q [e][n][k], s fp32
+ *  [e][ceil(n / 128)][ceil(k / 128)], the same rule.
+ *
+ * fp8_linear_forward -- y[t][n] = sum_g s[g][t] w_s[n / 128][g] sum_{k in group g} q[t][k] w_q[n][k].
+ *  q, s     device token codes and scales along the row.    w_q, w_s: quantize_fp8_blocks' codes.
+ *  offsets  NULL: one matrix w_q [n][k] (e = 1).  Else device [e + 1] int32, ascending: rows
+ *           offsets[x] .. offsets[x + 1] - 1 take matrix x of w_q [e][n][k]; rows of no expert
+ *           are left as they were.  (Values are kept inside [0, t].)
+ *  y        device [t][n] of y_dtype Q4_F16 or Q4_BF16: fp32 sums of the groups, rounded once.
+ *  workspace device buffer of fp8_linear_workspace_bytes(t, k, n, e, offsets != NULL) bytes (may
+ *           be 0): K slices where a product has few output tiles.
+ *  Within a group the matrix core adds eight products at a time, dropping what lies 2^-13 below
+ *  the largest of them, and the eights in fp32 (about 1.4e-5 of the result's norm).
+ *
+ * fp8_linear_backward -- given dy device [t][n] of dtype Q4_F16 or Q4_BF16: dy is quantised along
+ * its rows for dx and along the tokens for dw, each by quantize_fp8_tokens' rule, and
+ *   dx = dy_hat W_hat,   dw = dy_hat^T x_hat
+ *  (x_hat, W_hat, dy_hat: codes times scales; the quantisers count as the identity).
+ *  x_q, x_s device q_col and s_col of the forward's x (with the same offsets).
+ *  dx       device [t][k]; dw device [e][n][k] (overwritten; zeros for an expert without rows);
+ *           of dtype, fp32 sums rounded once.  Rows of dx of no expert are left as they were.
+ *  workspace device buffer of fp8_linear_backward_workspace_bytes(...) bytes.
+ * Sums run in a fixed order: equal inputs give equal bits.  Outputs may not alias inputs.
+ *  Requires 0 <= t < 2^23, k % 16 == 0, 16 <= k <= 2^20, 1 <= n <= 2^20 (backward: n % 16 == 0,
+ *  n >= 16), 1 <= e <= 4096.  t == 0: a no-op, but for dw, which is set to zero.
+ */
+Q4_API int quantize_fp8_tokens(const void* x, int dtype, int64_t t, int64_t k, int gated, const int32_t* offsets,
+                               int32_t e, uint8_t* q, float* s, uint8_t* q_col, float* s_col, hipStream_t stream);
+Q4_API int quantize_fp8_blocks(const void* w, int dtype, int64_t e, int64_t n, int64_t k, uint8_t* q, float* s,
+                               hipStream_t stream);
+Q4_API size_t fp8_linear_workspace_bytes(int64_t t, int64_t k, int64_t n, int32_t e, int grouped);
+Q4_API int fp8_linear_forward(const uint8_t* q, const float* s, int64_t t, int64_t k, const uint8_t* w_q,
+                              const float* w_s, int64_t n, const int32_t* offsets, int32_t e, int y_dtype, void* y,
+                              void* workspace, size_t ws_bytes, hipStream_t stream);
+Q4_API size_t fp8_linear_backward_workspace_bytes(int64_t t, int64_t k, int64_t n, int32_t e, int grouped);
+Q4_API int fp8_linear_backward(const void* dy, int dtype, int64_t t, int64_t k, int64_t n, const uint8_t* x_q,
+                               const float* x_s, const uint8_t* w_q, const float* w_s, const int32_t* offsets,
+                               int32_t e, void* dx, void* dw, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
  * q4_set_stage_events -- optional per-stage timing markers for profiling tools.
  * When set (count >= Q4_NUM_STAGES, non-NULL arrays), every later
  * moe_int4_ffn_forward call on this thread records begin[s] before and end[s] after

@@ -137,6 +137,18 @@ _sig("swiglu_linear_backward", _int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
 _sig("block_norm_forward", _int, [ctypes.POINTER(Q4BlockNorm), _vp, _vp, _vp, _vp, _vp])
 _sig("block_norm_workspace_bytes", _sz, [ctypes.POINTER(Q4BlockNorm)])
 _sig("block_norm_backward", _int, [ctypes.POINTER(Q4BlockNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("moe_dispatch_workspace_bytes", _sz, [_i64, _i32, _i32])
+_sig("moe_dispatch_forward", _int, [_vp, _int, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _sz, _vp])
+_sig("moe_dispatch_backward", _int, [_vp, _int, _i64, _i64, _vp, _i32, _vp, _vp])
+_sig("moe_combine_forward", _int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp])
+_sig("moe_combine_backward", _int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp])
+_sig("quantize_fp8_tokens", _int, [_vp, _int, _i64, _i64, _int, _vp, _i32, _vp, _vp, _vp, _vp, _vp])
+_sig("quantize_fp8_blocks", _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp])
+_sig("fp8_linear_workspace_bytes", _sz, [_i64, _i64, _i64, _i32, _int])
+_sig("fp8_linear_forward", _int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _int, _vp, _vp, _sz, _vp])
+_sig("fp8_linear_backward_workspace_bytes", _sz, [_i64, _i64, _i64, _i32, _int])
+_sig("fp8_linear_backward", _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp])
 _sig("q4_set_stage_events", _int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _int])
 
 raw = _lib  # the C entry points, for tests of the ABI itself
@@ -939,3 +951,210 @@ def block_norm_backward(dr, dn, res, y=None, w_post=None, gate=None, alpha=1.0, 
     _call("block_norm_backward", _lib.block_norm_backward, dev, d, _dp(dr), _dp(dn), out["res"].data_ptr(),
           _dp(out["y"]), _dp(out["w_post"]), _dp(out["gate"]), _dp(out["w_pre"]), _dp(ws), nbytes)
     return out
+
+
+# ------------------------------------------------------------------ tokens by expert, e4m3 products
+# (checks, streams and autograd as for the dense operators)
+_dispatch_ws = functools.lru_cache(4096)(_lib.moe_dispatch_workspace_bytes)
+_fp8_linear_ws = functools.lru_cache(4096)(_lib.fp8_linear_workspace_bytes)
+_fp8_linear_bwd_ws = functools.lru_cache(4096)(_lib.fp8_linear_backward_workspace_bytes)
+_E4M3 = torch.float8_e4m3fn
+
+
+def _out(out, dtype, shape, like, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _arg(out, "out", dtype, shape, dev)
+    return out
+
+
+def _slots(inv, name, t, dev):
+    """A [t, k] int32 tensor of the slots -> k."""
+    k = _first(inv, (torch.int32,), name)[0][1]
+    _arg(inv, name, torch.int32, (t, k), dev)
+    return k
+
+
+def _offsets(offsets, dev):
+    """-> the number of experts (1 without offsets)."""
+    if offsets is None:
+        return 1
+    _need(offsets, torch.int32, "offsets", 1)
+    _arg(offsets, "offsets", torch.int32, offsets.shape, dev)
+    if offsets.shape[0] < 2:
+        raise ValueError("offsets must hold the first row of each expert and the end")
+    return offsets.shape[0] - 1
+
+
+def moe_dispatch_forward(x, ids, num_experts, first=0, quantize=False, out=None):
+    """Rows of x [t, h] sorted by expert: -> (xp [t k, h], offsets [num_experts + 1], perm [t k],
+    inv [t, k]) for the choices ids [t, k] int32; experts [first, first + num_experts) are held,
+    slots of others dropped (inv -1, perm -1 behind the held rows; rows of xp from offsets[-1] on
+    are not written).  With ``quantize`` -> (q, s, offsets, perm, inv): the rows as e4m3 codes
+    [t k, h] and scales [ceil(h / 128), t k] for fp8_linear_forward."""
+    (t, h), dev = _first(x, _FLOATS, "x")
+    k = _slots(ids, "ids", t, dev)
+    device, n = x.device, t * k
+    order = torch.empty(num_experts + 1 + (-(num_experts + 1)) % 4 + n + (-n) % 4 + n, dtype=torch.int32, device=device)
+    offsets = order[:num_experts + 1]
+    at = num_experts + 1 + (-(num_experts + 1)) % 4
+    perm = order[at:at + n]
+    inv = order[at + n + (-n) % 4:].view(t, k)
+    s = None
+    if quantize:
+        if out is not None:
+            raise ValueError("out is for rows, not for codes")
+        rows = torch.empty((n, h), dtype=_E4M3, device=device)
+        s = torch.empty((-(-h // 128), n), dtype=torch.float32, device=device)
+    else:
+        rows = _out(out, x.dtype, (n, h), x, dev)
+    nbytes = _dispatch_ws(t, k, num_experts)
+    ws = _scratch(nbytes, device)
+    _call("moe_dispatch_forward", _lib.moe_dispatch_forward, dev, x.data_ptr(), _DT[x.dtype], t, h, ids.data_ptr(), k,
+          first, num_experts, None if quantize else rows.data_ptr(), rows.data_ptr() if quantize else None, _dp(s),
+          offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), _dp(ws), nbytes)
+    return (rows, s, offsets, perm, inv) if quantize else (rows, offsets, perm, inv)
+
+
+def _sorted_rows(rows, name, inv):
+    """Rows [t k, h] and inv [t, k] -> t, k, h, GPU."""
+    (n, h), dev = _first(rows, _FLOATS, name)
+    t = _first(inv, (torch.int32,), "inv")[0][0]
+    k = _slots(inv, "inv", t, dev)
+    if n != t * k:
+        raise ValueError(f"{name} must have {t * k} rows, got {n}")
+    return t, k, h, dev
+
+
+def moe_dispatch_backward(dxp, inv):
+    """dx [t, h] = sum_j dxp[inv[t, j]]: the gradient of moe_dispatch_forward."""
+    t, k, h, dev = _sorted_rows(dxp, "dxp", inv)
+    dx = torch.empty((t, h), dtype=dxp.dtype, device=dxp.device)
+    _call("moe_dispatch_backward", _lib.moe_dispatch_backward, dev, dxp.data_ptr(), _DT[dxp.dtype], t, h,
+          inv.data_ptr(), k, dx.data_ptr())
+    return dx
+
+
+def moe_combine_forward(y, inv, weights=None, add=None):
+    """out [t, h] = sum_j weights[t, j] y[inv[t, j]] (+ add) for rows y [t k, h] in expert order;
+    weights [t, k] fp32 or None (ones), add [t, h] or None."""
+    t, k, h, dev = _sorted_rows(y, "y", inv)
+    if weights is not None:
+        _arg(weights, "weights", torch.float32, (t, k), dev)
+    if add is not None:
+        _arg(add, "add", y.dtype, (t, h), dev)
+    out = torch.empty((t, h), dtype=y.dtype, device=y.device)
+    _call("moe_combine_forward", _lib.moe_combine_forward, dev, y.data_ptr(), _DT[y.dtype], t, h, inv.data_ptr(),
+          _dp(weights), _dp(add), k, out.data_ptr())
+    return out
+
+
+def moe_combine_backward(dout, y, inv, weights=None, out=None):
+    """Gradients (dy [t k, h], dweights [t, k] fp32 or None) of moe_combine_forward for dout [t, h];
+    rows of dy that no slot has are not written."""
+    t, k, h, dev = _sorted_rows(y, "y", inv)
+    _arg(dout, "dout", y.dtype, (t, h), dev)
+    dw = None
+    if weights is not None:
+        _arg(weights, "weights", torch.float32, (t, k), dev)
+        dw = torch.empty((t, k), dtype=torch.float32, device=y.device)
+    dy = _out(out, y.dtype, (t * k, h), y, dev)
+    _call("moe_combine_backward", _lib.moe_combine_backward, dev, dout.data_ptr(), y.data_ptr(), _DT[y.dtype], t, h,
+          inv.data_ptr(), _dp(weights), k, dy.data_ptr(), _dp(dw))
+    return dy, dw
+
+
+def quantize_fp8_tokens(x, columns=False, gated=False, offsets=None):
+    """e4m3 codes q [t, k] and scales s [ceil(k / 128), t] of x [t, k] in groups of 128 along the
+    row; ``gated``: of silu(x[:, :k]) x[:, k:] for x [t, 2 k].  With ``columns`` -> (q, s, qc, sc):
+    also in groups of 128 tokens, sc [groups, k], for fp8_linear_backward.  ``offsets`` (of
+    moe_dispatch_forward): rows behind the last expert are left out, and the groups of tokens
+    start anew with each expert."""
+    (t, k), dev = _first(x, _FLOATS, "x")
+    e = _offsets(offsets, dev)
+    if gated:
+        if k % 2:
+            raise ValueError("a gated x has an even width")
+        k //= 2
+    device = x.device
+    q = torch.empty((t, k), dtype=_E4M3, device=device)
+    s = torch.empty((-(-k // 128), t), dtype=torch.float32, device=device)
+    qc = sc = None
+    if columns:
+        qc = torch.empty((t, k), dtype=_E4M3, device=device)
+        sc = torch.empty((_column_groups(t, offsets, e), k), dtype=torch.float32, device=device)
+    _call("quantize_fp8_tokens", _lib.quantize_fp8_tokens, dev, x.data_ptr(), _DT[x.dtype], t, k, int(bool(gated)),
+          _dp(offsets), e, q.data_ptr(), s.data_ptr(), _dp(qc), _dp(sc))
+    return (q, s, qc, sc) if columns else (q, s)
+
+
+def _column_groups(t, offsets, e):
+    return -(-t // 128) if offsets is None else t // 128 + min(e, t)
+
+
+def quantize_fp8_blocks(w):
+    """e4m3 codes and scales [.., ceil(n / 128), ceil(k / 128)] of weights w [n, k] or [e, n, k] by
+    blocks of 128 x 128."""
+    _need(w, _FLOATS, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [n, k] or [e, n, k]")
+    e, n, k = (1,) * (3 - w.dim()) + tuple(w.shape)
+    q = torch.empty_like(w, dtype=_E4M3)
+    s = torch.empty(tuple(w.shape[:-2]) + (-(-n // 128), -(-k // 128)), dtype=torch.float32, device=w.device)
+    _call("quantize_fp8_blocks", _lib.quantize_fp8_blocks, w.get_device(), w.data_ptr(), _DT[w.dtype], e, n, k,
+          q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def _fp8_weights(w_q, w_s, k, offsets, dev):
+    """Checks the weights' codes and scales -> (experts, n)."""
+    e = _offsets(offsets, dev)
+    if not isinstance(w_q, torch.Tensor) or w_q.dim() != (2 if offsets is None else 3):
+        _need(w_q, _E4M3, "w_q")
+        raise ValueError("w_q must be [n, k], with offsets [e, n, k]")
+    n = w_q.shape[-2]
+    head = () if offsets is None else (e,)
+    _arg(w_q, "w_q", _E4M3, head + (n, k), dev)
+    _arg(w_s, "w_s", torch.float32, head + (-(-n // 128), -(-k // 128)), dev)
+    return e, n
+
+
+def fp8_linear_forward(q, s, w_q, w_s, offsets=None, out_dtype=torch.bfloat16, out=None):
+    """y [t, n] of out_dtype (fp16 or bf16): the product of token codes q [t, k] e4m3 with scales s
+    [ceil(k / 128), t] and weight codes w_q [n, k] with block scales w_s.  With ``offsets`` [e + 1]
+    the rows offsets[x] .. offsets[x + 1] - 1 take matrix x of w_q [e, n, k]; rows of no expert
+    are not written."""
+    (t, k), dev = _first(q, (_E4M3,), "q")
+    _arg(s, "s", torch.float32, (-(-k // 128), t), dev)
+    e, n = _fp8_weights(w_q, w_s, k, offsets, dev)
+    if out_dtype not in _16BIT:
+        raise TypeError(f"out_dtype {out_dtype} is not fp16 or bf16")
+    y = _out(out, out_dtype, (t, n), q, dev)
+    grouped = int(offsets is not None)
+    nbytes = _fp8_linear_ws(t, k, n, e, grouped)
+    ws = _scratch(nbytes, q.device)
+    _call("fp8_linear_forward", _lib.fp8_linear_forward, dev, q.data_ptr(), s.data_ptr(), t, k, w_q.data_ptr(),
+          w_s.data_ptr(), n, _dp(offsets), e, _DT[out_dtype], y.data_ptr(), _dp(ws), nbytes)
+    return y
+
+
+def fp8_linear_backward(dy, x_q, x_s, w_q, w_s, offsets=None, out=None):
+    """Gradients (dx [t, k], dw like w_q) of fp8_linear_forward, of dy's type, for dy [t, n]: dy is
+    quantised in groups of 128 along its rows (dx) and along the tokens (dw); x_q, x_s are the
+    forward's x by quantize_fp8_tokens(x, columns=True).  out: dx; its rows of no expert are not
+    written."""
+    (t, n), dev = _first(dy, _16BIT, "dy")
+    k = _first(x_q, (_E4M3,), "x_q")[0][1]
+    _arg(x_q, "x_q", _E4M3, (t, k), dev)
+    e, wn = _fp8_weights(w_q, w_s, k, offsets, dev)
+    if wn != n:
+        raise ValueError(f"dy must be {(t, wn)}, got {(t, n)}")
+    _arg(x_s, "x_s", torch.float32, (_column_groups(t, offsets, e), k), dev)
+    dx = _out(out, dy.dtype, (t, k), dy, dev)
+    dw = torch.empty_like(w_q, dtype=dy.dtype)
+    grouped = int(offsets is not None)
+    nbytes = _fp8_linear_bwd_ws(t, k, n, e, grouped)
+    ws = _scratch(nbytes, dy.device)
+    _call("fp8_linear_backward", _lib.fp8_linear_backward, dev, dy.data_ptr(), _DT[dy.dtype], t, k, n, x_q.data_ptr(),
+          x_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), _dp(offsets), e, dx.data_ptr(), dw.data_ptr(), _dp(ws), nbytes)
+    return dx, dw

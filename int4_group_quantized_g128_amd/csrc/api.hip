@@ -10,7 +10,10 @@
 
 #include "../../include/q4moe.h"
 #include "dense.h"
+#include "fp8.h"
+#include "fp8_plan.h"
 #include "internal.h"
+#include "tokens.h"
 
 using namespace q4;
 
@@ -1294,6 +1297,169 @@ int block_norm_backward(const q4_block_norm_t* p, const void* dr, const void* dn
   return check_hip(launch_block_norm_bwd(norm_args(p), p->dtype, dr, dn, dres, dy, dw_post, dgate, dw_pre,
                                          static_cast<float*>(workspace), stream),
                    "block norm backward launch");
+}
+
+// ---------------------------------------------------------------- token order
+static constexpr int64_t kMostTokens = int64_t(1) << 23, kMostSlots = int64_t(1) << 26;
+
+static int validate_slots(int dtype, int64_t t, int64_t h, int32_t k) {
+  Q4_REQUIRE(float_dtype(dtype), Q4_ERR_DTYPE, "dtype %d", dtype);
+  Q4_REQUIRE(t >= 0 && t < kMostTokens && k >= 1 && k <= 4096 && t * k < kMostSlots && h >= 1 && h <= kMaxWidth,
+             Q4_ERR_SHAPE, "need 0 <= t < 2^23, 1 <= k <= 4096, t k < 2^26, 1 <= h <= 2^20");
+  return ok();
+}
+
+size_t moe_dispatch_workspace_bytes(int64_t t, int32_t k, int32_t e) {
+  if (validate_slots(Q4_F32, t, 1, k) != Q4_OK || e < 1 || e > 4096) return 0;
+  return size_t(dispatch_workspace(t, k, e));
+}
+
+int moe_dispatch_forward(const void* x, int dtype, int64_t t, int64_t h, const int32_t* ids, int32_t k, int32_t first,
+                         int32_t e, void* out, uint8_t* q, float* s, int32_t* offsets, int32_t* perm, int32_t* inv,
+                         void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_slots(dtype, t, h, k)) return rc;
+  Q4_REQUIRE(e >= 1 && e <= 4096 && first >= 0, Q4_ERR_SHAPE, "need 1 <= e <= 4096, first >= 0");
+  Q4_REQUIRE((q != nullptr) == (s != nullptr), Q4_ERR_NULL, "q and s go together");
+  Q4_REQUIRE(!q || h % 16 == 0, Q4_ERR_SHAPE, "e4m3 codes need h %% 16 == 0");
+  Q4_REQUIRE(offsets, Q4_ERR_NULL, "offsets is required");
+  Q4_REQUIRE(t == 0 || (x && ids && perm && inv && (out != nullptr) != (q != nullptr)), Q4_ERR_NULL,
+             "x, ids, perm, inv and one of out and q are required");
+  Q4_REQUIRE(!misaligned(x) && !misaligned(ids) && !misaligned(out) && !misaligned(q) && !misaligned(s) &&
+                 !misaligned(offsets) && !misaligned(perm) && !misaligned(inv),
+             Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(dispatch_workspace(t, k, e));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  const DispatchArgs a{x, ids, t, h, k, first, e, dtype, out, q, s, offsets, perm, inv};
+  return check_hip(launch_dispatch(a, workspace, stream), "dispatch launch");
+}
+
+int moe_dispatch_backward(const void* dxp, int dtype, int64_t t, int64_t h, const int32_t* inv, int32_t k, void* dx,
+                          hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_slots(dtype, t, h, k)) return rc;
+  if (t == 0) return ok();
+  Q4_REQUIRE(dxp && inv && dx, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(dxp) && !misaligned(inv) && !misaligned(dx), Q4_ERR_ALIGN,
+             "device pointers must be 16-byte aligned");
+  return check_hip(launch_tokens_combine(dxp, inv, nullptr, nullptr, t, k, h, dtype, dx, stream),
+                   "dispatch backward launch");
+}
+
+int moe_combine_forward(const void* y, int dtype, int64_t t, int64_t h, const int32_t* inv, const float* weights,
+                        const void* add, int32_t k, void* out, hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_slots(dtype, t, h, k)) return rc;
+  if (t == 0) return ok();
+  Q4_REQUIRE(y && inv && out, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(y) && !misaligned(inv) && !misaligned(weights) && !misaligned(add) && !misaligned(out),
+             Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  return check_hip(launch_tokens_combine(y, inv, weights, add, t, k, h, dtype, out, stream), "combine launch");
+}
+
+int moe_combine_backward(const void* dout, const void* y, int dtype, int64_t t, int64_t h, const int32_t* inv,
+                         const float* weights, int32_t k, void* dy, float* dw, hipStream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_slots(dtype, t, h, k)) return rc;
+  if (t == 0) return ok();
+  Q4_REQUIRE(dout && inv && dy, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE((dw != nullptr) == (weights != nullptr) && (!dw || y), Q4_ERR_NULL,
+             "weights, dw and y go together (y may be given without)");
+  Q4_REQUIRE(!misaligned(dout) && !misaligned(y) && !misaligned(inv) && !misaligned(weights) && !misaligned(dy) &&
+                 !misaligned(dw), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  return check_hip(launch_tokens_combine_bwd(dout, y, inv, weights, t, k, h, dtype, dy, dw, stream),
+                   "combine backward launch");
+}
+
+// ---------------------------------------------------------------- e4m3 products
+static bool fp8_rows(int64_t t) { return t >= 0 && t < kMostTokens; }
+static bool fp8_width(int64_t k) { return k >= 16 && k % 16 == 0 && k <= kMaxWidth; }
+
+int quantize_fp8_tokens(const void* x, int dtype, int64_t t, int64_t k, int gated, const int32_t* offsets, int32_t e,
+                        uint8_t* q, float* s, uint8_t* q_col, float* s_col, hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(float_dtype(dtype), Q4_ERR_DTYPE, "dtype %d", dtype);
+  Q4_REQUIRE(fp8_rows(t) && fp8_width(k) && (!gated || k <= kMaxWidth / 2), Q4_ERR_SHAPE,
+             "need 0 <= t < 2^23, k a multiple of 16 up to 2^20 (gated: 2^19)");
+  Q4_REQUIRE(!offsets || (e >= 1 && e <= 4096), Q4_ERR_SHAPE, "need 1 <= e <= 4096");
+  Q4_REQUIRE((q != nullptr) == (s != nullptr) && (q_col != nullptr) == (s_col != nullptr), Q4_ERR_NULL,
+             "codes and scales go together");
+  Q4_REQUIRE(!gated || !q_col, Q4_ERR_UNSUPPORTED, "codes along the tokens are not gated");
+  if (t == 0) return ok();
+  Q4_REQUIRE(x && (q || q_col), Q4_ERR_NULL, "x and one form of codes are required");
+  Q4_REQUIRE(!misaligned(x) && !misaligned(offsets) && !misaligned(q) && !misaligned(s) && !misaligned(q_col) &&
+                 !misaligned(s_col), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const Fp8QuantArgs a{x, t, k, dtype, gated != 0, q, q_col, s, s_col, offsets, e};
+  return check_hip(launch_quantize_fp8_tokens(a, stream), "quantize fp8 tokens launch");
+}
+
+int quantize_fp8_blocks(const void* w, int dtype, int64_t e, int64_t n, int64_t k, uint8_t* q, float* s,
+                        hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(float_dtype(dtype), Q4_ERR_DTYPE, "dtype %d", dtype);
+  Q4_REQUIRE(e >= 1 && e <= 4096 && n >= 1 && n <= kMaxWidth && fp8_width(k) && e * ceil_div(n, 128) < int64_t(1) << 24,
+             Q4_ERR_SHAPE, "need 1 <= e <= 4096, 1 <= n <= 2^20, k a multiple of 16 up to 2^20");
+  Q4_REQUIRE(w && q && s, Q4_ERR_NULL, "w, q and s are required");
+  Q4_REQUIRE(!misaligned(w) && !misaligned(q) && !misaligned(s), Q4_ERR_ALIGN,
+             "device pointers must be 16-byte aligned");
+  return check_hip(launch_quantize_fp8_blocks(w, dtype, e, n, k, q, s, stream), "quantize fp8 blocks launch");
+}
+
+static bool fp8_shape(int64_t t, int64_t k, int64_t n, int32_t e) {
+  return fp8_rows(t) && fp8_width(k) && n >= 1 && n <= kMaxWidth && e >= 1 && e <= 4096;
+}
+static bool fp8_bwd_shape(int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
+  return fp8_shape(t, k, n, e) && n >= 16 && n % 16 == 0 && (grouped || e == 1) &&
+         fp8_fits(FP8_DX, t, k, n, e, grouped) && fp8_fits(FP8_DW, t, k, n, e, grouped);
+}
+
+size_t fp8_linear_workspace_bytes(int64_t t, int64_t k, int64_t n, int32_t e, int grouped) {
+  return fp8_shape(t, k, n, e) ? size_t(fp8_linear_workspace(t, k, n, e, grouped != 0)) : 0;
+}
+
+int fp8_linear_forward(const uint8_t* q, const float* s, int64_t t, int64_t k, const uint8_t* w_q, const float* w_s,
+                       int64_t n, const int32_t* offsets, int32_t e, int y_dtype, void* y, void* workspace,
+                       size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(y_dtype == Q4_F16 || y_dtype == Q4_BF16, Q4_ERR_DTYPE, "y_dtype must be Q4_F16 or Q4_BF16");
+  Q4_REQUIRE(fp8_shape(t, k, n, e) && (offsets || e == 1) && fp8_fits(FP8_Y, t, k, n, e, offsets != nullptr),
+             Q4_ERR_SHAPE,
+             "need 0 <= t < 2^23, k a multiple of 16 up to 2^20, 1 <= n <= 2^20, 1 <= e <= 4096 (1 without offsets)");
+  if (t == 0) return ok();
+  Q4_REQUIRE(q && s && w_q && w_s && y, Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(q) && !misaligned(s) && !misaligned(w_q) && !misaligned(w_s) && !misaligned(offsets) &&
+                 !misaligned(y), Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(fp8_linear_workspace(t, k, n, e, offsets != nullptr));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_fp8_linear(q, s, t, k, w_q, w_s, n, offsets, e, y_dtype, y, workspace, stream),
+                   "fp8 linear launch");
+}
+
+size_t fp8_linear_backward_workspace_bytes(int64_t t, int64_t k, int64_t n, int32_t e, int grouped) {
+  return fp8_bwd_shape(t, k, n, e, grouped != 0) ? size_t(fp8_linear_bwd_workspace(t, k, n, e, grouped != 0)) : 0;
+}
+
+int fp8_linear_backward(const void* dy, int dtype, int64_t t, int64_t k, int64_t n, const uint8_t* x_q,
+                        const float* x_s, const uint8_t* w_q, const float* w_s, const int32_t* offsets, int32_t e,
+                        void* dx, void* dw, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  Q4_REQUIRE(dtype == Q4_F16 || dtype == Q4_BF16, Q4_ERR_DTYPE, "dtype must be Q4_F16 or Q4_BF16");
+  Q4_REQUIRE(fp8_bwd_shape(t, k, n, e, offsets != nullptr), Q4_ERR_SHAPE,
+             "need 0 <= t < 2^23, k and n multiples of 16 up to 2^20, 1 <= e <= 4096 (1 without offsets)");
+  Q4_REQUIRE(dw && (t == 0 || (dy && x_q && x_s && w_q && w_s && dx)), Q4_ERR_NULL, "missing pointer");
+  Q4_REQUIRE(!misaligned(dy) && !misaligned(x_q) && !misaligned(x_s) && !misaligned(w_q) && !misaligned(w_s) &&
+                 !misaligned(offsets) && !misaligned(dx) && !misaligned(dw),
+             Q4_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  const size_t need = size_t(fp8_linear_bwd_workspace(t, k, n, e, offsets != nullptr));
+  Q4_REQUIRE(ws_bytes >= need, Q4_ERR_WORKSPACE, "workspace holds %zu bytes, need %zu", ws_bytes, need);
+  Q4_REQUIRE(need == 0 || workspace, Q4_ERR_NULL, "workspace is NULL");
+  Q4_REQUIRE(need == 0 || !misaligned(workspace), Q4_ERR_ALIGN, "workspace not 16-byte aligned");
+  return check_hip(launch_fp8_linear_bwd(dy, t, k, n, dtype, x_q, x_s, w_q, w_s, offsets, e, dx, dw, workspace, stream),
+                   "fp8 linear backward launch");
 }
 
 }  // extern "C"

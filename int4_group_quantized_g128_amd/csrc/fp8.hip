@@ -1,0 +1,868 @@
+// e4m3 products with a scale per block of 128, dense and by expert, with their quantisers.
+//
+//   y[t][n]  = sum_g s[g][t] ws[n / 128][g] sum_{k in g} q[t][k] wq[n][k]          g: 128 columns k
+//   dx[t][k] = sum_g s[g][t] ws[g][k / 128] sum_{n in g} d[t][n] wq[n][k]          g: 128 rows n of W
+//   dw[n][k] = sum_g c[g][n] x[g][k] sum_{t in g} dq[t][n] xq[t][k]                g: 128 tokens
+//
+// with d, dq the codes of dy along its rows and along the tokens.  One 16x16x128 matrix
+// instruction takes a whole group, so each of its results is scaled once on its way into the fp32
+// sums.  Within an instruction the matrix core aligns 8 products at a time to the largest and
+// drops what lies 2^-13 below it, then adds in fp32: with normally distributed codes the sums are
+// 1.4e-5 (relative, 2-norm) from the exact ones, which a result in 16 bits (2e-4 and up) hides and
+// one in fp32 would show; results are 16 bits wide.
+//
+// Operands are read as they lie in memory: "KC" panels are contiguous along the summed index (x,
+// dy and W in y), "MC" panels along their own (W in dx, both operands of dw), whose fragments come
+// out of LDS through the transposing 8-byte reads; no transposed copy is made.
+#include <algorithm>
+#include <type_traits>
+
+#include "e4m3.h"
+#include "fp8.h"
+#include "fp8_plan.h"
+#include "internal.h"
+#include "lds_copy.h"
+
+namespace q4 {
+
+namespace {
+
+constexpr uint32_t kNoByte = 0x80000000u;   // a byte offset past every descriptor's range
+typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+
+struct Frag {   // 32 codes of a lane: row (column) lane % 16, k in 16 q .. + 15 and 64 + 16 q .. + 15, q = lane / 16
+  u32x4_t lo, hi;
+};
+Q4_DEVICE f32x4_t group_product(const Frag& a, const Frag& b) {
+  struct Two {
+    u32x4_t lo, hi;
+  };
+  const i32x8_t x = bitcast<i32x8_t>(Two{a.lo, a.hi}), y = bitcast<i32x8_t>(Two{b.lo, b.hi});
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4_t{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+
+// A value that is the same in every lane, through the scalar cache (which does not count as one
+// of the vector loads that the copies' waits count).
+Q4_DEVICE float load_uniform(const float* p, int64_t i) {
+  typedef __attribute__((address_space(4))) const float* sptr;
+  return *(sptr)(uintptr_t)(p + i);
+}
+
+// ---------------------------------------------------------------- rows by expert
+// Rows of expert x: [first, first + count), kept inside [0, t) whatever the offsets hold.
+Q4_DEVICE void expert_rows(const int32_t* offsets, int x, int64_t t, int64_t& first, int64_t& count) {
+  const int64_t a = offsets[x], b = offsets[x + 1];
+  first = a < 0 ? 0 : a > t ? t : a;
+  const int64_t end = b < 0 ? 0 : b > t ? t : b;
+  count = end > first ? end - first : 0;
+}
+
+struct Span {
+  int e, tile;     // expert, the tile's number over all experts
+  int64_t row;     // its first row
+  int rows;
+};
+
+// Row tiles of BM rows, in expert order, over a workgroup of NT threads; each thread owns a run
+// of experts.
+template <int NT, int BM>
+struct ExpertTiles {
+  int beg, end, before, own;   // this thread's experts, tiles before them, tiles of them
+  int total;
+  __device__ void count(const int32_t* offsets, int e, int64_t t, int32_t* tot /* LDS [NT / 64] */) {
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int per = (e + NT - 1) / NT;
+    beg = min(e, tid * per), end = min(e, beg + per);
+    own = 0;
+    for (int x = beg; x < end; ++x) {
+      int64_t f, c;
+      expert_rows(offsets, x, t, f, c);
+      own += int((c + BM - 1) / BM);
+    }
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 63) tot[wid] = inc;
+    __syncthreads();
+    before = inc - own, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+      if (w < wid) before += tot[w];
+      total += tot[w];
+    }
+    __syncthreads();
+  }
+  // Tile `at` (below total) into *out (LDS); all threads call.
+  __device__ void find(const int32_t* offsets, int64_t t, int at, Span* out) const {
+    if (at >= before && at < before + own) {
+      int n = before;
+      for (int x = beg; x < end; ++x) {
+        int64_t f, c;
+        expert_rows(offsets, x, t, f, c);
+        const int nt = int((c + BM - 1) / BM);
+        if (at < n + nt) {
+          const int64_t r = int64_t(at - n) * BM;
+          *out = Span{x, at, f + r, int(c - r < BM ? c - r : BM)};
+          break;
+        }
+        n += nt;
+      }
+    }
+    __syncthreads();
+  }
+};
+
+// ---------------------------------------------------------------- quantisers
+// A workgroup takes 128 rows x 128 columns: thread i columns 8 (i % 16) .. + 7 of rows i / 16 + 16 j.
+enum Form { FORM_ROWS = 1, FORM_COLS = 2, FORM_BLOCK = 4 };
+
+template <int DT, bool GATED>
+Q4_DEVICE void load_tile(const void* x, int64_t ld, int64_t row0, int rows, int64_t c, int64_t k, float v[8][8]) {
+  typedef Elem<DT> E;
+  typename E::Raw g[8][8 / E::VEC], u[GATED ? 8 : 1][8 / E::VEC];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (threadIdx.x >> 4) + 16 * i;
+    if (r < rows && c < k) {
+#pragma unroll
+      for (int j = 0; j < 8 / E::VEC; ++j) {
+        g[i][j] = E::load(x, (row0 + r) * ld + c + j * E::VEC);
+        if constexpr (GATED) u[i][j] = E::load(x, (row0 + r) * ld + k + c + j * E::VEC);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (threadIdx.x >> 4) + 16 * i;
+    const bool in = r < rows && c < k;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (GATED)
+        v[i][j] = in ? swiglu(E::value(g[i][j / E::VEC], j % E::VEC), E::value(u[i][j / E::VEC], j % E::VEC)) : 0.f;
+      else v[i][j] = in ? E::value(g[i][j / E::VEC], j % E::VEC) : 0.f;
+    }
+  }
+}
+
+template <int DT, int FORM, bool GATED>
+__global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
+  __shared__ float part[4][128];
+  __shared__ Span span;
+  __shared__ int32_t tot[4];
+  int tile = blockIdx.x;
+  int64_t row0 = int64_t(tile) * 128, left;
+  if (FORM & FORM_COLS && a.offsets) {
+    ExpertTiles<256, 128> tiles;
+    tiles.count(a.offsets, a.e, a.t, tot);
+    if (tile >= tiles.total) return;
+    tiles.find(a.offsets, a.t, tile, &span);
+    row0 = span.row, left = span.rows;
+  } else {
+    int64_t end = a.t;
+    if (a.offsets) end = std::min<int64_t>(end, std::max<int64_t>(a.offsets[a.e], 0));
+    left = end - row0;
+  }
+  if (left <= 0) return;
+  const int rows = int(std::min<int64_t>(left, 128));
+  const int cb = blockIdx.y, lane16 = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t c = int64_t(cb) * 128 + lane16 * 8;
+  float v[8][8];
+  load_tile<DT, GATED>(a.x, GATED ? 2 * a.k : a.k, row0, rows, c, a.k, v);
+  if constexpr (FORM & FORM_ROWS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
+      const float s = e4m3_scale(row16_max(m));
+      const int r = slot + 16 * i;
+      if (r < rows) {
+        if (c < a.k)
+          *reinterpret_cast<u32x2_t*>(a.q_row + (row0 + r) * a.k + c) =
+              u32x2_t{e4m3_codes4(v[i], s), e4m3_codes4(v[i] + 4, s)};
+        if (lane16 == 0) a.s_row[cb * a.t + row0 + r] = s;
+      }
+    }
+  }
+  if constexpr (FORM & FORM_COLS) {
+    float m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], magnitude(v[i][j]));
+      m[j] = fmaxf(m[j], __shfl_xor(m[j], 16, 64));
+      m[j] = fmaxf(m[j], __shfl_xor(m[j], 32, 64));
+    }
+    if ((threadIdx.x & 48) == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[threadIdx.x >> 6][lane16 * 8 + j] = m[j];
+    }
+    __syncthreads();
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = lane16 * 8 + j;
+      s[j] = e4m3_scale(fmaxf(fmaxf(part[0][at], part[1][at]), fmaxf(part[2][at], part[3][at])));
+    }
+    if (c < a.k) {
+      if (slot == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a.s_col[int64_t(tile) * a.k + c + j] = s[j];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = slot + 16 * i;
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = s[j] > 0.f ? fminf(fmaxf(v[i][j] / s[j], -kE4m3Max), kE4m3Max) : 0.f;
+        int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+        w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
+        int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+        w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], w1, true);
+        if (r < rows) *reinterpret_cast<u32x2_t*>(a.q_col + (row0 + r) * a.k + c) = u32x2_t{uint32_t(w0), uint32_t(w1)};
+      }
+    }
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) k_quantize_fp8_blocks(const void* __restrict__ w, int64_t n, int64_t k,
+                                                             uint32_t row_blocks, uint8_t* __restrict__ q,
+                                                             float* __restrict__ s) {
+  __shared__ float part[4];
+  const int64_t x = blockIdx.x / row_blocks, rb = blockIdx.x - x * row_blocks;
+  const int rows = int(std::min<int64_t>(128, n - rb * 128));
+  const int64_t row0 = x * n + rb * 128, c = int64_t(blockIdx.y) * 128 + (threadIdx.x & 15) * 8;
+  float v[8][8];
+  load_tile<DT, false>(w, k, row0, rows, c, k, v);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  const float sc = e4m3_scale(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (threadIdx.x >> 4) + 16 * i;
+    if (r < rows && c < k)
+      *reinterpret_cast<u32x2_t*>(q + (row0 + r) * k + c) = u32x2_t{e4m3_codes4(v[i], sc), e4m3_codes4(v[i] + 4, sc)};
+  }
+  if (threadIdx.x == 0) s[blockIdx.x * int64_t(gridDim.y) + blockIdx.y] = sc;
+}
+
+// ---------------------------------------------------------------- products
+struct Fp8Args {
+  const uint8_t *a, *b;       // token side (dw: dy) and the other operand
+  int64_t lda, ldb;
+  const float *sa, *sb;       // sa [groups][sa_ld]; sb: W's blocks [N / 128][K / 128] (dw: [groups][ldb])
+  int64_t sa_ld, sb_ld;       // floats per row of sa and sb
+  int64_t M, N, K;            // (dw: K tokens)
+  int64_t b_stride, sb_stride;   // from one expert's matrix to the next
+  const int32_t* offsets;     // rows by expert, or NULL
+  int32_t e;
+  int32_t dtype;              // of c: 1 fp16, 2 bf16
+  void* c;
+  int64_t ldc;
+  int32_t ksplit;
+  float* part;                // ksplit > 1: [ksplit][M][N]
+};
+
+Q4_DEVICE uint16_t to16(float v, int dtype) {
+  return dtype == 1 ? bitcast<uint16_t>(_Float16(v)) : bitcast<uint16_t>(__bf16(v));
+}
+
+// N values of a row (its address is a multiple of 2 alone), `count` of them inside the matrix.
+template <int N>
+Q4_DEVICE void store_row(void* c, int dtype, int64_t at, const float* v, int count) {
+  struct __attribute__((packed, aligned(2))) Out {
+    uint32_t w[N / 2];
+  };
+  uint16_t* p = static_cast<uint16_t*>(c) + at;
+  Out o;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) o.w[i] = to16(v[2 * i], dtype) | uint32_t(to16(v[2 * i + 1], dtype)) << 16;
+  if (count >= N) {
+    *reinterpret_cast<Out*>(p) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < count) p[i] = uint16_t(o.w[i / 2] >> (16 * (i % 2)));
+  }
+}
+
+// R rows (MC: columns) of one operand, one K step of 128 codes: 128 R bytes in copies of 1 KB.
+// 16-byte chunks are XOR-swizzled so that fragment reads hit distinct banks:
+//   KC  [R][128]: chunk c of row r at c ^ ((r / 2) % 8)
+//   MC  [128][R]: chunk c of row k at c ^ f(k), f from the bits of k in which the 16 rows that two
+//       quarters of a transposing read touch differ.
+template <bool MC, int R>
+struct Panel8 {
+  static constexpr int BYTES = R * 128;
+  static constexpr int COPIES = BYTES / 1024;
+  static constexpr int CPR = MC ? R / 16 : 8;
+
+  static Q4_DEVICE int swz(int r) {
+    if constexpr (!MC) return (r >> 1) & 7;
+    else if constexpr (R == 256) return (r & 7) | ((r >> 4) & 1) << 3;
+    else if constexpr (R == 128) return ((r >> 1) & 3) | ((r >> 4) & 1) << 2;
+    else return ((r >> 2) & 1) | ((r >> 4) & 1) << 1;
+  }
+  // Byte offset of the lane's chunk of copy `copy` from the panel's first row and first k of the
+  // step.  `left`: KC, codes of K left at the step; MC, columns left at the first column.
+  static Q4_DEVICE uint32_t offset(int copy, int lane, int64_t ld, int64_t left) {
+    const int id = copy * 64 + lane, r = id / CPR, c = (id % CPR) ^ swz(r);
+    return c * 16 < left ? uint32_t(r * ld + c * 16) : kNoByte;
+  }
+  struct Feed {   // what is left of the panel from the next K step on
+    uint64_t addr;
+    int64_t left;
+    uint32_t inc;
+    Q4_DEVICE u32x4_t rsrc(bool valid) const {
+      const uint32_t n = !valid || left <= 0 ? 0u : left > 0x7fffffff ? 0x7fffffffu : uint32_t(left);
+      return u32x4_t{uint32_t(addr), uint32_t(addr >> 32) & 0xffffu, n, 0x00020000u};
+    }
+    Q4_DEVICE void next() { addr += inc, left -= inc; }
+  };
+  // The panel from row (MC: column) row0 on of `rows` rows x K codes, at step `step`.
+  static Q4_DEVICE Feed feed(const uint8_t* p, int64_t ld, int64_t rows, int64_t K, int64_t row0, int step) {
+    const uint32_t inc = MC ? uint32_t(ld) * 128u : 128u;
+    const int64_t at = (MC ? row0 : row0 * ld) + int64_t(step) * inc;
+    return Feed{reinterpret_cast<uint64_t>(p) + at, (MC ? K * ld : rows * ld) - at, inc};
+  }
+
+  static Q4_DEVICE uint32_t lane_base(int lane) {
+    const int q = lane >> 4, s = lane & 15;
+    if constexpr (!MC) return s * 128 + ((q ^ swz(s)) << 4);
+    else return (16 * q + (s >> 1)) * R + (swz(16 * q + (s >> 1)) << 4) + ((s & 1) << 3);
+  }
+  // Fragment of rows (columns) r0 .. r0 + 15 of the panel at LDS address `lds`.
+  static Q4_DEVICE Frag frag(uint32_t lds, uint32_t lb, int r0) {
+    Frag f;
+    if constexpr (!MC) {
+      typedef __attribute__((address_space(3))) const u32x4_t* lptr;
+      f.lo = *(lptr)(uintptr_t)(lds + r0 * 128 + lb);
+      f.hi = *(lptr)(uintptr_t)(lds + r0 * 128 + (lb ^ 64));
+    } else {
+      // a 16-lane group reads 8 rows k x 16 columns and each lane gets its column's 8 codes
+      typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+      typedef __attribute__((address_space(3))) i32x2* lptr;
+      const uint32_t at = lds + (lb ^ r0);
+      u32x2_t v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        v[r] = bitcast<u32x2_t>(
+            __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr)(uintptr_t)(at + (8 * (r & 1) + 64 * (r >> 1)) * R)));
+      f.lo = u32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
+      f.hi = u32x4_t{v[2][0], v[2][1], v[3][0], v[3][1]};
+    }
+    return f;
+  }
+};
+
+template <typename P, int N>
+Q4_DEVICE void copies8(const u32x4_t& rs, uint32_t at, int first, int lane, int64_t ld, int64_t left) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    if constexpr (N == 1) copy_to_lds(rs, at + first * 1024, P::offset(first, lane, ld, left));
+    else
+      copy2_to_lds(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left),
+                   P::offset(first + j + 1, lane, ld, left));
+  }
+}
+
+template <int N>
+Q4_DEVICE void wait_barrier8() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Scales of one step, 4 bytes per row, beside the panels.
+struct ScaleFeed {
+  uint64_t addr;
+  int64_t inc;
+  uint32_t bytes;
+  Q4_DEVICE u32x4_t rsrc(bool valid) const {
+    return u32x4_t{uint32_t(addr), uint32_t(addr >> 32) & 0xffffu, valid ? bytes : 0u, 0x00020000u};
+  }
+  Q4_DEVICE void next() { addr += inc; }
+  static Q4_DEVICE ScaleFeed of(const float* s, int64_t ld, int64_t group, int64_t row0, int64_t rows) {
+    return ScaleFeed{reinterpret_cast<uint64_t>(s + group * ld + row0), ld * 4,
+                     rows <= 0 ? 0u : uint32_t(rows > 256 ? 1024 : rows * 4)};
+  }
+};
+
+// BM x BN per workgroup of WM x WN waves, a ring of NS K steps in LDS: step s + NS - 1 is copied
+// while step s is multiplied, one barrier per step.  By expert, the grid's workgroups walk the
+// tiles that the offsets make; workgroup b runs on XCD b % 8, and each XCD takes one contiguous
+// range of tiles (its L2 keeps the panels they share), in groups of 8 row tiles that walk the
+// column tiles together.
+template <int MODE, int BM, int BN, int WM, int WN, int NS>
+__global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles_in, uint32_t ntiles) {
+  constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
+  constexpr int NW = WM * WN, NT = 64 * NW;
+  typedef Panel8<AMC, BM> PA;
+  typedef Panel8<BMC, BN> PB;
+  constexpr int SCALES = (BM + (VECB ? BN : 0)) * 4;
+  constexpr int STAGE = PA::BYTES + PB::BYTES + SCALES;
+  constexpr int CA = PA::COPIES / NW, CB = PB::COPIES / NW, CPW = CA + CB + 1 + (VECB ? 1 : 0);
+  constexpr int MB = BM / WM / 16, NB = BN / WN / 16, COLS = NB * 16;
+  constexpr int AHEAD = NS - 1;
+  static_assert(BN / WN <= 64, "a wave's columns lie in one block of W");
+  static_assert(NS * STAGE >= NW * 32 * COLS * 4, "the turn at a tile's end");
+  __shared__ __align__(16) uint8_t ring[NS * STAGE];
+  __shared__ Span span;
+  __shared__ int32_t tot[NW];
+
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int wm = wid % WM, wn = wid / WM;
+  const uint32_t lds0 = lds_addr(ring);
+  const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
+
+  const bool by_expert = MODE != FP8_DW && g.offsets;
+  ExpertTiles<NT, MODE == FP8_DW ? 128 : BM> tiles;
+  if (g.offsets) tiles.count(g.offsets, g.e, MODE == FP8_DW ? g.K : g.M, tot);
+  const uint32_t mtiles = by_expert ? uint32_t(tiles.total) : mtiles_in;
+  const uint32_t plane = mtiles * ntiles;
+  const uint32_t total = plane * (MODE == FP8_DW ? uint32_t(g.e) : 1u) * uint32_t(g.ksplit);
+  const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
+  const uint32_t mine = share + (xcd < rest ? 1 : 0), start = xcd * share + (xcd < rest ? xcd : rest);
+  for (uint32_t item = blockIdx.x / 8; item < mine; item += (gridDim.x + 7) / 8) {
+    uint32_t i = start + item;
+    const uint32_t z = i / plane;   // expert (dw) or K slice
+    i -= z * plane;
+    constexpr uint32_t GM = 8;
+    const uint32_t band = i / (GM * ntiles), b0 = band * GM, gm = mtiles - b0 < GM ? mtiles - b0 : GM;
+    i -= band * GM * ntiles;
+    const uint32_t mt = b0 + i % gm, nt = i / gm;
+
+    // the tile's rows, its operands, its K steps
+    int64_t m0 = int64_t(mt) * BM, m_end = g.M, k_rows = g.K;
+    const int64_t n0 = int64_t(nt) * BN;
+    int x = 0;
+    int64_t group0 = 0, k_first = 0;
+    if (by_expert) {
+      tiles.find(g.offsets, g.M, int(mt), &span);
+      x = span.e, m0 = span.row, m_end = span.row + span.rows;
+    } else if (MODE == FP8_DW && g.offsets) {
+      x = int(z);
+      expert_rows(g.offsets, x, g.K, k_first, k_rows);
+      // the expert's first group: groups of the threads before its owner, and of its own run
+      if (x >= tiles.beg && x < tiles.end) {
+        int n = tiles.before;
+        for (int y = tiles.beg; y < x; ++y) {
+          int64_t f, c;
+          expert_rows(g.offsets, y, g.K, f, c);
+          n += int((c + 127) / 128);
+        }
+        span.tile = n;
+      }
+      __syncthreads();
+      group0 = span.tile;
+    }
+    const int all = int((k_rows + 127) / 128);
+    const int per = (all + g.ksplit - 1) / g.ksplit;
+    const int slice = g.ksplit > 1 ? int(z) : 0;
+    const int s_begin = min(all, slice * per), s_end = min(all, s_begin + per);
+    const uint8_t* ap = g.a + (MODE == FP8_DW ? k_first * g.lda : 0);
+    const uint8_t* bp = g.b + (MODE == FP8_DW ? k_first * g.ldb : x * g.b_stride);
+    typename PA::Feed fda = PA::feed(ap, g.lda, m_end, k_rows, m0, s_begin);
+    typename PB::Feed fdb = PB::feed(bp, g.ldb, g.N, k_rows, n0, s_begin);
+    ScaleFeed fsa = ScaleFeed::of(g.sa, g.sa_ld, group0 + s_begin, m0, m_end - m0);
+    ScaleFeed fsb = ScaleFeed::of(g.sb, g.sb_ld, group0 + s_begin, n0, g.N - n0);
+    const float* sb = g.sb + x * g.sb_stride;
+    const int64_t nb = std::min<int64_t>(n0 + wn * COLS, g.N - 1) / 128;   // the wave's block of W's columns
+    int64_t k_left = k_rows - int64_t(s_begin) * 128;
+    int si = s_begin, slot_in = 0;
+    auto issue = [&]() {
+      const bool in = si < s_end;
+      const uint32_t at = lds0 + slot_in * STAGE;
+      copies8<PA, CA>(fda.rsrc(in), at, wid * CA, lane, g.lda, AMC ? g.M - m0 : k_left);
+      copies8<PB, CB>(fdb.rsrc(in), at + PA::BYTES, wid * CB, lane, g.ldb, BMC ? g.N - n0 : k_left);
+      // (64 scales a copy; waves beyond the panel's repeat a copy)
+      const int ca = wid % (BM / 64), cb = wid % (BN / 64);
+      copy4_to_lds(fsa.rsrc(in), at + PA::BYTES + PB::BYTES + ca * 256, (ca * 64 + lane) * 4);
+      if constexpr (VECB)
+        copy4_to_lds(fsb.rsrc(in), at + PA::BYTES + PB::BYTES + BM * 4 + cb * 256, (cb * 64 + lane) * 4);
+      fda.next(), fdb.next(), fsa.next(), fsb.next();
+      k_left -= 128;
+      ++si;
+      slot_in = slot_in == NS - 1 ? 0 : slot_in + 1;
+    };
+    auto block_scale = [&](int s) -> float {
+      if constexpr (MODE == FP8_Y) return load_uniform(sb, nb * g.sb_ld + s);
+      else if constexpr (MODE == FP8_DX) return load_uniform(sb, s * g.sb_ld + nb);
+      else return 0.f;
+    };
+
+    f32x4_t acc[MB][NB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) issue();
+    float sb_next = s_begin < s_end ? block_scale(s_begin) : 0.f;
+    int slot = 0;
+    for (int s = s_begin; s < s_end; ++s) {
+      wait_barrier8<(AHEAD - 1) * CPW>();
+      const uint32_t base = lds0 + slot * STAGE;
+      slot = slot == NS - 1 ? 0 : slot + 1;
+      const float sbs = sb_next;
+      if (s + 1 < s_end) sb_next = block_scale(s + 1);
+      typedef __attribute__((address_space(3))) const float* fptr;
+      typedef __attribute__((address_space(3))) const f32x4_t* vptr;
+      const uint32_t sc = base + PA::BYTES + PB::BYTES;
+      Frag fb[NB];
+      f32x4_t vb[VECB ? NB : 1];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        fb[b] = PB::frag(base + PA::BYTES, lbb, wn * COLS + 16 * b);
+        if constexpr (VECB) vb[b] = *(vptr)(uintptr_t)(sc + (BM + wn * COLS + 16 * b + 4 * (lane >> 4)) * 4);
+      }
+      issue();
+#pragma unroll
+      for (int a = 0; a < MB; ++a) {
+        const Frag fa = PA::frag(base, lba, wm * (BM / WM) + 16 * a);
+        const float sa = *(fptr)(uintptr_t)(sc + (wm * (BM / WM) + 16 * a + (lane & 15)) * 4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const f32x4_t p = group_product(fb[b], fa);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][b][e] = __builtin_fmaf(p[e], sa * (VECB ? vb[b][e] : sbs), acc[a][b][e]);
+        }
+      }
+    }
+    wait_barrier8<0>();   // every wave's copies and reads are done: LDS is free
+
+    if (g.ksplit > 1) {
+      // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3
+#pragma unroll
+      for (int a = 0; a < MB; ++a) {
+        const int64_t m = m0 + wm * (BM / WM) + 16 * a + (lane & 15);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int64_t n = n0 + wn * COLS + 16 * b + 4 * (lane >> 4);
+          float* o = g.part + (int64_t(slice) * g.M + m) * g.N + n;
+          if (m < m_end && n + 4 <= g.N && (g.N & 3) == 0) {
+            *reinterpret_cast<f32x4_t*>(o) = acc[a][b];
+          } else if (m < m_end) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < g.N) o[e] = acc[a][b][e];
+          }
+        }
+      }
+    } else {
+      // through the wave's part of LDS, 32 rows at a time, so that a lane stores 8 columns of one
+      // row; 16-byte chunk c of row r lies at c ^ (r % chunks of a row)
+      constexpr int CH = COLS / 4, LPR = COLS / 8;
+      typedef __attribute__((address_space(3))) f32x4_t* lptr;
+      const uint32_t turn = lds0 + wid * (32 * COLS * 4);
+      void* c = g.c;
+      if (MODE == FP8_DW) c = static_cast<uint16_t*>(c) + x * g.M * g.ldc;
+#pragma unroll
+      for (int h = 0; h < MB / 2; ++h) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int r = 16 * a + (lane & 15), ch = 4 * b + (lane >> 4);
+            *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4)) = acc[2 * h + a][b];
+          }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 64 / LPR) {
+          const int r = r0 + lane / LPR, ch = 2 * (lane % LPR);
+          const f32x4_t u = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4));
+          const f32x4_t v = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + (((ch + 1) ^ (r & (CH - 1))) << 4));
+          const int64_t m = m0 + wm * (BM / WM) + 32 * h + r, n = n0 + wn * COLS + 4 * ch;
+          const float o[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+          if (m < m_end && n < g.N) store_row<8>(c, g.dtype, m * g.ldc + n, o, int(std::min<int64_t>(8, g.N - n)));
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+    }
+    __syncthreads();   // LDS is read to its end: the next tile's copies may land
+  }
+}
+
+// Adds the K slices of a split product in slice order, four columns per thread.
+__global__ void __launch_bounds__(256) k_fp8_join(Fp8Args g) {
+  const uint32_t quads = uint32_t((g.N + 3) / 4), i = blockIdx.x * 256 + threadIdx.x;   // (fp8_plan_us: below 2^32)
+  const int64_t m = i / quads;
+  if (m >= g.M) return;
+  const int64_t n = int64_t(i - uint32_t(m) * quads) * 4;
+  const int count = int(std::min<int64_t>(4, g.N - n));
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.ksplit; ++s) {
+    const float* q = g.part + (int64_t(s) * g.M + m) * g.N + n;
+    if (count == 4 && (g.N & 3) == 0) {
+      const f32x4_t u = *reinterpret_cast<const f32x4_t*>(q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < count) v[e] += q[e];
+    }
+  }
+  store_row<4>(g.c, g.dtype, m * g.ldc + n, v, count);
+}
+
+// Few rows (per expert): bound by reading the weights once.  A workgroup owns 16 columns of y of
+// one expert, its 8 waves take the 128-code K steps in turn and feed the matrix core straight from
+// global memory, then add their sums through LDS in wave order.
+template <int RB>
+Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws, int64_t n0, int64_t row0, int rows,
+                            f32x4_t (*sums)[4][64]) {
+  constexpr int W = 8;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int l = lane & 15, quarter = (lane >> 4) * 16;
+  const uint8_t* wp = w + std::min<int64_t>(n0 + l, g.N - 1) * g.K + quarter;
+  const uint8_t* xp[RB];
+  const float* sp[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int64_t m = row0 + min(16 * r + l, rows - 1);
+    xp[r] = g.a + m * g.K + quarter;
+    sp[r] = g.sa + m;
+  }
+  f32x4_t acc[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
+  const int full = int(g.K / 128);
+  const int64_t sb0 = (n0 / 128) * g.sb_ld;
+  auto steps = [&](auto n_c, int s) {
+    constexpr int N = decltype(n_c)::value;
+    Frag fw[N], fx[N][RB];
+    float sc[N][RB];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int64_t at = int64_t(s + u * W) * 128;
+      fw[u].lo = *reinterpret_cast<const u32x4_t*>(wp + at);
+      fw[u].hi = *reinterpret_cast<const u32x4_t*>(wp + at + 64);
+      const float sw = load_uniform(ws, sb0 + s + u * W);
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        fx[u][r].lo = *reinterpret_cast<const u32x4_t*>(xp[r] + at);
+        fx[u][r].hi = *reinterpret_cast<const u32x4_t*>(xp[r] + at + 64);
+        sc[u][r] = sw * sp[r][(s + u * W) * g.sa_ld];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const f32x4_t p = group_product(fw[u], fx[u][r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(p[e], sc[u][r], acc[r][e]);
+      }
+  };
+  constexpr int U = RB == 1 ? 4 : RB == 2 ? 2 : 1;
+  int s = wave;
+  for (; s + (U - 1) * W < full; s += U * W) steps(std::integral_constant<int, U>{}, s);
+  for (; s < full; s += W) steps(std::integral_constant<int, 1>{}, s);
+  if (s == full && g.K % 128) {   // the K tail: chunks past the row's end hold zeros
+    const int64_t at = int64_t(full) * 128;
+    const bool lo = at + quarter < g.K, hi = at + 64 + quarter < g.K;
+    const u32x4_t zero = {0, 0, 0, 0};
+    Frag fw;
+    fw.lo = lo ? *reinterpret_cast<const u32x4_t*>(wp + at) : zero;
+    fw.hi = hi ? *reinterpret_cast<const u32x4_t*>(wp + at + 64) : zero;
+    const float sw = load_uniform(ws, sb0 + full);
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      Frag fx;
+      fx.lo = lo ? *reinterpret_cast<const u32x4_t*>(xp[r] + at) : zero;
+      fx.hi = hi ? *reinterpret_cast<const u32x4_t*>(xp[r] + at + 64) : zero;
+      const float sc = sw * sp[r][full * g.sa_ld];
+      const f32x4_t p = group_product(fw, fx);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(p[e], sc, acc[r][e]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) sums[wave][r][lane] = acc[r];
+  __syncthreads();
+  if (wave < RB) {
+    f32x4_t v = sums[0][wave][lane];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v += sums[i][wave][lane];
+    const int m = 16 * wave + l;
+    const int64_t n = n0 + 4 * (lane >> 4);
+    const float o[4] = {v[0], v[1], v[2], v[3]};
+    if (m < rows && n < g.N)
+      store_row<4>(g.c, g.dtype, (row0 + m) * g.ldc + n, o, int(std::min<int64_t>(4, g.N - n)));
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols) {
+  __shared__ f32x4_t sums[8][4][64];
+  const int x = int(blockIdx.x / ncols);
+  const int64_t n0 = int64_t(blockIdx.x - x * ncols) * 16;
+  int64_t first = 0, count = g.M;
+  if (g.offsets) expert_rows(g.offsets, x, g.M, first, count);
+  const uint8_t* w = g.b + x * g.b_stride;
+  const float* ws = g.sb + x * g.sb_stride;
+  while (count > 0) {
+    const int rows = int(count < 64 ? count : 64);
+    if (rows <= 16) rows_product<1>(g, w, ws, n0, first, rows, sums);
+    else if (rows <= 32) rows_product<2>(g, w, ws, n0, first, rows, sums);
+    else rows_product<4>(g, w, ws, n0, first, rows, sums);
+    first += rows, count -= rows;
+  }
+}
+
+// ---------------------------------------------------------------- launches
+template <int MODE>
+hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
+  g.ksplit = p.ksplit;
+  const uint32_t nt = uint32_t(ceil_div(g.N, p.tile));
+  uint32_t mt = uint32_t(ceil_div(g.M, p.tile));
+  int64_t items;
+  if (MODE != FP8_DW && g.offsets)   // as many tiles as the offsets can make
+    items = (g.M / p.tile + std::min<int64_t>(g.e, g.M)) * nt;
+  else items = int64_t(mt) * nt * (MODE == FP8_DW ? g.e : 1) * p.ksplit;
+  unsigned grid = unsigned(items);
+  if (MODE != FP8_DW && g.offsets) {
+    const int64_t room = 256 * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 3);
+    grid = unsigned(std::min<int64_t>(room, ceil_div(items, 8) * 8));
+  }
+  if (p.tile == 256) hipLaunchKernelGGL((k_fp8<MODE, 256, 256, 2, 4, 2>), dim3(grid), dim3(512), 0, st, g, mt, nt);
+  else if (p.tile == 128) hipLaunchKernelGGL((k_fp8<MODE, 128, 128, 2, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  else hipLaunchKernelGGL((k_fp8<MODE, 64, 64, 2, 2, 3>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ksplit == 1) return e;
+  const int64_t threads = g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL(k_fp8_join, dim3(unsigned(ceil_div(threads, 256))), dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
+int64_t part_bytes8(const Plan& p, int64_t m, int64_t n) { return p.ksplit > 1 ? int64_t(p.ksplit) * m * n * 4 : 0; }
+
+template <int DT>
+hipError_t quantize_as(const Fp8QuantArgs& a, hipStream_t st) {
+  const bool rows = a.q_row, cols = a.q_col;
+  const int64_t tiles = cols && a.offsets ? a.t / 128 + std::min<int64_t>(a.e, a.t) : ceil_div(a.t, 128);
+  const dim3 grid(unsigned(tiles), unsigned(ceil_div(a.k, 128)));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a); };
+  if (a.gated) go(k_quantize_fp8<DT, FORM_ROWS, true>);
+  else if (rows && cols) go(k_quantize_fp8<DT, FORM_ROWS | FORM_COLS, false>);
+  else if (cols) go(k_quantize_fp8<DT, FORM_COLS, false>);
+  else go(k_quantize_fp8<DT, FORM_ROWS, false>);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_fp8_tokens(const Fp8QuantArgs& a, hipStream_t st) {
+  return a.dtype == 0 ? quantize_as<0>(a, st) : a.dtype == 1 ? quantize_as<1>(a, st) : quantize_as<2>(a, st);
+}
+
+hipError_t launch_quantize_fp8_blocks(const void* w, int dtype, int64_t e, int64_t n, int64_t k, uint8_t* q, float* s,
+                                      hipStream_t st) {
+  const uint32_t rb = uint32_t(ceil_div(n, 128));
+  const dim3 grid(unsigned(e * rb), unsigned(ceil_div(k, 128)));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, w, n, k, rb, q, s); };
+  if (dtype == 0) go(k_quantize_fp8_blocks<0>);
+  else if (dtype == 1) go(k_quantize_fp8_blocks<1>);
+  else go(k_quantize_fp8_blocks<2>);
+  return hipGetLastError();
+}
+
+int64_t fp8_linear_workspace(int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
+  return t == 0 ? 0 : part_bytes8(fp8_plan(FP8_Y, t, k, n, e, grouped), t, n);
+}
+
+hipError_t launch_fp8_linear(const uint8_t* q, const float* s, int64_t t, int64_t k, const uint8_t* wq, const float* ws,
+                             int64_t n, const int32_t* offsets, int32_t e, int y_dtype, void* y, void* work,
+                             hipStream_t st) {
+  Fp8Args g{};
+  g.a = q, g.b = wq;
+  g.lda = g.ldb = k;
+  g.sa = s, g.sb = ws;
+  g.sa_ld = t, g.sb_ld = ceil_div(k, 128);
+  g.M = t, g.N = n, g.K = k;
+  g.b_stride = n * k, g.sb_stride = ceil_div(n, 128) * g.sb_ld;
+  g.offsets = offsets, g.e = e;
+  g.dtype = y_dtype;
+  g.c = y, g.ldc = n;
+  g.ksplit = 1;
+  g.part = static_cast<float*>(work);
+  const Plan p = fp8_plan(FP8_Y, t, k, n, e, offsets != nullptr);
+  if (p.tile) return launch_tiles8<FP8_Y>(g, p, st);
+  const uint32_t ncols = uint32_t(ceil_div(n, 16));
+  hipLaunchKernelGGL(k_fp8_rows, dim3(ncols * uint32_t(offsets ? e : 1)), dim3(512), 0, st, g, ncols);
+  return hipGetLastError();
+}
+
+// Workspace of the gradients: codes and scales of dy along its rows and along the tokens, the K
+// slices of whichever product splits K.
+struct Fp8GradWork {
+  Plan dx, dw;
+  uint8_t *q_row, *q_col;
+  float *s_row, *s_col, *part;
+  int64_t bytes;
+};
+static Fp8GradWork grad_work8(void* base, int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
+  Fp8GradWork w{};
+  w.dx = fp8_plan(FP8_DX, t, k, n, e, grouped);
+  w.dw = fp8_plan(FP8_DW, t, k, n, e, grouped);
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = static_cast<uint8_t*>(base) + w.bytes;
+    w.bytes += align256(bytes);
+    return p;
+  };
+  w.q_row = take(t * n), w.q_col = take(t * n);
+  w.s_row = reinterpret_cast<float*>(take(ceil_div(n, 128) * t * 4));
+  w.s_col = reinterpret_cast<float*>(take((grouped ? t / 128 + std::min<int64_t>(e, t) : ceil_div(t, 128)) * n * 4));
+  w.part = reinterpret_cast<float*>(take(std::max(part_bytes8(w.dx, t, k), part_bytes8(w.dw, n, k))));
+  return w;
+}
+int64_t fp8_linear_bwd_workspace(int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
+  return t == 0 ? 0 : grad_work8(nullptr, t, k, n, e, grouped).bytes;
+}
+
+hipError_t launch_fp8_linear_bwd(const void* dy, int64_t t, int64_t k, int64_t n, int dtype, const uint8_t* xq,
+                                 const float* xs, const uint8_t* wq, const float* ws, const int32_t* offsets, int32_t e,
+                                 void* dx, void* dw, void* work, hipStream_t st) {
+  const bool grouped = offsets != nullptr;
+  const Fp8GradWork w = grad_work8(work, t, k, n, e, grouped);
+  Fp8Args g{};
+  g.dtype = dtype;
+  g.ksplit = 1;
+  g.part = w.part;
+  g.offsets = offsets, g.e = e;
+  if (t > 0) {
+    const Fp8QuantArgs a{dy, t, n, dtype, 0, w.q_row, w.q_col, w.s_row, w.s_col, offsets, e};
+    hipError_t rc = launch_quantize_fp8_tokens(a, st);
+    if (rc != hipSuccess) return rc;
+    g.a = w.q_row, g.b = wq;
+    g.lda = n, g.ldb = k;
+    g.sa = w.s_row, g.sb = ws;
+    g.sa_ld = t, g.sb_ld = ceil_div(k, 128);
+    g.M = t, g.N = k, g.K = n;
+    g.b_stride = n * k, g.sb_stride = ceil_div(n, 128) * g.sb_ld;
+    g.c = dx, g.ldc = k;
+    rc = launch_tiles8<FP8_DX>(g, w.dx, st);
+    if (rc != hipSuccess) return rc;
+  }
+  g.a = w.q_col, g.b = xq;   // (t == 0: no K step, zeros)
+  g.lda = n, g.ldb = k;
+  g.sa = w.s_col, g.sb = xs;
+  g.sa_ld = n, g.sb_ld = k;
+  g.M = n, g.N = k, g.K = t;
+  g.b_stride = g.sb_stride = 0;
+  g.c = dw, g.ldc = k;
+  return launch_tiles8<FP8_DW>(g, w.dw, st);
+}
+
+}  // namespace q4

@@ -37,4 +37,17 @@ Q4_DEVICE void copy2_to_lds(const u32x4_t& rsrc, uint32_t lds_in, uint32_t voff0
   (void)saved;
 }
 
+// Copies 4 bytes per lane to lds + 4 lane.
+Q4_DEVICE void copy4_to_lds(const u32x4_t& rsrc, uint32_t lds_in, uint32_t voff) {
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_in);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_nop 4\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+      "buffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(voff), "s"(rsrc)
+      : "memory");
+  (void)saved;
+}
+
 }  // namespace q4
