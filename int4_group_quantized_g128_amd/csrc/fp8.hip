@@ -314,6 +314,11 @@ struct Panel8 {
     else if constexpr (R == 128) return ((r >> 1) & 3) | ((r >> 4) & 1) << 2;
     else return ((r >> 2) & 1) | ((r >> 4) & 1) << 1;
   }
+  // Rows (MC: of k) per copy; which of two swizzles copy j (of a wave's, the first a multiple of
+  // their number) has, and the first copy that has it.
+  static constexpr int ROWS = 64 / CPR;
+  static constexpr int odd(int j) { return MC && R == 128 ? (j >> 1) & 1 : j & 1; }
+  static constexpr int copy_of(int odd) { return MC && R == 128 ? 2 * odd : odd; }
   // Byte offset of the lane's chunk of copy `copy` from the panel's first row and first k of the
   // step.  `left`: KC, codes of K left at the step; MC, columns left at the first column.
   static Q4_DEVICE uint32_t offset(int copy, int lane, int64_t ld, int64_t left) {
@@ -342,6 +347,28 @@ struct Panel8 {
     if constexpr (!MC) return s * 128 + ((q ^ swz(s)) << 4);
     else return (16 * q + (s >> 1)) * R + (swz(16 * q + (s >> 1)) << 4) + ((s & 1) << 3);
   }
+  // The same through addresses kept in registers, with constant offsets: `at` panel bytes on, rows
+  // (columns) r0 (a constant) on.
+  struct Reader {
+    uint32_t lo, hi;
+    Q4_DEVICE void start(uint32_t lds, int lane, int first) {   // first: a multiple of 16 (MC: of 64)
+      const uint32_t lb = lane_base(lane);
+      lo = MC ? lds + (lb ^ first) : lds + first * 128 + lb;
+      hi = lds + first * 128 + (lb ^ 64);
+    }
+    Q4_DEVICE void move(int32_t by) { lo += by, hi += by; }
+    Q4_DEVICE Frag read(int at, int r0) const {
+      Frag f;
+      if constexpr (!MC) {
+        typedef __attribute__((address_space(3))) const u32x4_t* lptr;
+        f.lo = *((lptr)(uintptr_t)lo + (at + r0 * 128) / 16);
+        f.hi = *((lptr)(uintptr_t)hi + (at + r0 * 128) / 16);
+      } else {
+        return frag(at, lo, r0);
+      }
+      return f;
+    }
+  };
   // Fragment of rows (columns) r0 .. r0 + 15 of the panel at LDS address `lds`.
   static Q4_DEVICE Frag frag(uint32_t lds, uint32_t lb, int r0) {
     Frag f;
@@ -397,13 +424,144 @@ struct ScaleFeed {
   }
 };
 
+// What a workgroup multiplies: rows m0 .. m_end - 1 (at most BM of them) by columns from n0 on, K
+// steps s_begin .. s_end - 1 of expert x (0: the only matrix).
+struct Work {
+  int64_t m0, m_end, n0;
+  int64_t k_first, k_rows;   // the summed index's range (dw by expert: the expert's tokens)
+  int64_t group0;            // its first group (dw)
+  int x, slice, s_begin, s_end;
+};
+
+// By expert, the grid's workgroups walk the tiles that the offsets make; else each has one.
+// Workgroup b runs on XCD b % 8, and each XCD takes one contiguous range of tiles (its L2 keeps
+// the panels they share), in groups of 8 row tiles that walk the column tiles together.
+template <int MODE, int NT, int BM, int BN>
+struct Tiles {
+  ExpertTiles<NT, MODE == FP8_DW ? 128 : BM> experts;
+  uint32_t mtiles, ntiles, plane, start, mine;
+  Span* span;
+
+  __device__ Tiles(const Fp8Args& g, uint32_t mt, uint32_t nt, Span* sp, int32_t* tot) : ntiles(nt), span(sp) {
+    if (g.offsets) experts.count(g.offsets, g.e, MODE == FP8_DW ? g.K : g.M, tot);
+    mtiles = MODE != FP8_DW && g.offsets ? uint32_t(experts.total) : mt;
+    plane = mtiles * ntiles;
+    const uint32_t total = plane * (MODE == FP8_DW ? uint32_t(g.e) : 1u) * uint32_t(g.ksplit);
+    const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
+    mine = share + (xcd < rest ? 1 : 0), start = xcd * share + (xcd < rest ? xcd : rest);
+  }
+  // All threads call; item: 0 .. mine - 1 of this XCD.
+  __device__ Work at(const Fp8Args& g, uint32_t item) const {
+    uint32_t i = start + item;
+    const uint32_t z = i / plane;   // expert (dw) or K slice
+    i -= z * plane;
+    constexpr uint32_t GM = 8;
+    const uint32_t band = i / (GM * ntiles), b0 = band * GM, gm = mtiles - b0 < GM ? mtiles - b0 : GM;
+    i -= band * GM * ntiles;
+    const uint32_t mt = b0 + i % gm, nt = i / gm;
+    Work w{int64_t(mt) * BM, g.M, int64_t(nt) * BN, 0, g.K, 0, 0, 0, 0, 0};
+    if (MODE != FP8_DW && g.offsets) {
+      experts.find(g.offsets, g.M, int(mt), span);
+      w.x = __builtin_amdgcn_readfirstlane(span->e);
+      w.m0 = __builtin_amdgcn_readfirstlane(int(span->row));
+      w.m_end = w.m0 + __builtin_amdgcn_readfirstlane(span->rows);
+    } else if (MODE == FP8_DW && g.offsets) {
+      w.x = int(z);
+      expert_rows(g.offsets, w.x, g.K, w.k_first, w.k_rows);
+      // the expert's first group: those of the threads before its owner and of the owner's run
+      if (w.x >= experts.beg && w.x < experts.end) {
+        int n = experts.before;
+        for (int y = experts.beg; y < w.x; ++y) {
+          int64_t f, c;
+          expert_rows(g.offsets, y, g.K, f, c);
+          n += int((c + 127) / 128);
+        }
+        span->tile = n;
+      }
+      __syncthreads();
+      w.group0 = __builtin_amdgcn_readfirstlane(span->tile);
+    }
+    const int all = int((w.k_rows + 127) / 128), per = (all + g.ksplit - 1) / g.ksplit;
+    w.slice = g.ksplit > 1 ? int(z) : 0;
+    w.s_begin = min(all, w.slice * per), w.s_end = min(all, w.s_begin + per);
+    return w;
+  }
+};
+
+// W's block scales of a wave's columns.
+template <int MODE>
+struct BlockScale {
+  const float* s;
+  int64_t step;
+  __device__ BlockScale(const Fp8Args& g, const Work& w, int64_t n) {
+    const int64_t nb = std::min<int64_t>(n, g.N - 1) / 128;
+    s = g.sb + w.x * g.sb_stride + (MODE == FP8_Y ? nb * g.sb_ld : nb);
+    step = MODE == FP8_Y ? 1 : g.sb_ld;
+  }
+  Q4_DEVICE float at(int k) const {
+    if constexpr (MODE == FP8_DW) return 1.f;
+    else return load_uniform(s, k * step);
+  }
+};
+
+// The end of a tile: sums of rows m (lane % 16 of each 16), columns n + 16 b + 4 (lane / 16) .. + 3.
+template <int MODE, int MB, int NB>
+Q4_DEVICE void finish(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB][NB], int64_t m, int64_t n, uint32_t turn,
+                      int lane) {
+  constexpr int COLS = 16 * NB;
+  if (g.ksplit > 1) {
+#pragma unroll
+    for (int a = 0; a < MB; ++a) {
+      const int64_t row = m + 16 * a + (lane & 15);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int64_t col = n + 16 * b + 4 * (lane >> 4);
+        float* o = g.part + (int64_t(w.slice) * g.M + row) * g.N + col;
+        if (row < w.m_end && col + 4 <= g.N && (g.N & 3) == 0) {
+          *reinterpret_cast<f32x4_t*>(o) = acc[a][b];
+        } else if (row < w.m_end) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < g.N) o[e] = acc[a][b][e];
+        }
+      }
+    }
+    return;
+  }
+  // through the wave's part of LDS, 32 rows at a time, so that a lane stores 8 columns of one row;
+  // 16-byte chunk c of row r lies at c ^ (r % chunks of a row)
+  constexpr int CH = COLS / 4, LPR = COLS / 8;
+  typedef __attribute__((address_space(3))) f32x4_t* lptr;
+  void* c = g.c;
+  if (MODE == FP8_DW) c = static_cast<uint16_t*>(c) + w.x * g.M * g.ldc;
+#pragma unroll
+  for (int h = 0; h < MB / 2; ++h) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int r = 16 * a + (lane & 15), ch = 4 * b + (lane >> 4);
+        *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4)) = acc[2 * h + a][b];
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 64 / LPR) {
+      const int r = r0 + lane / LPR, ch = 2 * (lane % LPR);
+      const f32x4_t u = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4));
+      const f32x4_t v = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + (((ch + 1) ^ (r & (CH - 1))) << 4));
+      const int64_t row = m + 32 * h + r, col = n + 4 * ch;
+      const float o[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+      if (row < w.m_end && col < g.N)
+        store_row<8>(c, g.dtype, row * g.ldc + col, o, int(std::min<int64_t>(8, g.N - col)));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 // BM x BN per workgroup of WM x WN waves, a ring of NS K steps in LDS: step s + NS - 1 is copied
-// while step s is multiplied, one barrier per step.  By expert, the grid's workgroups walk the
-// tiles that the offsets make; workgroup b runs on XCD b % 8, and each XCD takes one contiguous
-// range of tiles (its L2 keeps the panels they share), in groups of 8 row tiles that walk the
-// column tiles together.
+// while step s is multiplied, one barrier per step.
 template <int MODE, int BM, int BN, int WM, int WN, int NS>
-__global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles_in, uint32_t ntiles) {
+__global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
   constexpr int NW = WM * WN, NT = 64 * NW;
   typedef Panel8<AMC, BM> PA;
@@ -424,67 +582,23 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
   const int wm = wid % WM, wn = wid / WM;
   const uint32_t lds0 = lds_addr(ring);
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
-
-  const bool by_expert = MODE != FP8_DW && g.offsets;
-  ExpertTiles<NT, MODE == FP8_DW ? 128 : BM> tiles;
-  if (g.offsets) tiles.count(g.offsets, g.e, MODE == FP8_DW ? g.K : g.M, tot);
-  const uint32_t mtiles = by_expert ? uint32_t(tiles.total) : mtiles_in;
-  const uint32_t plane = mtiles * ntiles;
-  const uint32_t total = plane * (MODE == FP8_DW ? uint32_t(g.e) : 1u) * uint32_t(g.ksplit);
-  const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
-  const uint32_t mine = share + (xcd < rest ? 1 : 0), start = xcd * share + (xcd < rest ? xcd : rest);
-  for (uint32_t item = blockIdx.x / 8; item < mine; item += (gridDim.x + 7) / 8) {
-    uint32_t i = start + item;
-    const uint32_t z = i / plane;   // expert (dw) or K slice
-    i -= z * plane;
-    constexpr uint32_t GM = 8;
-    const uint32_t band = i / (GM * ntiles), b0 = band * GM, gm = mtiles - b0 < GM ? mtiles - b0 : GM;
-    i -= band * GM * ntiles;
-    const uint32_t mt = b0 + i % gm, nt = i / gm;
-
-    // the tile's rows, its operands, its K steps
-    int64_t m0 = int64_t(mt) * BM, m_end = g.M, k_rows = g.K;
-    const int64_t n0 = int64_t(nt) * BN;
-    int x = 0;
-    int64_t group0 = 0, k_first = 0;
-    if (by_expert) {
-      tiles.find(g.offsets, g.M, int(mt), &span);
-      x = span.e, m0 = span.row, m_end = span.row + span.rows;
-    } else if (MODE == FP8_DW && g.offsets) {
-      x = int(z);
-      expert_rows(g.offsets, x, g.K, k_first, k_rows);
-      // the expert's first group: groups of the threads before its owner, and of its own run
-      if (x >= tiles.beg && x < tiles.end) {
-        int n = tiles.before;
-        for (int y = tiles.beg; y < x; ++y) {
-          int64_t f, c;
-          expert_rows(g.offsets, y, g.K, f, c);
-          n += int((c + 127) / 128);
-        }
-        span.tile = n;
-      }
-      __syncthreads();
-      group0 = span.tile;
-    }
-    const int all = int((k_rows + 127) / 128);
-    const int per = (all + g.ksplit - 1) / g.ksplit;
-    const int slice = g.ksplit > 1 ? int(z) : 0;
-    const int s_begin = min(all, slice * per), s_end = min(all, s_begin + per);
-    const uint8_t* ap = g.a + (MODE == FP8_DW ? k_first * g.lda : 0);
-    const uint8_t* bp = g.b + (MODE == FP8_DW ? k_first * g.ldb : x * g.b_stride);
-    typename PA::Feed fda = PA::feed(ap, g.lda, m_end, k_rows, m0, s_begin);
-    typename PB::Feed fdb = PB::feed(bp, g.ldb, g.N, k_rows, n0, s_begin);
-    ScaleFeed fsa = ScaleFeed::of(g.sa, g.sa_ld, group0 + s_begin, m0, m_end - m0);
-    ScaleFeed fsb = ScaleFeed::of(g.sb, g.sb_ld, group0 + s_begin, n0, g.N - n0);
-    const float* sb = g.sb + x * g.sb_stride;
-    const int64_t nb = std::min<int64_t>(n0 + wn * COLS, g.N - 1) / 128;   // the wave's block of W's columns
-    int64_t k_left = k_rows - int64_t(s_begin) * 128;
-    int si = s_begin, slot_in = 0;
+  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
+  for (uint32_t item = blockIdx.x / 8; item < tiles.mine; item += (gridDim.x + 7) / 8) {
+    const Work w = tiles.at(g, item);
+    const uint8_t* ap = g.a + (MODE == FP8_DW ? w.k_first * g.lda : 0);
+    const uint8_t* bp = g.b + (MODE == FP8_DW ? w.k_first * g.ldb : w.x * g.b_stride);
+    typename PA::Feed fda = PA::feed(ap, g.lda, w.m_end, w.k_rows, w.m0, w.s_begin);
+    typename PB::Feed fdb = PB::feed(bp, g.ldb, g.N, w.k_rows, w.n0, w.s_begin);
+    ScaleFeed fsa = ScaleFeed::of(g.sa, g.sa_ld, w.group0 + w.s_begin, w.m0, w.m_end - w.m0);
+    ScaleFeed fsb = ScaleFeed::of(g.sb, g.sb_ld, w.group0 + w.s_begin, w.n0, g.N - w.n0);
+    const BlockScale<MODE> block(g, w, w.n0 + wn * COLS);
+    int64_t k_left = w.k_rows - int64_t(w.s_begin) * 128;
+    int si = w.s_begin, slot_in = 0;
     auto issue = [&]() {
-      const bool in = si < s_end;
+      const bool in = si < w.s_end;
       const uint32_t at = lds0 + slot_in * STAGE;
-      copies8<PA, CA>(fda.rsrc(in), at, wid * CA, lane, g.lda, AMC ? g.M - m0 : k_left);
-      copies8<PB, CB>(fdb.rsrc(in), at + PA::BYTES, wid * CB, lane, g.ldb, BMC ? g.N - n0 : k_left);
+      copies8<PA, CA>(fda.rsrc(in), at, wid * CA, lane, g.lda, AMC ? g.M - w.m0 : k_left);
+      copies8<PB, CB>(fdb.rsrc(in), at + PA::BYTES, wid * CB, lane, g.ldb, BMC ? g.N - w.n0 : k_left);
       // (64 scales a copy; waves beyond the panel's repeat a copy)
       const int ca = wid % (BM / 64), cb = wid % (BN / 64);
       copy4_to_lds(fsa.rsrc(in), at + PA::BYTES + PB::BYTES + ca * 256, (ca * 64 + lane) * 4);
@@ -495,11 +609,6 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
       ++si;
       slot_in = slot_in == NS - 1 ? 0 : slot_in + 1;
     };
-    auto block_scale = [&](int s) -> float {
-      if constexpr (MODE == FP8_Y) return load_uniform(sb, nb * g.sb_ld + s);
-      else if constexpr (MODE == FP8_DX) return load_uniform(sb, s * g.sb_ld + nb);
-      else return 0.f;
-    };
 
     f32x4_t acc[MB][NB];
 #pragma unroll
@@ -508,87 +617,260 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
       for (int b = 0; b < NB; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) issue();
-    float sb_next = s_begin < s_end ? block_scale(s_begin) : 0.f;
+    float sb_next = w.s_begin < w.s_end ? block.at(w.s_begin) : 0.f;
     int slot = 0;
-    for (int s = s_begin; s < s_end; ++s) {
+    for (int s = w.s_begin; s < w.s_end; ++s) {
       wait_barrier8<(AHEAD - 1) * CPW>();
       const uint32_t base = lds0 + slot * STAGE;
       slot = slot == NS - 1 ? 0 : slot + 1;
       const float sbs = sb_next;
-      if (s + 1 < s_end) sb_next = block_scale(s + 1);
+      if (s + 1 < w.s_end) sb_next = block.at(s + 1);
       typedef __attribute__((address_space(3))) const float* fptr;
       typedef __attribute__((address_space(3))) const f32x4_t* vptr;
       const uint32_t sc = base + PA::BYTES + PB::BYTES;
-      Frag fb[NB];
+      Frag fa[MB], fb[NB];
+      float sa[MB];
       f32x4_t vb[VECB ? NB : 1];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         fb[b] = PB::frag(base + PA::BYTES, lbb, wn * COLS + 16 * b);
         if constexpr (VECB) vb[b] = *(vptr)(uintptr_t)(sc + (BM + wn * COLS + 16 * b + 4 * (lane >> 4)) * 4);
       }
+#pragma unroll
+      for (int a = 0; a < MB; ++a) {
+        fa[a] = PA::frag(base, lba, wm * (BM / WM) + 16 * a);
+        sa[a] = *(fptr)(uintptr_t)(sc + (wm * (BM / WM) + 16 * a + (lane & 15)) * 4);
+      }
       issue();
 #pragma unroll
-      for (int a = 0; a < MB; ++a) {
-        const Frag fa = PA::frag(base, lba, wm * (BM / WM) + 16 * a);
-        const float sa = *(fptr)(uintptr_t)(sc + (wm * (BM / WM) + 16 * a + (lane & 15)) * 4);
+      for (int a = 0; a < MB; ++a)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const f32x4_t p = group_product(fb[b], fa);
+          const f32x4_t p = group_product(fb[b], fa[a]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][b][e] = __builtin_fmaf(p[e], sa * (VECB ? vb[b][e] : sbs), acc[a][b][e]);
+          for (int e = 0; e < 4; ++e) acc[a][b][e] = __builtin_fmaf(p[e], sa[a] * (VECB ? vb[b][e] : sbs), acc[a][b][e]);
         }
-      }
     }
     wait_barrier8<0>();   // every wave's copies and reads are done: LDS is free
+    finish<MODE, MB, NB>(g, w, acc, w.m0 + wm * (BM / WM), w.n0 + wn * COLS, lds0 + wid * (32 * COLS * 4), lane);
+    __syncthreads();   // LDS is read to its end: the next tile's copies may land
+  }
+}
 
-    if (g.ksplit > 1) {
-      // lane: row lane % 16 of its block, columns 4 (lane / 16) .. + 3
+// Large tiles: BM x BN per workgroup of WM x WN waves with one barrier per K step and copies a
+// whole step ahead from two slots of LDS, so that the matrix core never waits for a step to begin.
+// A's panel lies in two halves: A0 the first half of every wave's rows, A1 the second.  Wave tiles
+// are walked row block by row block; each block's products run while the next block's fragment is
+// read and the last block's results are scaled into the sums.  In step s
+//   block MB / 2 - 1 begins with the barrier: every wave has read B and A0 of step s and A1 of
+//     step s - 1; copied since the last barrier, and complete, are A1 of s and B and A0 of s + 1;
+//     then the copies of A1 of s + 1 and of B and A0 of s + 2 go into the slots that are free;
+//   the last block ends with the reads of B and of A0's first block of step s + 1.
+template <int MODE, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
+  constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
+  constexpr int NW = WM * WN, NT = 64 * NW;
+  constexpr int HR = BM / 2, HW = HR / WM;   // rows of half a panel, of it a wave's
+  typedef Panel8<AMC, HR> PA;
+  typedef Panel8<BMC, BN> PB;
+  constexpr int CA = PA::COPIES / NW, CB = PB::COPIES / NW;
+  constexpr int MB = BM / WM / 16, NB = BN / WN / 16, COLS = NB * 16;
+  // LDS: B of both slots, A0, A1, then the scales: A0's, A1's, B's
+  constexpr int A0 = 2 * PB::BYTES, A1 = A0 + 2 * PA::BYTES, S0 = A1 + 2 * PA::BYTES, S1 = S0 + 2 * HR * 4;
+  constexpr int SB = S1 + 2 * HR * 4, BYTES = SB + (VECB ? 2 * BN * 4 : 0);
+  static_assert(HR % 64 == 0 && CA >= 1 && CB >= 1 && MB >= 4, "");
+  static_assert(COLS <= 64, "a wave's columns lie in one block of W");
+  static_assert(S0 >= NW * 32 * COLS * 4, "the turn at a tile's end");
+  __shared__ __align__(16) uint8_t mem[BYTES];
+  __shared__ Span span;
+  __shared__ int32_t tot[NW];
+
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int wm = wid % WM, wn = wid / WM;
+  const uint32_t lds0 = lds_addr(mem);
+  const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
+  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
+  for (uint32_t item = blockIdx.x / 8; item < tiles.mine; item += (gridDim.x + 7) / 8) {
+    const Work w = tiles.at(g, item);
+    const uint8_t* ap = g.a + (MODE == FP8_DW ? w.k_first * g.lda : 0);
+    const uint8_t* bp = g.b + (MODE == FP8_DW ? w.k_first * g.ldb : w.x * g.b_stride);
+    // Row r of half h is row (r / HW) 2 HW + h HW + r % HW of the tile; the rows (MC: the lane's
+    // columns) of a copy lie in one wave's part.
+    const int steps = w.s_end - w.s_begin;
+    const int32_t k_all = int32_t(w.k_rows - int64_t(w.s_begin) * 128);   // (below 2^31: t, n and k are)
+    const int32_t a_left = int32_t(std::min<int64_t>(AMC ? g.M - w.m0 : w.m_end - w.m0, BM));
+    const int32_t b_left = int32_t(std::min<int64_t>(g.N - w.n0, BN));
+    const uint32_t lda = uint32_t(g.lda), ldb = uint32_t(g.ldb);
+    // byte offsets of a lane's chunk from the panel's start at the step (KC: without the first row)
+    uint32_t oa[2], oa1[2], ob[2];   // (by swizzle; MC: oa1 of half 1)
+    int chunk[2];   // KC: the chunk's first code in the step
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int ia = wid * CA + (CA > 1 ? PA::copy_of(v) : 0), ra0 = (ia * 64 + lane) / PA::CPR;
+      const int ca = (lane % PA::CPR) ^ PA::swz(ra0);
+      if (AMC) {
+        const uint32_t row = uint32_t(ra0 - (CA > 1 ? PA::copy_of(v) : 0) * PA::ROWS) * lda;
+        const int at = ca * 16 + ca * 16 / HW * HW;
+        oa[v] = at < a_left ? row + at : kNoByte;
+        oa1[v] = at + HW < a_left ? row + at + HW : kNoByte;
+      } else {
+        oa[v] = uint32_t(lane / PA::CPR) * lda + ca * 16;
+        chunk[v] = ca * 16;
+      }
+      const int ib = wid * CB + PB::copy_of(v), rb0 = (ib * 64 + lane) / PB::CPR;
+      const int cb = (lane % PB::CPR) ^ PB::swz(rb0);
+      if (BMC) ob[v] = cb * 16 < b_left ? uint32_t(rb0 - PB::copy_of(v) * PB::ROWS) * ldb + cb * 16 : kNoByte;
+      else ob[v] = uint32_t(lane / PB::CPR) * ldb + cb * 16, chunk[v] = cb * 16;   // (as in A's copies)
+    }
+    uint64_t a_at = reinterpret_cast<uint64_t>(ap) + (AMC ? w.m0 : w.m0 * g.lda) + w.s_begin * (AMC ? g.lda * 128 : 128);
+    uint64_t b_at = reinterpret_cast<uint64_t>(bp) + (BMC ? w.n0 : w.n0 * g.ldb) + w.s_begin * (BMC ? g.ldb * 128 : 128);
+    uint64_t sa_at = reinterpret_cast<uint64_t>(g.sa + (w.group0 + w.s_begin) * g.sa_ld + w.m0);
+    uint64_t sb_at = reinterpret_cast<uint64_t>(g.sb + (VECB ? (w.group0 + w.s_begin) * g.sb_ld + w.n0 : 0));
+    const BlockScale<MODE> block(g, w, w.n0 + wn * COLS);
+    // The panel of step i: what the descriptor covers ends with the panel's last row (KC: of the
+    // tile, MC: of the step), so that rows beyond read as zeros; past the last step it is empty.
+    auto rsrc = [](uint64_t at, uint32_t bytes) {
+      return u32x4_t{uint32_t(at), uint32_t(at >> 32) & 0xffffu, bytes, 0x00020000u};
+    };
+    auto range = [&](bool mc, int i, uint32_t rows, uint32_t ld) -> uint32_t {
+      if (i >= steps) return 0;
+      return mc ? uint32_t(min(128, k_all - i * 128)) * ld : rows * ld - uint32_t(w.s_begin + i) * 128;
+    };
+    // KC: chunks past K's end take no byte
+    auto inside = [&](int i, uint32_t o, int odd) { return chunk[odd] < k_all - i * 128 ? o : kNoByte; };
+    // Copy j of step i (0: s_begin) of half h of A, of B.
+    auto copy_a = [&](int i, int h, int j) {
+      uint32_t o;
+      if constexpr (AMC) {
+        o = (h ? oa1 : oa)[PA::odd(j)] + j * PA::ROWS * lda;   // (kNoByte stays beyond every range)
+      } else {
+        const int r = (wid * CA + j) * PA::ROWS;
+        o = inside(i, oa[PA::odd(j)], PA::odd(j)) + uint32_t(r + r / HW * HW + h * HW) * lda;
+      }
+      const uint64_t at = a_at + uint64_t(i) * (AMC ? g.lda * 128 : 128);
+      copy_to_lds(rsrc(at, range(AMC, i, a_left, lda)), lds0 + (h ? A1 : A0) + (i & 1) * PA::BYTES + (wid * CA + j) * 1024,
+                  o);
+    };
+    auto copy_b = [&](int i, int j) {
+      uint32_t o = ob[PB::odd(j)];
+      if constexpr (BMC) o += j * PB::ROWS * ldb;
+      else o = inside(i, o, PB::odd(j)) + uint32_t((wid * CB + j) * PB::ROWS) * ldb;
+      const uint64_t at = b_at + uint64_t(i) * (BMC ? g.ldb * 128 : 128);
+      copy_to_lds(rsrc(at, range(BMC, i, b_left, ldb)), lds0 + (i & 1) * PB::BYTES + (wid * CB + j) * 1024, o);
+    };
+    // Scales, 64 a copy and one copy a wave: of a half of A (half 1 one step before half 0, as the
+    // panels), of B.  (Waves beyond their number repeat a copy.)
+    const int sh = wid & 1, sc = (wid >> 1) % (HR / 64);
+    const uint32_t s_off = uint32_t(sc * 64 + lane + (sc * 64 + lane) / HW * HW + sh * HW) * 4;
+    const uint32_t s_rows = uint32_t(std::min<int64_t>(w.m_end - w.m0, BM)) * 4;
+    auto copy_sa = [&](int i) {   // half 0 of step i or half 1 of step i - 1
+      const int k = i - sh;
+      copy4_to_lds(rsrc(sa_at + int64_t(k) * g.sa_ld * 4, k >= 0 && k < steps ? s_rows : 0),
+                   lds0 + (sh ? S1 : S0) + (k & 1) * (HR * 4) + sc * 256, s_off);
+    };
+    auto copy_sb = [&](int i) {
+      const int c = wid % (BN / 64);
+      copy4_to_lds(rsrc(sb_at + uint64_t(i) * g.sb_ld * 4, i < steps ? b_left * 4 : 0),
+                   lds0 + SB + (i & 1) * (BN * 4) + c * 256, (c * 64 + lane) * 4);
+    };
+    // Copy `t` of those that step i begins: A1 of i + 1, B and A0 of i + 2.
+    auto copy_next = [&](int i, int t) {
+      if (t < CA) copy_a(i + 1, 1, t);
+      else if (t < CA + CB) copy_b(i + 2, t - CA);
+      else if (t < 2 * CA + CB) copy_a(i + 2, 0, t - CA - CB);
+      else if (t == 2 * CA + CB) copy_sa(i + 2);
+      else if (VECB && t == 2 * CA + CB + 1) copy_sb(i + 2);
+    };
+    static_assert(2 * CA + CB + (VECB ? 2 : 1) <= (MB / 2 + 1) * NB, "a place for each copy");
+    typedef __attribute__((address_space(3))) const float* fptr;
+    typedef __attribute__((address_space(3))) const f32x4_t* vptr;
+    typename PA::Reader ra;
+    typename PB::Reader rb;
+    ra.start(lds0 + A0, lane, wm * HW);
+    rb.start(lds0, lane, wn * COLS);
+    uint32_t rsa = lds0 + S0 + (wm * HW + (lane & 15)) * 4, rsb = lds0 + SB + (wn * COLS + 4 * (lane >> 4)) * 4;
+    auto read_a = [&](int a) { return ra.read(a / (MB / 2) * (A1 - A0), 16 * (a % (MB / 2))); };
+    auto read_sa = [&](int a) {
+      return *((fptr)(uintptr_t)rsa + (a / (MB / 2) * (S1 - S0) + 64 * (a % (MB / 2))) / 4);
+    };
+    auto read_b = [&](int b) { return rb.read(0, 16 * b); };
+    auto read_sb = [&](int b) { return *((vptr)(uintptr_t)rsb + 4 * b); };
+    // the readers' slot for step i + 1
+    auto other_slot = [&](int i) {
+      const int sign = i & 1 ? -1 : 1;
+      ra.move(sign * PA::BYTES), rb.move(sign * PB::BYTES);
+      rsa += sign * HR * 4, rsb += sign * BN * 4;
+    };
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+
+    f32x4_t acc[MB][NB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
+    constexpr int NEXT = 2 * CA + CB + (VECB ? 2 : 1);   // copies (of a wave) in a step
+    copy_sa(0);
+#pragma unroll
+    for (int j = 0; j < CA; ++j) copy_a(0, 0, j);
+#pragma unroll
+    for (int j = 0; j < CB; ++j) copy_b(0, j);
+    if constexpr (VECB) copy_sb(0);
+#pragma unroll
+    for (int t = 0; t < NEXT; ++t) copy_next(-1, t);
+    float sb_next = steps > 0 ? block.at(w.s_begin) : 0.f;
+    wait_barrier8<0>();
+    Frag fa[2], fb[NB];
+    float sa[2], scale = 0.f, last = 0.f;   // of the block whose results are scaled, of the one before
+    f32x4_t p[2][NB], vb[VECB ? NB : 1], vl[VECB ? NB : 1];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      fb[b] = read_b(b);
+      p[1][b] = f32x4_t{0, 0, 0, 0};
+      if constexpr (VECB) vb[b] = vl[b] = read_sb(b);
+    }
+    fa[0] = read_a(0), sa[0] = read_sa(0);
+    for (int i = 0; i < steps; ++i) {
+      const float sbs = sb_next;
+      if (i + 1 < steps) sb_next = block.at(w.s_begin + i + 1);
 #pragma unroll
       for (int a = 0; a < MB; ++a) {
-        const int64_t m = m0 + wm * (BM / WM) + 16 * a + (lane & 15);
+        const int cur = a & 1;
+        fence();
+        if (a == MB / 2 - 1) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // the next block's fragment
+        if (a + 1 == MB) other_slot(i);
+        fa[1 - cur] = read_a((a + 1) % MB), sa[1 - cur] = read_sa((a + 1) % MB);
+        last = scale;
+        scale = VECB ? sa[cur] : sa[cur] * sbs;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int64_t n = n0 + wn * COLS + 16 * b + 4 * (lane >> 4);
-          float* o = g.part + (int64_t(slice) * g.M + m) * g.N + n;
-          if (m < m_end && n + 4 <= g.N && (g.N & 3) == 0) {
-            *reinterpret_cast<f32x4_t*>(o) = acc[a][b];
-          } else if (m < m_end) {
+          fence();
+          p[cur][b] = group_product(fb[b], fa[cur]);
+          if (a == MB - 1) fb[b] = read_b(b);
+          const int to = a == 0 ? MB - 1 : a - 1;   // the block before (a == 0: of the step before)
+          f32x4_t v = p[1 - cur][b];
+          if constexpr (VECB) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < g.N) o[e] = acc[a][b][e];
+            for (int e = 0; e < 4; ++e) v[e] *= a == 0 ? vl[b][e] : vb[b][e];
+            if (a == MB - 1) vl[b] = vb[b], vb[b] = read_sb(b);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[to][b][e] = __builtin_fmaf(v[e], last, acc[to][b][e]);
+          if (a >= MB / 2 - 1) {
+            fence();
+            copy_next(i, (a - (MB / 2 - 1)) * NB + b);
           }
         }
-      }
-    } else {
-      // through the wave's part of LDS, 32 rows at a time, so that a lane stores 8 columns of one
-      // row; 16-byte chunk c of row r lies at c ^ (r % chunks of a row)
-      constexpr int CH = COLS / 4, LPR = COLS / 8;
-      typedef __attribute__((address_space(3))) f32x4_t* lptr;
-      const uint32_t turn = lds0 + wid * (32 * COLS * 4);
-      void* c = g.c;
-      if (MODE == FP8_DW) c = static_cast<uint16_t*>(c) + x * g.M * g.ldc;
-#pragma unroll
-      for (int h = 0; h < MB / 2; ++h) {
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int r = 16 * a + (lane & 15), ch = 4 * b + (lane >> 4);
-            *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4)) = acc[2 * h + a][b];
-          }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 64 / LPR) {
-          const int r = r0 + lane / LPR, ch = 2 * (lane % LPR);
-          const f32x4_t u = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + ((ch ^ (r & (CH - 1))) << 4));
-          const f32x4_t v = *(lptr)(uintptr_t)(turn + r * (COLS * 4) + (((ch + 1) ^ (r & (CH - 1))) << 4));
-          const int64_t m = m0 + wm * (BM / WM) + 32 * h + r, n = n0 + wn * COLS + 4 * ch;
-          const float o[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-          if (m < m_end && n < g.N) store_row<8>(c, g.dtype, m * g.ldc + n, o, int(std::min<int64_t>(8, g.N - n)));
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
     }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[MB - 1][b][e] = __builtin_fmaf(p[1][b][e] * (VECB ? vl[b][e] : 1.f), scale, acc[MB - 1][b][e]);
+    wait_barrier8<0>();   // every wave's copies and reads are done: LDS is free
+    finish<MODE, MB, NB>(g, w, acc, w.m0 + wm * (BM / WM), w.n0 + wn * COLS, lds0 + wid * (32 * COLS * 4), lane);
     __syncthreads();   // LDS is read to its end: the next tile's copies may land
   }
 }
@@ -736,8 +1018,8 @@ hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
     const int64_t room = 256 * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 3);
     grid = unsigned(std::min<int64_t>(room, ceil_div(items, 8) * 8));
   }
-  if (p.tile == 256) hipLaunchKernelGGL((k_fp8<MODE, 256, 256, 2, 4, 2>), dim3(grid), dim3(512), 0, st, g, mt, nt);
-  else if (p.tile == 128) hipLaunchKernelGGL((k_fp8<MODE, 128, 128, 2, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  if (p.tile == 256) hipLaunchKernelGGL((k_fp8_big<MODE, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, g, mt, nt);
+  else if (p.tile == 128) hipLaunchKernelGGL((k_fp8_big<MODE, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else hipLaunchKernelGGL((k_fp8<MODE, 64, 64, 2, 2, 3>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ksplit == 1) return e;
