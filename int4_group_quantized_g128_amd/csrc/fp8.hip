@@ -181,8 +181,7 @@ __global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
       const int r = slot + 16 * i;
       if (r < rows) {
         if (c < a.k)
-          *reinterpret_cast<u32x2_t*>(a.q_row + (row0 + r) * a.k + c) =
-              u32x2_t{e4m3_codes4(v[i], s), e4m3_codes4(v[i] + 4, s)};
+          *reinterpret_cast<u32x2_t*>(a.q_row + (row0 + r) * a.k + c) = e4m3_codes8(v[i], s);
         if (lane16 == 0) a.s_row[cb * a.t + row0 + r] = s;
       }
     }
@@ -213,17 +212,24 @@ __global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.s_col[int64_t(tile) * a.k + c + j] = s[j];
       }
+      float inv[8];
+      bool plain = true;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) inv[j] = 1.f / s[j], plain = plain && s[j] >= kPlainScale;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = slot + 16 * i;
         float q[8];
+        if (plain) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = s[j] > 0.f ? fminf(fmaxf(v[i][j] / s[j], -kE4m3Max), kE4m3Max) : 0.f;
-        int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-        w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
-        int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-        w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], w1, true);
-        if (r < rows) *reinterpret_cast<u32x2_t*>(a.q_col + (row0 + r) * a.k + c) = u32x2_t{uint32_t(w0), uint32_t(w1)};
+          for (int j = 0; j < 8; ++j) q[j] = e4m3_clamp(quotient(v[i][j], s[j], inv[j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = s[j] > 0.f ? e4m3_clamp(v[i][j] / s[j]) : 0.f;
+        }
+        if (r < rows)
+          *reinterpret_cast<u32x2_t*>(a.q_col + (row0 + r) * a.k + c) =
+              u32x2_t{e4m3_pack4(q[0], q[1], q[2], q[3]), e4m3_pack4(q[4], q[5], q[6], q[7])};
       }
     }
   }
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(256) k_quantize_fp8_blocks(const void* __restr
   for (int i = 0; i < 8; ++i) {
     const int r = (threadIdx.x >> 4) + 16 * i;
     if (r < rows && c < k)
-      *reinterpret_cast<u32x2_t*>(q + (row0 + r) * k + c) = u32x2_t{e4m3_codes4(v[i], sc), e4m3_codes4(v[i] + 4, sc)};
+      *reinterpret_cast<u32x2_t*>(q + (row0 + r) * k + c) = e4m3_codes8(v[i], sc);
   }
   if (threadIdx.x == 0) s[blockIdx.x * int64_t(gridDim.y) + blockIdx.y] = sc;
 }
@@ -657,16 +663,16 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
   }
 }
 
-// Large tiles: BM x BN per workgroup of WM x WN waves with one barrier per K step and copies a
-// whole step ahead from two slots of LDS, so that the matrix core never waits for a step to begin.
+// Large tiles: BM x BN per workgroup of WM x WN waves with one barrier per K step and copies
+// SLOTS - 1 whole steps ahead, so that the matrix core never waits for a step to begin.
 // A's panel lies in two halves: A0 the first half of every wave's rows, A1 the second.  Wave tiles
 // are walked row block by row block; each block's products run while the next block's fragment is
 // read and the last block's results are scaled into the sums.  In step s
 //   block MB / 2 - 1 begins with the barrier: every wave has read B and A0 of step s and A1 of
-//     step s - 1; copied since the last barrier, and complete, are A1 of s and B and A0 of s + 1;
-//     then the copies of A1 of s + 1 and of B and A0 of s + 2 go into the slots that are free;
+//     step s - 1, and A1 of s and B and A0 of s + 1 are in LDS; then the copies of A1 of
+//     s + SLOTS - 1 and of B and A0 of s + SLOTS go into the places that are free;
 //   the last block ends with the reads of B and of A0's first block of step s + 1.
-template <int MODE, int BM, int BN, int WM, int WN>
+template <int MODE, int BM, int BN, int WM, int WN, int SLOTS>
 __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
   constexpr int NW = WM * WN, NT = 64 * NW;
@@ -675,9 +681,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
   typedef Panel8<BMC, BN> PB;
   constexpr int CA = PA::COPIES / NW, CB = PB::COPIES / NW;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16, COLS = NB * 16;
-  // LDS: B of both slots, A0, A1, then the scales: A0's, A1's, B's
-  constexpr int A0 = 2 * PB::BYTES, A1 = A0 + 2 * PA::BYTES, S0 = A1 + 2 * PA::BYTES, S1 = S0 + 2 * HR * 4;
-  constexpr int SB = S1 + 2 * HR * 4, BYTES = SB + (VECB ? 2 * BN * 4 : 0);
+  // LDS: B of every slot, A0, A1, then the scales: A0's, A1's, B's
+  constexpr int A0 = SLOTS * PB::BYTES, A1 = A0 + SLOTS * PA::BYTES, S0 = A1 + SLOTS * PA::BYTES;
+  constexpr int S1 = S0 + SLOTS * HR * 4, SB = S1 + SLOTS * HR * 4, BYTES = SB + (VECB ? SLOTS * BN * 4 : 0);
   static_assert(HR % 64 == 0 && CA >= 1 && CB >= 1 && MB >= 4, "");
   static_assert(COLS <= 64, "a wave's columns lie in one block of W");
   static_assert(S0 >= NW * 32 * COLS * 4, "the turn at a tile's end");
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
 
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int wm = wid % WM, wn = wid / WM;
+  const int wm = wid / WN, wn = wid % WN;   // (a SIMD's two waves in different rows)
   const uint32_t lds0 = lds_addr(mem);
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
   const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
@@ -734,13 +740,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       return u32x4_t{uint32_t(at), uint32_t(at >> 32) & 0xffffu, bytes, 0x00020000u};
     };
     auto range = [&](bool mc, int i, uint32_t rows, uint32_t ld) -> uint32_t {
-      if (i >= steps) return 0;
+      if (i < 0 || i >= steps) return 0;
       return mc ? uint32_t(min(128, k_all - i * 128)) * ld : rows * ld - uint32_t(w.s_begin + i) * 128;
     };
     // KC: chunks past K's end take no byte
     auto inside = [&](int i, uint32_t o, int odd) { return chunk[odd] < k_all - i * 128 ? o : kNoByte; };
-    // Copy j of step i (0: s_begin) of half h of A, of B.
-    auto copy_a = [&](int i, int h, int j) {
+    // Copy j of step i (0: s_begin) of half h of A, of B, into a slot.
+    auto copy_a = [&](int i, int slot, int h, int j) {
       uint32_t o;
       if constexpr (AMC) {
         o = (h ? oa1 : oa)[PA::odd(j)] + j * PA::ROWS * lda;   // (kNoByte stays beyond every range)
@@ -748,39 +754,40 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
         const int r = (wid * CA + j) * PA::ROWS;
         o = inside(i, oa[PA::odd(j)], PA::odd(j)) + uint32_t(r + r / HW * HW + h * HW) * lda;
       }
-      const uint64_t at = a_at + uint64_t(i) * (AMC ? g.lda * 128 : 128);
-      copy_to_lds(rsrc(at, range(AMC, i, a_left, lda)), lds0 + (h ? A1 : A0) + (i & 1) * PA::BYTES + (wid * CA + j) * 1024,
-                  o);
+      const uint64_t at = a_at + int64_t(i) * (AMC ? g.lda * 128 : 128);
+      copy_to_lds(rsrc(at, range(AMC, i, a_left, lda)), lds0 + (h ? A1 : A0) + slot * PA::BYTES + (wid * CA + j) * 1024, o);
     };
-    auto copy_b = [&](int i, int j) {
+    auto copy_b = [&](int i, int slot, int j) {
       uint32_t o = ob[PB::odd(j)];
       if constexpr (BMC) o += j * PB::ROWS * ldb;
       else o = inside(i, o, PB::odd(j)) + uint32_t((wid * CB + j) * PB::ROWS) * ldb;
-      const uint64_t at = b_at + uint64_t(i) * (BMC ? g.ldb * 128 : 128);
-      copy_to_lds(rsrc(at, range(BMC, i, b_left, ldb)), lds0 + (i & 1) * PB::BYTES + (wid * CB + j) * 1024, o);
+      const uint64_t at = b_at + int64_t(i) * (BMC ? g.ldb * 128 : 128);
+      copy_to_lds(rsrc(at, range(BMC, i, b_left, ldb)), lds0 + slot * PB::BYTES + (wid * CB + j) * 1024, o);
     };
     // Scales, 64 a copy and one copy a wave: of a half of A (half 1 one step before half 0, as the
     // panels), of B.  (Waves beyond their number repeat a copy.)
     const int sh = wid & 1, sc = (wid >> 1) % (HR / 64);
     const uint32_t s_off = uint32_t(sc * 64 + lane + (sc * 64 + lane) / HW * HW + sh * HW) * 4;
     const uint32_t s_rows = uint32_t(std::min<int64_t>(w.m_end - w.m0, BM)) * 4;
-    auto copy_sa = [&](int i) {   // half 0 of step i or half 1 of step i - 1
+    auto copy_sa = [&](int i, int slot, int before) {   // half 0 of step i or half 1 of step i - 1
       const int k = i - sh;
       copy4_to_lds(rsrc(sa_at + int64_t(k) * g.sa_ld * 4, k >= 0 && k < steps ? s_rows : 0),
-                   lds0 + (sh ? S1 : S0) + (k & 1) * (HR * 4) + sc * 256, s_off);
+                   lds0 + (sh ? S1 : S0) + (sh ? before : slot) * (HR * 4) + sc * 256, s_off);
     };
-    auto copy_sb = [&](int i) {
+    auto copy_sb = [&](int i, int slot) {
       const int c = wid % (BN / 64);
-      copy4_to_lds(rsrc(sb_at + uint64_t(i) * g.sb_ld * 4, i < steps ? b_left * 4 : 0),
-                   lds0 + SB + (i & 1) * (BN * 4) + c * 256, (c * 64 + lane) * 4);
+      copy4_to_lds(rsrc(sb_at + int64_t(i) * g.sb_ld * 4, i < steps ? b_left * 4 : 0),
+                   lds0 + SB + slot * (BN * 4) + c * 256, (c * 64 + lane) * 4);
     };
-    // Copy `t` of those that step i begins: A1 of i + 1, B and A0 of i + 2.
-    auto copy_next = [&](int i, int t) {
-      if (t < CA) copy_a(i + 1, 1, t);
-      else if (t < CA + CB) copy_b(i + 2, t - CA);
-      else if (t < 2 * CA + CB) copy_a(i + 2, 0, t - CA - CB);
-      else if (t == 2 * CA + CB) copy_sa(i + 2);
-      else if (VECB && t == 2 * CA + CB + 1) copy_sb(i + 2);
+    // Copy `t` of those that step i, which lies in slot `sl`, begins: A1 of i + SLOTS - 1, B and A0 of
+    // i + SLOTS.
+    auto copy_next = [&](int i, int sl, int t) {
+      const int before = sl == 0 ? SLOTS - 1 : sl - 1;
+      if (t < CA) copy_a(i + SLOTS - 1, before, 1, t);
+      else if (t < CA + CB) copy_b(i + SLOTS, sl, t - CA);
+      else if (t < 2 * CA + CB) copy_a(i + SLOTS, sl, 0, t - CA - CB);
+      else if (t == 2 * CA + CB) copy_sa(i + SLOTS, sl, before);
+      else if (VECB && t == 2 * CA + CB + 1) copy_sb(i + SLOTS, sl);
     };
     static_assert(2 * CA + CB + (VECB ? 2 : 1) <= (MB / 2 + 1) * NB, "a place for each copy");
     typedef __attribute__((address_space(3))) const float* fptr;
@@ -796,11 +803,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     };
     auto read_b = [&](int b) { return rb.read(0, 16 * b); };
     auto read_sb = [&](int b) { return *((vptr)(uintptr_t)rsb + 4 * b); };
-    // the readers' slot for step i + 1
-    auto other_slot = [&](int i) {
-      const int sign = i & 1 ? -1 : 1;
-      ra.move(sign * PA::BYTES), rb.move(sign * PB::BYTES);
-      rsa += sign * HR * 4, rsb += sign * BN * 4;
+    // the readers from slot `sl` to the next
+    auto next_slot = [&](int sl) {
+      const int by = sl == SLOTS - 1 ? 1 - SLOTS : 1;
+      ra.move(by * PA::BYTES), rb.move(by * PB::BYTES);
+      rsa += by * HR * 4, rsb += by * BN * 4;
     };
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
@@ -810,16 +817,22 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
     constexpr int NEXT = 2 * CA + CB + (VECB ? 2 : 1);   // copies (of a wave) in a step
-    copy_sa(0);
 #pragma unroll
-    for (int j = 0; j < CA; ++j) copy_a(0, 0, j);
+    for (int i = -SLOTS; i < 0; ++i)
 #pragma unroll
-    for (int j = 0; j < CB; ++j) copy_b(0, j);
-    if constexpr (VECB) copy_sb(0);
-#pragma unroll
-    for (int t = 0; t < NEXT; ++t) copy_next(-1, t);
+      for (int t = 0; t < NEXT; ++t) copy_next(i, i + SLOTS, t);
     float sb_next = steps > 0 ? block.at(w.s_begin) : 0.f;
-    wait_barrier8<0>();
+    wait_barrier8<(SLOTS - 1) * NEXT>();
+    if (w.m0 + wm * (BM / WM) >= w.m_end) {   // no row of the wave's: it copies for the others
+      for (int i = 0, sl = 0; i < steps; ++i, sl = sl == SLOTS - 1 ? 0 : sl + 1) {
+        wait_barrier8<(SLOTS - 2) * NEXT>();
+#pragma unroll
+        for (int t = 0; t < NEXT; ++t) copy_next(i, sl, t);
+      }
+      wait_barrier8<0>();
+      __syncthreads();
+      continue;
+    }
     Frag fa[2], fb[NB];
     float sa[2], scale = 0.f, last = 0.f;   // of the block whose results are scaled, of the one before
     f32x4_t p[2][NB], vb[VECB ? NB : 1], vl[VECB ? NB : 1];
@@ -830,6 +843,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       if constexpr (VECB) vb[b] = vl[b] = read_sb(b);
     }
     fa[0] = read_a(0), sa[0] = read_sa(0);
+    int sl = 0;
     for (int i = 0; i < steps; ++i) {
       const float sbs = sb_next;
       if (i + 1 < steps) sb_next = block.at(w.s_begin + i + 1);
@@ -837,9 +851,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       for (int a = 0; a < MB; ++a) {
         const int cur = a & 1;
         fence();
-        if (a == MB / 2 - 1) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (a == MB / 2 - 1) wait_barrier8<(SLOTS - 2) * NEXT>();
         // the next block's fragment
-        if (a + 1 == MB) other_slot(i);
+        if (a + 1 == MB) next_slot(sl);
         fa[1 - cur] = read_a((a + 1) % MB), sa[1 - cur] = read_sa((a + 1) % MB);
         last = scale;
         scale = VECB ? sa[cur] : sa[cur] * sbs;
@@ -859,10 +873,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
           for (int e = 0; e < 4; ++e) acc[to][b][e] = __builtin_fmaf(v[e], last, acc[to][b][e]);
           if (a >= MB / 2 - 1) {
             fence();
-            copy_next(i, (a - (MB / 2 - 1)) * NB + b);
+            copy_next(i, sl, (a - (MB / 2 - 1)) * NB + b);
           }
         }
       }
+      sl = sl == SLOTS - 1 ? 0 : sl + 1;
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -1018,8 +1033,8 @@ hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
     const int64_t room = 256 * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 3);
     grid = unsigned(std::min<int64_t>(room, ceil_div(items, 8) * 8));
   }
-  if (p.tile == 256) hipLaunchKernelGGL((k_fp8_big<MODE, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, g, mt, nt);
-  else if (p.tile == 128) hipLaunchKernelGGL((k_fp8_big<MODE, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
+  if (p.tile == 256) hipLaunchKernelGGL((k_fp8_big<MODE, 256, 256, 2, 4, 2>), dim3(grid), dim3(512), 0, st, g, mt, nt);
+  else if (p.tile == 128) hipLaunchKernelGGL((k_fp8_big<MODE, 128, 128, 2, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else hipLaunchKernelGGL((k_fp8<MODE, 64, 64, 2, 2, 3>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ksplit == 1) return e;

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, magnitude(v[i]));
       const float s = e4m3_scale(row16_max(m));
-      const u32x2_t q = {e4m3_codes4(v, s), e4m3_codes4(v + 4, s)};
+      const u32x2_t q = e4m3_codes8(v, s);
       for (int j = 0; j < a.k; ++j) {
         const int32_t at = p[j];
         if (at < 0) continue;
