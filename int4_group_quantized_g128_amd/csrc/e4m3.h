@@ -25,11 +25,24 @@ template <int DT> struct Elem {
   struct __attribute__((packed, aligned(SIZE))) Raw {
     uint32_t w[4];
   };
+  template <bool NT = false>
   static Q4_DEVICE Raw load(const void* p, int64_t i) {
-    return *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + i * SIZE);
+    const uint8_t* at = static_cast<const uint8_t*>(p) + i * SIZE;
+    if constexpr (NT) {
+      typedef u32x4_t any_t __attribute__((aligned(2)));
+      return bitcast<Raw>(u32x4_t(__builtin_nontemporal_load(reinterpret_cast<const any_t*>(at))));
+    }
+    return *reinterpret_cast<const Raw*>(at);
   }
+  template <bool NT = false>
   static Q4_DEVICE void store(void* p, int64_t i, const Raw& r) {
-    *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + i * SIZE) = r;
+    uint8_t* at = static_cast<uint8_t*>(p) + i * SIZE;
+    if constexpr (NT) {
+      typedef u32x4_t any_t __attribute__((aligned(2)));
+      __builtin_nontemporal_store(bitcast<u32x4_t>(r), reinterpret_cast<any_t*>(at));
+    } else {
+      *reinterpret_cast<Raw*>(at) = r;
+    }
   }
   static Q4_DEVICE float value(const Raw& r, int i) {
     if constexpr (DT == 0) return __uint_as_float(r.w[i]);

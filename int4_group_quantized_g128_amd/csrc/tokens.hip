@@ -8,6 +8,7 @@
 // All are bound by the rows' bytes.  Sums are fp32 in ascending j, so equal inputs give equal
 // bits; nothing is added by atomics.
 #include <algorithm>
+#include <type_traits>
 
 #include "e4m3.h"
 #include "tokens.h"
@@ -17,12 +18,15 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kCacheBytes = int64_t(256) << 20;   // the last-level cache
 
 // Slots that a workgroup ranks against each other: a range of whole tokens of at most this many
 // slots (one token where it has more).
 constexpr int kRangeSlots = 1024;
-// Up to this many slots there is one range, and each workgroup finds the positions by itself.
-constexpr int64_t kOneRange = 4096;
+// Up to this many slots there is one range, and each workgroup finds the positions by itself: one
+// launch instead of three (a call of 500 tokens of 2048, k = 4: 12.8 us against 20.2; 500 of 7168,
+// k = 8, 4000 slots: 26.3 against 21.7).
+constexpr int64_t kOneRange = 2048;
 
 int64_t range_tokens(int64_t t, int32_t k) {
   return t * k <= kOneRange ? std::max<int64_t>(1, t) : std::max<int64_t>(1, kRangeSlots / k);
@@ -36,6 +40,20 @@ int64_t ranges(int64_t t, int32_t k) {
 Q4_DEVICE int slot_local(const int32_t* ids, int64_t s, int first, int e) {
   const uint32_t x = uint32_t(ids[s]) - uint32_t(first);
   return x < uint32_t(e) ? int(x) : e;
+}
+
+// use(i, expert of slot s0 + i) for i below n, a workgroup's threads side by side, 8 loads in flight.
+template <typename F>
+Q4_DEVICE void each_slot(const int32_t* ids, int64_t s0, int n, int first, int e, F use) {
+  constexpr int U = 8;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    int x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = i0 + u * kThreads < n ? slot_local(ids, s0 + i0 + u * kThreads, first, e) : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kThreads < n) use(i0 + u * kThreads, x[u]);
+  }
 }
 
 // In-place exclusive scan of n ints in LDS by 64 * W threads; returns the total.
@@ -77,44 +95,57 @@ __global__ void __launch_bounds__(kThreads) k_order_count(const int32_t* __restr
   for (int x = threadIdx.x; x <= e; x += kThreads) lds[x] = 0;
   __syncthreads();
   const int64_t beg = int64_t(blockIdx.x) * per * k, end = std::min<int64_t>(t * k, beg + per * k);
-  for (int64_t s = beg + threadIdx.x; s < end; s += kThreads) atomicAdd(&lds[slot_local(ids, s, first, e)], 1);
+  each_slot(ids, beg, int(end - beg), first, e, [&](int, int x) { atomicAdd(&lds[x], 1); });
   __syncthreads();
   for (int x = threadIdx.x; x <= e; x += kThreads) cnt[int64_t(blockIdx.x) * (e + 1) + x] = lds[x];
 }
 
-// The ranges' counts [nr][e + 1] become each range's first position per expert; offsets.
-__global__ void __launch_bounds__(1024) k_order_plan(int32_t* __restrict__ cnt, int nr, int32_t e,
+// The ranges' counts [nr][e + 1] become each range's first position per expert; offsets.  Thread
+// (part, x) adds a part of the ranges of expert x, as many parts as 1024 threads make.
+__global__ void __launch_bounds__(1024) k_order_plan(int32_t* __restrict__ cnt, int nr, int32_t e, int parts,
                                                      int32_t* __restrict__ offsets) {
-  extern __shared__ int32_t lds[];   // [e + 1]
+  extern __shared__ int32_t lds[];   // [e + 1], [parts][e + 1]
   __shared__ int32_t tot[16];
   constexpr int U = 8;   // ranges in flight
   const int64_t ld = e + 1;
-  for (int x = threadIdx.x; x <= e; x += 1024) {
-    int32_t run = 0;
-    for (int r = 0; r < nr; r += U) {
+  int32_t* sums = lds + e + 1;
+  const int per = (nr + parts - 1) / parts;
+  auto walk = [&](int x, int r0, int r1, auto use) {
+    for (int r = r0; r < r1; r += U) {
       int32_t c[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) c[u] = r + u < nr ? cnt[(r + u) * ld + x] : 0;
+      for (int u = 0; u < U; ++u) c[u] = r + u < r1 ? cnt[(r + u) * ld + x] : 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) run += c[u];
+      for (int u = 0; u < U; ++u)
+        if (r + u < r1) use(r + u, c[u]);
+    }
+  };
+  for (int i = threadIdx.x; i < parts * (e + 1); i += 1024) {
+    const int part = i / (e + 1), x = i - part * (e + 1);
+    int32_t run = 0;
+    walk(x, part * per, min(nr, (part + 1) * per), [&](int, int32_t c) { run += c; });
+    sums[i] = run;
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x <= e; x += 1024) {
+    int32_t run = 0;
+    for (int p = 0; p < parts; ++p) {
+      const int32_t c = sums[p * (e + 1) + x];
+      sums[p * (e + 1) + x] = run;
+      run += c;
     }
     lds[x] = run;
   }
   __syncthreads();
   scan_lds<16>(lds, e + 1, tot);
-  for (int x = threadIdx.x; x <= e; x += 1024) {
-    int32_t run = lds[x];
-    offsets[x] = run;   // (x == e: the held slots)
-    for (int r = 0; r < nr; r += U) {
-      int32_t c[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) c[u] = r + u < nr ? cnt[(r + u) * ld + x] : 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r + u < nr) cnt[(r + u) * ld + x] = run;
-        run += c[u];
-      }
-    }
+  for (int x = threadIdx.x; x <= e; x += 1024) offsets[x] = lds[x];   // (x == e: the held slots)
+  for (int i = threadIdx.x; i < parts * (e + 1); i += 1024) {
+    const int part = i / (e + 1), x = i - part * (e + 1);
+    int32_t run = lds[x] + sums[i];
+    walk(x, part * per, min(nr, (part + 1) * per), [&](int r, int32_t c) {
+      cnt[r * ld + x] = run;
+      run += c;
+    });
   }
 }
 
@@ -122,7 +153,7 @@ __global__ void __launch_bounds__(1024) k_order_plan(int32_t* __restrict__ cnt, 
 __device__ void offsets_of(const DispatchArgs& a, int32_t* hist, int32_t* tot) {
   for (int x = threadIdx.x; x <= a.e; x += kThreads) hist[x] = 0;
   __syncthreads();
-  for (int64_t s = threadIdx.x; s < a.t * a.k; s += kThreads) atomicAdd(&hist[slot_local(a.ids, s, a.first, a.e)], 1);
+  each_slot(a.ids, 0, int(a.t * a.k), a.first, a.e, [&](int, int x) { atomicAdd(&hist[x], 1); });
   __syncthreads();
   scan_lds<kThreads / 64>(hist, a.e + 1, tot);
   for (int x = threadIdx.x; x <= a.e; x += kThreads) a.offsets[x] = hist[x];
@@ -132,8 +163,9 @@ __device__ void offsets_of(const DispatchArgs& a, int32_t* hist, int32_t* tot) {
 // Positions: a slot's key is (expert, slot); its position is the number of smaller keys, which
 // the waves count by ballots over the range's experts in LDS -- all slots with one range, else the
 // same expert's slots of the range, on top of the range's first position.  Then the rows go out,
-// each token read once and written k times.
-template <bool QUANT, int DT, int TPW>
+// each token read once and written k times.  NT: rows larger than the last-level cache are written
+// past it (4096 tokens of 7168, k = 8: 121 -> 106 us).
+template <bool QUANT, int DT, int TPW, bool NT>
 __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t per, const int32_t* __restrict__ base,
                                                        int64_t col_block) {
   typedef Elem<DT> E;
@@ -154,17 +186,35 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
   int32_t* pos = lds;                                      // [TPW k]
   uint16_t* ex = reinterpret_cast<uint16_t*>(lds + TPW * a.k);   // [slots of a range]
   const int64_t slot0 = tok0 * a.k;
-  for (int i = tid; i < n; i += kThreads) ex[i] = uint16_t(slot_local(a.ids, slot0 + i, a.first, a.e));
-  for (int i = tid; i < ns; i += kThreads) pos[i] = 0;
+  // the thread's first columns are on their way while the slots are ranked
+  constexpr int TPT = kThreads / TPW;   // threads per token
+  constexpr int VEC = QUANT ? 8 : E::VEC, RAWS = VEC / E::VEC;
+  const int tk = min(tid / TPT, nt - 1), l = tid % TPT;
+  const int64_t row = tok0 + mine + tk;
+  const int64_t c0 = int64_t(blockIdx.y) * col_block, c1 = std::min<int64_t>(a.h, c0 + col_block);
+  typename E::Raw raw[RAWS];
+  auto load = [&](int64_t c) {
+#pragma unroll
+    for (int i = 0; i < RAWS; ++i) raw[i] = E::load(a.x, row * a.h + c + i * E::VEC);
+  };
+  if (c0 + l * VEC + VEC <= c1) load(c0 + l * VEC);
+  each_slot(a.ids, slot0, n, a.first, a.e, [&](int i, int x) { ex[i] = uint16_t(x); });
   __syncthreads();
-  for (int i0 = wid * 64; i0 < n; i0 += kThreads) {
-    const int i = i0 + lane;
-    const int x = i < n ? int(ex[i]) : 0x10000;
-    for (int j = 0; j < ns; ++j) {
-      const int xj = ex[s0 + j];
-      const bool before = (x == xj && i < s0 + j) || (!base && x < xj);
-      const int c = __popcll(__ballot(before));
-      if (lane == 0 && c) atomicAdd(&pos[j], c);
+  // (the experts of U 64 slots stay in registers while the wave's slots are ranked against them)
+  constexpr int U = 16;
+  for (int i0 = 0; i0 < n; i0 += 64 * U) {
+    int x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = i0 + 64 * u + lane < n ? int(ex[i0 + 64 * u + lane]) : 0x10000;
+    for (int j = wid; j < ns; j += kThreads / 64) {
+      const int xj = __builtin_amdgcn_readfirstlane(int(ex[s0 + j]));
+      int c = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool earlier = i0 + 64 * u + lane < s0 + j;
+        c += __popcll(__ballot(base ? x[u] == xj && earlier : x[u] < xj + (earlier ? 1 : 0)));
+      }
+      if (lane == 0) pos[j] = i0 ? pos[j] + c : c;
     }
   }
   __syncthreads();
@@ -179,31 +229,20 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
     }
   }
   __syncthreads();
-  constexpr int TPT = kThreads / TPW;   // threads per token
-  const int tk = tid / TPT, l = tid % TPT;
-  if (tk >= nt) return;
-  const int64_t row = tok0 + mine + tk;
+  if (tid / TPT >= nt) return;
   const int32_t* p = pos + tk * a.k;
-  const int64_t c0 = int64_t(blockIdx.y) * col_block, c1 = std::min<int64_t>(a.h, c0 + col_block);
   if constexpr (QUANT) {
     // 16 lanes hold a group's 128 columns
     const int64_t slots = a.t * a.k;
     for (int64_t c = c0 + l * 8; c < (c1 + 127) / 128 * 128; c += TPT * 8) {
-      float v[8];
+      float v[8], m = 0.f;
       const bool in = c < c1;   // (h is a multiple of 16)
-      if (in) {
-        typename E::Raw r[8 / E::VEC];
+      if (in && c >= c0 + TPT * 8) load(c);
 #pragma unroll
-        for (int i = 0; i < 8 / E::VEC; ++i) r[i] = E::load(a.x, row * a.h + c + i * E::VEC);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = E::value(r[i / E::VEC], i % E::VEC);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = in ? E::value(raw[i / E::VEC], i % E::VEC) : 0.f;
+        m = fmaxf(m, magnitude(v[i]));
       }
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, magnitude(v[i]));
       const float s = e4m3_scale(row16_max(m));
       const u32x2_t q = e4m3_codes8(v, s);
       for (int j = 0; j < a.k; ++j) {
@@ -214,13 +253,13 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
       }
     }
   } else {
-    for (int64_t c = c0 + l * E::VEC; c < c1; c += TPT * E::VEC) {
-      if (c + E::VEC <= a.h) {
-        const typename E::Raw r = E::load(a.x, row * a.h + c);
+    for (int64_t c = c0 + l * VEC; c < c1; c += TPT * VEC) {
+      if (c + VEC <= c1) {
+        if (c >= c0 + TPT * VEC) load(c);
         for (int j = 0; j < a.k; ++j)
-          if (p[j] >= 0) E::store(a.out, p[j] * a.h + c, r);
+          if (p[j] >= 0) E::template store<NT>(a.out, p[j] * a.h + c, raw[0]);
       } else {
-        for (int64_t i = c; i < a.h; ++i)
+        for (int64_t i = c; i < c1; ++i)
           for (int j = 0; j < a.k; ++j)
             if (p[j] >= 0) E::put(a.out, p[j] * a.h + i, E::get(a.x, row * a.h + i));
       }
@@ -228,14 +267,16 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
   }
 }
 
-// out[t] = sum_j w y[inv] (+ add): a wave per token and 64 vectors of columns, U rows in flight.
-template <int DT>
+// out[t] = sum_j w y[inv] (+ add): a wave per token and 64 vectors of columns, U rows in flight (as
+// many as k: 4096 tokens of 2048, k = 2, 8 in flight 13.6 us, 2 9.5).  NT: rows larger than the
+// last-level cache are read past it (4096 tokens of 7168, k = 8: 105 -> 91 us; of 2048, k = 2, which
+// the cache holds, 10.0 -> 11.0).
+template <int DT, int U, bool NT>
 __global__ void __launch_bounds__(kThreads) k_tokens_combine(const void* __restrict__ y, const int32_t* __restrict__ inv,
                                                              const float* __restrict__ w, const void* __restrict__ add,
                                                              int64_t t, int32_t k, int64_t h, uint32_t chunks,
                                                              void* __restrict__ out) {
   typedef Elem<DT> E;
-  constexpr int U = 8;
   const uint32_t item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int64_t tok = item / chunks;
   if (tok >= t) return;
@@ -263,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens_combine(const void* __restr
     typename E::Raw v[U];
     if (whole) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = E::load(y, at[u]);
+      for (int u = 0; u < U; ++u) v[u] = E::template load<NT>(y, at[u]);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -293,8 +334,10 @@ __global__ void __launch_bounds__(kThreads) k_tokens_combine(const void* __restr
   }
 }
 
-// dy and dw of a slot by TPS threads (a wave, or the workgroup where there are few slots).
-template <int DT, int TPS>
+// dy and dw of a slot by TPS threads (a wave, or the workgroup where there are few slots).  NT: y and
+// dy larger than the last-level cache pass it by (4096 tokens of 7168, k = 8: 207 -> 190 us; 2048
+// wide, k = 2, 14.7 -> 17.1).
+template <int DT, int TPS, bool NT>
 __global__ void __launch_bounds__(kThreads) k_tokens_combine_bwd(const void* __restrict__ dout,
                                                                  const void* __restrict__ y,
                                                                  const int32_t* __restrict__ inv,
@@ -318,14 +361,14 @@ __global__ void __launch_bounds__(kThreads) k_tokens_combine_bwd(const void* __r
       if (c + E::VEC <= h) {
         const typename E::Raw d = E::load(dout, d0 + c);
         if (dw) {
-          const typename E::Raw v = E::load(y, y0 + c);
+          const typename E::Raw v = E::template load<NT>(y, y0 + c);
 #pragma unroll
           for (int i = 0; i < E::VEC; ++i) dot = __builtin_fmaf(E::value(d, i), E::value(v, i), dot);
         }
         float g[E::VEC];
 #pragma unroll
         for (int i = 0; i < E::VEC; ++i) g[i] = ws * E::value(d, i);
-        E::store(dy, y0 + c, E::pack(g));
+        E::template store<NT>(dy, y0 + c, E::pack(g));
       } else {
         for (int64_t i = c; i < h; ++i) {
           const float d = E::get(dout, d0 + i);
@@ -347,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens_combine_bwd(const void* __r
   }
 }
 
-template <bool QUANT, int DT, int TPW>
+template <bool QUANT, int DT, int TPW, bool NT>
 hipError_t dispatch_as(const DispatchArgs& a, const int32_t* base, hipStream_t st) {
   const int64_t per = range_tokens(a.t, a.k), nr = ranges(a.t, a.k);
   const int64_t groups = (per + TPW - 1) / TPW;
@@ -358,15 +401,16 @@ hipError_t dispatch_as(const DispatchArgs& a, const int32_t* base, hipStream_t s
   const int64_t block = (most + split - 1) / split * unit;
   const size_t lds = std::max<size_t>(size_t(TPW) * a.k * 4 + size_t(per) * a.k * 2, base ? 0 : size_t(a.e + 1) * 4);
   const dim3 grid(unsigned(nr * groups + (base ? 0 : 1)), unsigned((a.h + block - 1) / block));
-  hipLaunchKernelGGL((k_dispatch<QUANT, DT, TPW>), grid, dim3(kThreads), lds, st, a, per, base, block);
+  hipLaunchKernelGGL((k_dispatch<QUANT, DT, TPW, NT>), grid, dim3(kThreads), lds, st, a, per, base, block);
   return hipGetLastError();
 }
 
 template <bool QUANT, int DT>
 hipError_t dispatch_rows(const DispatchArgs& a, const int32_t* base, hipStream_t st) {
   // narrow rows: a wave per token
-  return a.h * Elem<DT>::SIZE <= 2048 && a.k <= 64 ? dispatch_as<QUANT, DT, 4>(a, base, st)
-                                                   : dispatch_as<QUANT, DT, 1>(a, base, st);
+  if (a.h * Elem<DT>::SIZE <= 1024 && a.k <= 64) return dispatch_as<QUANT, DT, 4, false>(a, base, st);
+  if (!QUANT && a.t * a.k * a.h * Elem<DT>::SIZE > kCacheBytes) return dispatch_as<QUANT, DT, 1, !QUANT>(a, base, st);
+  return dispatch_as<QUANT, DT, 1, false>(a, base, st);
 }
 
 }  // namespace
@@ -383,7 +427,8 @@ hipError_t launch_dispatch(const DispatchArgs& a, void* work, hipStream_t st) {
     const size_t lds = size_t(a.e + 1) * 4;
     hipLaunchKernelGGL(k_order_count, dim3(unsigned(nr)), dim3(kThreads), lds, st, a.ids, a.t, a.k, a.first, a.e, per,
                        base);
-    hipLaunchKernelGGL(k_order_plan, dim3(1), dim3(1024), lds, st, base, int(nr), a.e, a.offsets);
+    const int parts = int(std::max<int64_t>(1, std::min<int64_t>((nr + 7) / 8, 1024 / (a.e + 1))));
+    hipLaunchKernelGGL(k_order_plan, dim3(1), dim3(1024), lds * (parts + 1), st, base, int(nr), a.e, parts, a.offsets);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -400,31 +445,40 @@ hipError_t launch_tokens_combine(const void* y, const int32_t* inv, const float*
   const dim3 grid(unsigned((t * chunks + kThreads / 64 - 1) / (kThreads / 64)));
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, y, inv, w, add, t, k, h, uint32_t(chunks), out);
+    return hipGetLastError();
   };
-  if (dtype == 0) go(k_tokens_combine<0>);
-  else if (dtype == 1) go(k_tokens_combine<1>);
-  else go(k_tokens_combine<2>);
-  return hipGetLastError();
+  const bool nt = t * k * h * (dtype == 0 ? 4 : 2) > kCacheBytes;
+  auto by_rows = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (nt) return k <= 2 ? go(k_tokens_combine<DT, 2, true>) : k <= 4 ? go(k_tokens_combine<DT, 4, true>)
+                                                                       : go(k_tokens_combine<DT, 8, true>);
+    return k <= 2 ? go(k_tokens_combine<DT, 2, false>) : k <= 4 ? go(k_tokens_combine<DT, 4, false>)
+                                                                : go(k_tokens_combine<DT, 8, false>);
+  };
+  return dtype == 0 ? by_rows(std::integral_constant<int, 0>{}) : dtype == 1 ? by_rows(std::integral_constant<int, 1>{})
+                                                                             : by_rows(std::integral_constant<int, 2>{});
 }
 
-template <int TPS>
+template <int TPS, bool NT>
 static hipError_t combine_bwd_as(const void* dout, const void* y, const int32_t* inv, const float* w, int64_t slots,
                                  int32_t k, int64_t h, int dtype, void* dy, float* dw, hipStream_t st) {
   const dim3 grid(unsigned(TPS == 64 ? (slots + 3) / 4 : slots));
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, dout, y, inv, w, slots, k, h, dy, dw);
   };
-  if (dtype == 0) go(k_tokens_combine_bwd<0, TPS>);
-  else if (dtype == 1) go(k_tokens_combine_bwd<1, TPS>);
-  else go(k_tokens_combine_bwd<2, TPS>);
+  if (dtype == 0) go(k_tokens_combine_bwd<0, TPS, NT>);
+  else if (dtype == 1) go(k_tokens_combine_bwd<1, TPS, NT>);
+  else go(k_tokens_combine_bwd<2, TPS, NT>);
   return hipGetLastError();
 }
 
 hipError_t launch_tokens_combine_bwd(const void* dout, const void* y, const int32_t* inv, const float* w, int64_t t,
                                      int32_t k, int64_t h, int dtype, void* dy, float* dw, hipStream_t st) {
   const int64_t slots = t * k;
-  return slots < 2048 ? combine_bwd_as<kThreads>(dout, y, inv, w, slots, k, h, dtype, dy, dw, st)
-                      : combine_bwd_as<64>(dout, y, inv, w, slots, k, h, dtype, dy, dw, st);
+  if (slots < 2048) return combine_bwd_as<kThreads, false>(dout, y, inv, w, slots, k, h, dtype, dy, dw, st);
+  return slots * h * (dtype == 0 ? 4 : 2) > kCacheBytes
+             ? combine_bwd_as<64, true>(dout, y, inv, w, slots, k, h, dtype, dy, dw, st)
+             : combine_bwd_as<64, false>(dout, y, inv, w, slots, k, h, dtype, dy, dw, st);
 }
 
 }  // namespace q4
