@@ -10,46 +10,65 @@ enum Fp8Mode { FP8_Y = 0, FP8_DX = 1, FP8_DW = 2 };
 // A launch holds fewer workgroups than this (of up to 512 threads: below 2^32 in all).
 constexpr int64_t kMostItems = int64_t(1) << 23;
 
-// Square tiles of `bm`, K in `ks` slices of whole 128-element steps: the estimate of plan_us with
-// these products' step times.
-inline double fp8_plan_us(int64_t m, int64_t n, int64_t steps, int batches, int bm, int64_t ks) {
+// Estimated time (us) of `batches` products with square tiles of `bm` and K in `ks` slices of whole
+// 128-element steps: the form of plan_us, its constants (per mode and tile: a step of a workgroup
+// alone on its CU and of a full CU per workgroup, a workgroup's start and end) fitted to 210
+// products (17 to 4096 rows, widths 512 to 16384), whose tiles and slices were all timed: the
+// plan's choice is the fastest or within 10 % of it (205 of them within 5 %).  Weights from memory
+// take at least their bytes at 5.8 TB/s.
+inline double fp8_plan_us(Fp8Mode mode, int64_t m, int64_t n, int64_t steps, int64_t batches, int bm, int64_t ks,
+                          bool uneven = false) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
-  static const int held[3] = {3, 2, 1};
-  static const double alone[3] = {0.40, 0.80, 1.40}, full[3] = {0.25, 0.45, 1.40}, ends[3] = {2.0, 4.0, 8.0};
+  static const int held[3] = {3, 2, 1};   // workgroups a CU holds
+  static const double alone[3][3] = {{0.34, 0.75, 1.45}, {0.48, 0.89, 1.43}, {0.46, 0.84, 0.83}};
+  static const double full[3][3] = {{0.24, 0.53, 0.19}, {0.35, 0.58, 0.16}, {0.31, 0.63, 2.04}};
+  static const double ends[3][3] = {{4.3, 5.8, 8.5}, {0.7, 3.5, 6.2}, {3.3, 6.7, 17.9}};
+  static const double join[3][3] = {{1.5, 0.36, 3.9e6}, {2.9, 0.45, 2.9e6}, {3.5, 0.14, 4.3e6}};
   const int64_t per = ceil_div(steps, ks);
-  const int64_t wgs = ceil_div(m, bm) * ceil_div(n, bm) * batches * ceil_div(steps, per);
+  // (`uneven`: m rows on average, whose tiles end with half a tile)
+  const int64_t row_tiles = uneven && m > bm ? (batches * (2 * m + bm) + 2 * bm - 1) / (2 * bm) : ceil_div(m, bm) * batches;
+  const int64_t wgs = row_tiles * ceil_div(n, bm) * ceil_div(steps, per);
   if (wgs >= kMostItems || (ks > 1 && m * ceil_div(n, 4) >= int64_t(1) << 32)) return 1e300;
   const int64_t rounds = ceil_div(wgs, 256 * held[t]);
   const int64_t last = std::min<int64_t>(held[t], ceil_div(wgs - (rounds - 1) * 256 * held[t], 256));
-  const auto slice = [&](int64_t on_cu) { return ends[t] + per * std::max(alone[t], full[t] * on_cu); };
+  const auto slice = [&](int64_t on_cu) {
+    return ends[mode][t] + per * std::max(alone[mode][t], full[mode][t] * on_cu);
+  };
   double us = (rounds - 1) * slice(held[t]) + slice(last);
-  if (ks > 1) us += 2.9 + 0.5 * ks + double(ks) * m * n * 4 / 4.5e6;
-  return us;
+  if (ks > 1) us += join[mode][0] + join[mode][1] * ks + double(ks) * m * n * 4 / join[mode][2];
+  return mode == FP8_DW ? us : std::max(us, double(batches) * n * steps * 128 / 5.8e6);
 }
 
-inline Plan fp8_tiles(int64_t m, int64_t n, int64_t steps, int batches, bool split) {
+// The few-rows kernel of y, m rows by each of `batches` matrices (fitted to 25 products of 17 to 128
+// rows): a wave's chain of K steps, or the weights and the rows that each 16 columns read again.
+inline double fp8_rows_us(int64_t m, int64_t k, int64_t n, int64_t batches) {
+  return 3.2 + std::max(ceil_div(k, 1024) * (0.6 + 0.025 * m), double(batches) * n * k / 1e6 * (0.15 + 0.0068 * m));
+}
+
+inline Plan fp8_tiles(Fp8Mode mode, int64_t m, int64_t n, int64_t steps, int64_t batches, bool split, double* us,
+                      bool uneven = false) {
   Plan best{64, 1};
-  double us = 1e301;
+  *us = 1e301;
   for (const int bm : {64, 128, 256})
     for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (ks > 1 && (!split || steps / ks < 2)) break;
-      const double u = fp8_plan_us(m, n, steps, batches, bm, ks);
-      if (u < us) us = u, best = Plan{bm, int(ceil_div(steps, ceil_div(steps, ks)))};
+      const double u = fp8_plan_us(mode, m, n, steps, batches, bm, ks, uneven);
+      if (u < *us) *us = u, best = Plan{bm, int(ceil_div(steps, ceil_div(steps, ks)))};
     }
   return best;
 }
 
-// The product over t rows in all, e matrices of them with `grouped`.
+// The product over t rows in all, e matrices of them with `grouped`; by expert the rows are known
+// by their number alone (the offsets are on the device).
 inline Plan fp8_plan(Fp8Mode mode, int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
-  if (mode == FP8_DW) return fp8_tiles(n, k, std::max<int64_t>(1, ceil_div(ceil_div(t, e), 128)), e, !grouped);
+  double us;
+  const int64_t rows = grouped ? std::max<int64_t>(1, ceil_div(t, e)) : t;
+  if (mode == FP8_DW) return fp8_tiles(mode, n, k, std::max<int64_t>(1, ceil_div(rows, 128)), e, !grouped, &us);
   const int64_t cols = mode == FP8_Y ? n : k, depth = mode == FP8_Y ? k : n;
-  if (!grouped) {
-    if (mode == FP8_Y && t <= 16) return Plan{0, 1};
-    return fp8_tiles(t, cols, ceil_div(depth, 128), 1, true);
-  }
-  const int64_t rows = ceil_div(t, e);
-  if (mode == FP8_Y && rows <= 32 && e * ceil_div(n, 16) < kMostItems) return Plan{0, 1};
-  return Plan{rows <= 64 ? 64 : rows <= 256 ? 128 : 256, 1};
+  const int64_t hit = grouped ? std::min<int64_t>(e, t) : 1;   // matrices with a row, at most
+  const Plan p = fp8_tiles(mode, rows, cols, ceil_div(depth, 128), std::max<int64_t>(1, hit), !grouped, &us, grouped);
+  const bool few = mode == FP8_Y && rows <= 128 && e * ceil_div(n, 16) < kMostItems;
+  return few && fp8_rows_us(rows, k, n, hit) < us ? Plan{0, 1} : p;
 }
 
 // Whether the product's launches stay below kMostItems (products by expert walk their tiles with
