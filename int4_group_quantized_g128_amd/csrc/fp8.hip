@@ -27,6 +27,10 @@ namespace q4 {
 
 namespace {
 
+// (lambdas called from several places: their captured state, the kernel's arguments among it, has
+// to stay in registers)
+#define Q4_INLINE __attribute__((always_inline))
+
 constexpr uint32_t kNoByte = 0x80000000u;   // a byte offset past every descriptor's range
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
@@ -47,6 +51,14 @@ Q4_DEVICE float load_uniform(const float* p, int64_t i) {
   typedef __attribute__((address_space(4))) const float* sptr;
   return *(sptr)(uintptr_t)(p + i);
 }
+
+// Values that every lane has alike, kept in scalar registers.
+Q4_DEVICE int32_t scalar(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+Q4_DEVICE uint32_t scalar(uint32_t v) { return uint32_t(__builtin_amdgcn_readfirstlane(int32_t(v))); }
+Q4_DEVICE uint64_t scalar(uint64_t v) {
+  return uint64_t(scalar(uint32_t(v >> 32))) << 32 | scalar(uint32_t(v));
+}
+Q4_DEVICE int64_t scalar(int64_t v) { return int64_t(scalar(uint64_t(v))); }
 
 // ---------------------------------------------------------------- rows by expert
 // Rows of expert x: [first, first + count), kept inside [0, t) whatever the offsets hold.
@@ -69,7 +81,7 @@ template <int NT, int BM>
 struct ExpertTiles {
   int beg, end, before, own;   // this thread's experts, tiles before them, tiles of them
   int total;
-  __device__ void count(const int32_t* offsets, int e, int64_t t, int32_t* tot /* LDS [NT / 64] */) {
+  Q4_DEVICE void count(const int32_t* offsets, int e, int64_t t, int32_t* tot /* LDS [NT / 64] */) {
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int per = (e + NT - 1) / NT;
     beg = min(e, tid * per), end = min(e, beg + per);
@@ -96,7 +108,7 @@ struct ExpertTiles {
     __syncthreads();
   }
   // Tile `at` (below total) into *out (LDS); all threads call.
-  __device__ void find(const int32_t* offsets, int64_t t, int at, Span* out) const {
+  Q4_DEVICE void find(const int32_t* offsets, int64_t t, int at, Span* out) const {
     if (at >= before && at < before + own) {
       int n = before;
       for (int x = beg; x < end; ++x) {
@@ -448,16 +460,17 @@ struct Tiles {
   uint32_t mtiles, ntiles, plane, start, mine;
   Span* span;
 
-  __device__ Tiles(const Fp8Args& g, uint32_t mt, uint32_t nt, Span* sp, int32_t* tot) : ntiles(nt), span(sp) {
+  Q4_DEVICE Tiles(const Fp8Args& g, uint32_t mt, uint32_t nt, Span* sp, int32_t* tot) : ntiles(nt), span(sp) {
     if (g.offsets) experts.count(g.offsets, g.e, MODE == FP8_DW ? g.K : g.M, tot);
     mtiles = MODE != FP8_DW && g.offsets ? uint32_t(experts.total) : mt;
     plane = mtiles * ntiles;
     const uint32_t total = plane * (MODE == FP8_DW ? uint32_t(g.e) : 1u) * uint32_t(g.ksplit);
     const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
-    mine = share + (xcd < rest ? 1 : 0), start = xcd * share + (xcd < rest ? xcd : rest);
+    mine = scalar(share + (xcd < rest ? 1u : 0u)), start = scalar(xcd * share + (xcd < rest ? xcd : rest));
+    plane = scalar(plane), mtiles = scalar(mtiles);
   }
   // All threads call; item: 0 .. mine - 1 of this XCD.
-  __device__ Work at(const Fp8Args& g, uint32_t item) const {
+  Q4_DEVICE Work at(const Fp8Args& g, uint32_t item) const {
     uint32_t i = start + item;
     const uint32_t z = i / plane;   // expert (dw) or K slice
     i -= z * plane;
@@ -468,9 +481,9 @@ struct Tiles {
     Work w{int64_t(mt) * BM, g.M, int64_t(nt) * BN, 0, g.K, 0, 0, 0, 0, 0};
     if (MODE != FP8_DW && g.offsets) {
       experts.find(g.offsets, g.M, int(mt), span);
-      w.x = __builtin_amdgcn_readfirstlane(span->e);
-      w.m0 = __builtin_amdgcn_readfirstlane(int(span->row));
-      w.m_end = w.m0 + __builtin_amdgcn_readfirstlane(span->rows);
+      w.x = span->e;
+      w.m0 = span->row;
+      w.m_end = w.m0 + span->rows;
     } else if (MODE == FP8_DW && g.offsets) {
       w.x = int(z);
       expert_rows(g.offsets, w.x, g.K, w.k_first, w.k_rows);
@@ -485,11 +498,14 @@ struct Tiles {
         span->tile = n;
       }
       __syncthreads();
-      w.group0 = __builtin_amdgcn_readfirstlane(span->tile);
+      w.group0 = span->tile;
     }
     const int all = int((w.k_rows + 127) / 128), per = (all + g.ksplit - 1) / g.ksplit;
     w.slice = g.ksplit > 1 ? int(z) : 0;
     w.s_begin = min(all, w.slice * per), w.s_end = min(all, w.s_begin + per);
+    w.m0 = scalar(w.m0), w.m_end = scalar(w.m_end), w.n0 = scalar(w.n0), w.k_first = scalar(w.k_first);
+    w.k_rows = scalar(w.k_rows), w.group0 = scalar(w.group0), w.x = scalar(w.x), w.slice = scalar(w.slice);
+    w.s_begin = scalar(w.s_begin), w.s_end = scalar(w.s_end);
     return w;
   }
 };
@@ -499,7 +515,7 @@ template <int MODE>
 struct BlockScale {
   const float* s;
   int64_t step;
-  __device__ BlockScale(const Fp8Args& g, const Work& w, int64_t n) {
+  Q4_DEVICE BlockScale(const Fp8Args& g, const Work& w, int64_t n) {
     const int64_t nb = std::min<int64_t>(n, g.N - 1) / 128;
     s = g.sb + w.x * g.sb_stride + (MODE == FP8_Y ? nb * g.sb_ld : nb);
     step = MODE == FP8_Y ? 1 : g.sb_ld;
@@ -511,29 +527,34 @@ struct BlockScale {
 };
 
 // The end of a tile: sums of rows m (lane % 16 of each 16), columns n + 16 b + 4 (lane / 16) .. + 3.
+// A K slice's, as they are:
+template <int MB, int NB>
+Q4_DEVICE void store_slice(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB][NB], int64_t m, int64_t n, int lane) {
+#pragma unroll
+  for (int a = 0; a < MB; ++a) {
+    const int64_t row = m + 16 * a + (lane & 15);
+    if (row >= w.m_end) continue;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int64_t col = n + 16 * b + 4 * (lane >> 4);
+      float* o = g.part + (int64_t(w.slice) * g.M + row) * g.N + col;
+      if (col + 4 <= g.N && (g.N & 3) == 0) {
+        *reinterpret_cast<f32x4_t*>(o) = acc[a][b];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < g.N) o[e] = acc[a][b][e];
+      }
+    }
+  }
+}
+
+// The result, through `turn`, the wave's part of LDS:
 template <int MODE, int MB, int NB>
 Q4_DEVICE void finish(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB][NB], int64_t m, int64_t n, uint32_t turn,
                       int lane) {
   constexpr int COLS = 16 * NB;
-  if (g.ksplit > 1) {
-#pragma unroll
-    for (int a = 0; a < MB; ++a) {
-      const int64_t row = m + 16 * a + (lane & 15);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int64_t col = n + 16 * b + 4 * (lane >> 4);
-        float* o = g.part + (int64_t(w.slice) * g.M + row) * g.N + col;
-        if (row < w.m_end && col + 4 <= g.N && (g.N & 3) == 0) {
-          *reinterpret_cast<f32x4_t*>(o) = acc[a][b];
-        } else if (row < w.m_end) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < g.N) o[e] = acc[a][b][e];
-        }
-      }
-    }
-    return;
-  }
+  if (g.ksplit > 1) return store_slice<MB, NB>(g, w, acc, m, n, lane);
   // through the wave's part of LDS, 32 rows at a time, so that a lane stores 8 columns of one row;
   // 16-byte chunk c of row r lies at c ^ (r % chunks of a row)
   constexpr int CH = COLS / 4, LPR = COLS / 8;
@@ -561,6 +582,52 @@ Q4_DEVICE void finish(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB][
         store_row<8>(c, g.dtype, row * g.ldc + col, o, int(std::min<int64_t>(8, g.N - col)));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// Two values of a row as 16 bits.
+template <bool F16>
+Q4_DEVICE uint32_t pack2(float a, float b) {
+  if constexpr (F16) return bitcast<uint16_t>(_Float16(a)) | uint32_t(bitcast<uint16_t>(_Float16(b))) << 16;
+  else return bitcast<uint16_t>(__bf16(a)) | uint32_t(bitcast<uint16_t>(__bf16(b))) << 16;
+}
+
+// The same for 64 columns without LDS: 4 x 4 transposes over the lanes' quarters and the four
+// blocks (swaps of half waves, then of quarters) leave a lane 16 columns of its row, 32 bytes,
+// four lanes a whole line.
+template <int MODE, int MB, bool F16>
+Q4_DEVICE void finish64(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB][4], int64_t m, int64_t n, int lane) {
+  struct __attribute__((packed, aligned(2))) Out {
+    uint32_t w[4];
+  };
+  const int64_t col = n + 16 * (lane >> 4);
+  const int rows = int(std::min<int64_t>(w.m_end - m, 16 * MB)) - (lane & 15);   // below: 16 a
+  const int cols = int(std::min<int64_t>(g.N - col, 16));
+  uint16_t* c = static_cast<uint16_t*>(g.c) + (MODE == FP8_DW ? w.x * g.M * g.ldc : 0) + (m + (lane & 15)) * g.ldc + col;
+  const int64_t down = 16 * g.ldc;
+#pragma unroll
+  for (int a = 0; a < MB; ++a, c += down) {
+    uint32_t o[8];   // piece p (columns 4 p .. + 3) of the lane's block: o[2 p], o[2 p + 1]
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      uint32_t v[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v[b] = pack2<F16>(acc[a][b][2 * d], acc[a][b][2 * d + 1]);
+      const auto x = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+      const auto p01 = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+      const auto p23 = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+      o[d] = p01[0], o[2 + d] = p01[1], o[4 + d] = p23[0], o[6 + d] = p23[1];
+    }
+    if (16 * a >= rows) continue;
+    if (cols == 16) {
+      *reinterpret_cast<Out*>(c) = Out{{o[0], o[1], o[2], o[3]}};
+      *reinterpret_cast<Out*>(c + 8) = Out{{o[4], o[5], o[6], o[7]}};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (e < cols) c[e] = uint16_t(o[e / 2] >> (16 * (e % 2)));
+    }
   }
 }
 
@@ -672,6 +739,9 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
 //     step s - 1, and A1 of s and B and A0 of s + 1 are in LDS; then the copies of A1 of
 //     s + SLOTS - 1 and of B and A0 of s + SLOTS go into the places that are free;
 //   the last block ends with the reads of B and of A0's first block of step s + 1.
+// A workgroup's next tile is on its way while the results of one are stored.  (Everything that has
+// one value per workgroup is kept in scalar registers and every helper inlined: as soon as the
+// arguments went through memory the loops spilled, dw of 4096 x 7168 x 4096 141 -> 233 us.)
 template <int MODE, int BM, int BN, int WM, int WN, int SLOTS>
 __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
@@ -685,8 +755,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
   constexpr int A0 = SLOTS * PB::BYTES, A1 = A0 + SLOTS * PA::BYTES, S0 = A1 + SLOTS * PA::BYTES;
   constexpr int S1 = S0 + SLOTS * HR * 4, SB = S1 + SLOTS * HR * 4, BYTES = SB + (VECB ? SLOTS * BN * 4 : 0);
   static_assert(HR % 64 == 0 && CA >= 1 && CB >= 1 && MB >= 4, "");
-  static_assert(COLS <= 64, "a wave's columns lie in one block of W");
-  static_assert(S0 >= NW * 32 * COLS * 4, "the turn at a tile's end");
+  static_assert(COLS == 64, "a wave's columns lie in one block of W, and finish64");
   __shared__ __align__(16) uint8_t mem[BYTES];
   __shared__ Span span;
   __shared__ int32_t tot[NW];
@@ -695,22 +764,31 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
   const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int wm = wid / WN, wn = wid % WN;   // (a SIMD's two waves in different rows)
   const uint32_t lds0 = lds_addr(mem);
-  const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
   const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
-  for (uint32_t item = blockIdx.x / 8; item < tiles.mine; item += (gridDim.x + 7) / 8) {
-    const Work w = tiles.at(g, item);
+  uint32_t item = blockIdx.x / 8;
+  if (item >= tiles.mine) return;
+  Work w = tiles.at(g, item);
+  const uint32_t lda = uint32_t(g.lda), ldb = uint32_t(g.ldb);
+  // what a tile's copies need
+  int steps;
+  int32_t k_all, a_left, b_left;
+  uint32_t oa[2], oa1[2], ob[2], s_rows;   // (by swizzle; MC: oa1 of half 1)
+  int chunk[2];   // KC: the chunk's first code in the step
+  uint64_t a_at, b_at, sa_at, sb_at;
+  auto aim = [&]() Q4_INLINE {
+    // (nothing that follows from the lane alone is worth a register through the tiles' loop)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     const uint8_t* ap = g.a + (MODE == FP8_DW ? w.k_first * g.lda : 0);
     const uint8_t* bp = g.b + (MODE == FP8_DW ? w.k_first * g.ldb : w.x * g.b_stride);
     // Row r of half h is row (r / HW) 2 HW + h HW + r % HW of the tile; the rows (MC: the lane's
     // columns) of a copy lie in one wave's part.
-    const int steps = w.s_end - w.s_begin;
-    const int32_t k_all = int32_t(w.k_rows - int64_t(w.s_begin) * 128);   // (below 2^31: t, n and k are)
-    const int32_t a_left = int32_t(std::min<int64_t>(AMC ? g.M - w.m0 : w.m_end - w.m0, BM));
-    const int32_t b_left = int32_t(std::min<int64_t>(g.N - w.n0, BN));
-    const uint32_t lda = uint32_t(g.lda), ldb = uint32_t(g.ldb);
+    steps = scalar(w.s_end - w.s_begin);
+    k_all = scalar(int32_t(w.k_rows - int64_t(w.s_begin) * 128));   // (below 2^31: t, n and k are)
+    a_left = scalar(int32_t(std::min<int64_t>(AMC ? g.M - w.m0 : w.m_end - w.m0, BM)));
+    b_left = scalar(int32_t(std::min<int64_t>(g.N - w.n0, BN)));
+    s_rows = uint32_t(scalar(int32_t(std::min<int64_t>(w.m_end - w.m0, BM)))) * 4;
     // byte offsets of a lane's chunk from the panel's start at the step (KC: without the first row)
-    uint32_t oa[2], oa1[2], ob[2];   // (by swizzle; MC: oa1 of half 1)
-    int chunk[2];   // KC: the chunk's first code in the step
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const int ia = wid * CA + (CA > 1 ? PA::copy_of(v) : 0), ra0 = (ia * 64 + lane) / PA::CPR;
@@ -729,24 +807,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       if (BMC) ob[v] = cb * 16 < b_left ? uint32_t(rb0 - PB::copy_of(v) * PB::ROWS) * ldb + cb * 16 : kNoByte;
       else ob[v] = uint32_t(lane / PB::CPR) * ldb + cb * 16, chunk[v] = cb * 16;   // (as in A's copies)
     }
-    uint64_t a_at = reinterpret_cast<uint64_t>(ap) + (AMC ? w.m0 : w.m0 * g.lda) + w.s_begin * (AMC ? g.lda * 128 : 128);
-    uint64_t b_at = reinterpret_cast<uint64_t>(bp) + (BMC ? w.n0 : w.n0 * g.ldb) + w.s_begin * (BMC ? g.ldb * 128 : 128);
-    uint64_t sa_at = reinterpret_cast<uint64_t>(g.sa + (w.group0 + w.s_begin) * g.sa_ld + w.m0);
-    uint64_t sb_at = reinterpret_cast<uint64_t>(g.sb + (VECB ? (w.group0 + w.s_begin) * g.sb_ld + w.n0 : 0));
-    const BlockScale<MODE> block(g, w, w.n0 + wn * COLS);
+    a_at = scalar(uint64_t(reinterpret_cast<uint64_t>(ap) + (AMC ? w.m0 : w.m0 * g.lda) + w.s_begin * (AMC ? g.lda * 128 : 128)));
+    b_at = scalar(uint64_t(reinterpret_cast<uint64_t>(bp) + (BMC ? w.n0 : w.n0 * g.ldb) + w.s_begin * (BMC ? g.ldb * 128 : 128)));
+    sa_at = scalar(uint64_t(reinterpret_cast<uint64_t>(g.sa + (w.group0 + w.s_begin) * g.sa_ld + w.m0)));
+    sb_at = scalar(uint64_t(reinterpret_cast<uint64_t>(g.sb + (VECB ? (w.group0 + w.s_begin) * g.sb_ld + w.n0 : 0))));
+  };
     // The panel of step i: what the descriptor covers ends with the panel's last row (KC: of the
     // tile, MC: of the step), so that rows beyond read as zeros; past the last step it is empty.
     auto rsrc = [](uint64_t at, uint32_t bytes) {
-      return u32x4_t{uint32_t(at), uint32_t(at >> 32) & 0xffffu, bytes, 0x00020000u};
+      return u32x4_t{uint32_t(scalar(int32_t(uint32_t(at)))), uint32_t(scalar(int32_t(at >> 32))) & 0xffffu,
+                     uint32_t(scalar(int32_t(bytes))), 0x00020000u};
     };
-    auto range = [&](bool mc, int i, uint32_t rows, uint32_t ld) -> uint32_t {
+    auto range = [&](bool mc, int i, uint32_t rows, uint32_t ld) Q4_INLINE -> uint32_t {
       if (i < 0 || i >= steps) return 0;
       return mc ? uint32_t(min(128, k_all - i * 128)) * ld : rows * ld - uint32_t(w.s_begin + i) * 128;
     };
     // KC: chunks past K's end take no byte
-    auto inside = [&](int i, uint32_t o, int odd) { return chunk[odd] < k_all - i * 128 ? o : kNoByte; };
+    auto inside = [&](int i, uint32_t o, int odd) Q4_INLINE { return chunk[odd] < k_all - i * 128 ? o : kNoByte; };
     // Copy j of step i (0: s_begin) of half h of A, of B, into a slot.
-    auto copy_a = [&](int i, int slot, int h, int j) {
+    auto copy_a = [&](int i, int slot, int h, int j) Q4_INLINE {
       uint32_t o;
       if constexpr (AMC) {
         o = (h ? oa1 : oa)[PA::odd(j)] + j * PA::ROWS * lda;   // (kNoByte stays beyond every range)
@@ -757,7 +836,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       const uint64_t at = a_at + int64_t(i) * (AMC ? g.lda * 128 : 128);
       copy_to_lds(rsrc(at, range(AMC, i, a_left, lda)), lds0 + (h ? A1 : A0) + slot * PA::BYTES + (wid * CA + j) * 1024, o);
     };
-    auto copy_b = [&](int i, int slot, int j) {
+    auto copy_b = [&](int i, int slot, int j) Q4_INLINE {
       uint32_t o = ob[PB::odd(j)];
       if constexpr (BMC) o += j * PB::ROWS * ldb;
       else o = inside(i, o, PB::odd(j)) + uint32_t((wid * CB + j) * PB::ROWS) * ldb;
@@ -768,20 +847,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     // panels), of B.  (Waves beyond their number repeat a copy.)
     const int sh = wid & 1, sc = (wid >> 1) % (HR / 64);
     const uint32_t s_off = uint32_t(sc * 64 + lane + (sc * 64 + lane) / HW * HW + sh * HW) * 4;
-    const uint32_t s_rows = uint32_t(std::min<int64_t>(w.m_end - w.m0, BM)) * 4;
-    auto copy_sa = [&](int i, int slot, int before) {   // half 0 of step i or half 1 of step i - 1
+    auto copy_sa = [&](int i, int slot, int before) Q4_INLINE {   // half 0 of step i or half 1 of step i - 1
       const int k = i - sh;
       copy4_to_lds(rsrc(sa_at + int64_t(k) * g.sa_ld * 4, k >= 0 && k < steps ? s_rows : 0),
                    lds0 + (sh ? S1 : S0) + (sh ? before : slot) * (HR * 4) + sc * 256, s_off);
     };
-    auto copy_sb = [&](int i, int slot) {
+    auto copy_sb = [&](int i, int slot) Q4_INLINE {
       const int c = wid % (BN / 64);
       copy4_to_lds(rsrc(sb_at + int64_t(i) * g.sb_ld * 4, i < steps ? b_left * 4 : 0),
                    lds0 + SB + slot * (BN * 4) + c * 256, (c * 64 + lane) * 4);
     };
     // Copy `t` of those that step i, which lies in slot `sl`, begins: A1 of i + SLOTS - 1, B and A0 of
     // i + SLOTS.
-    auto copy_next = [&](int i, int sl, int t) {
+    auto copy_next = [&](int i, int sl, int t) Q4_INLINE {
       const int before = sl == 0 ? SLOTS - 1 : sl - 1;
       if (t < CA) copy_a(i + SLOTS - 1, before, 1, t);
       else if (t < CA + CB) copy_b(i + SLOTS, sl, t - CA);
@@ -794,9 +872,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     typedef __attribute__((address_space(3))) const f32x4_t* vptr;
     typename PA::Reader ra;
     typename PB::Reader rb;
-    ra.start(lds0 + A0, lane, wm * HW);
-    rb.start(lds0, lane, wn * COLS);
-    uint32_t rsa = lds0 + S0 + (wm * HW + (lane & 15)) * 4, rsb = lds0 + SB + (wn * COLS + 4 * (lane >> 4)) * 4;
+    uint32_t rsa, rsb;
     auto read_a = [&](int a) { return ra.read(a / (MB / 2) * (A1 - A0), 16 * (a % (MB / 2))); };
     auto read_sa = [&](int a) {
       return *((fptr)(uintptr_t)rsa + (a / (MB / 2) * (S1 - S0) + 64 * (a % (MB / 2))) / 4);
@@ -811,36 +887,43 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     };
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
+  constexpr int NEXT = 2 * CA + CB + (VECB ? 2 : 1);   // copies (of a wave) in a step
+  auto begin = [&]() Q4_INLINE {
+    aim();
+#pragma unroll
+    for (int i = -SLOTS; i < 0; ++i)
+#pragma unroll
+      for (int t = 0; t < NEXT; ++t) copy_next(i, i + SLOTS, t);
+  };
+  begin();
+  for (;;) {
+    const BlockScale<MODE> block(g, w, w.n0 + wn * COLS);
+    ra.start(lds0 + A0, lane, wm * HW);
+    rb.start(lds0, lane, wn * COLS);
+    rsa = lds0 + S0 + (wm * HW + (lane & 15)) * 4, rsb = lds0 + SB + (wn * COLS + 4 * (lane >> 4)) * 4;
     f32x4_t acc[MB][NB];
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
-    constexpr int NEXT = 2 * CA + CB + (VECB ? 2 : 1);   // copies (of a wave) in a step
-#pragma unroll
-    for (int i = -SLOTS; i < 0; ++i)
-#pragma unroll
-      for (int t = 0; t < NEXT; ++t) copy_next(i, i + SLOTS, t);
     float sb_next = steps > 0 ? block.at(w.s_begin) : 0.f;
-    wait_barrier8<(SLOTS - 1) * NEXT>();
-    if (w.m0 + wm * (BM / WM) >= w.m_end) {   // no row of the wave's: it copies for the others
+    wait_barrier8<0>();   // (the last tile's stores are counted with the copies)
+    const bool rows = w.m0 + wm * (BM / WM) < w.m_end;
+    if (!rows) {   // no row of the wave's: it copies for the others
       for (int i = 0, sl = 0; i < steps; ++i, sl = sl == SLOTS - 1 ? 0 : sl + 1) {
         wait_barrier8<(SLOTS - 2) * NEXT>();
 #pragma unroll
         for (int t = 0; t < NEXT; ++t) copy_next(i, sl, t);
       }
-      wait_barrier8<0>();
-      __syncthreads();
-      continue;
-    }
+    } else {
     Frag fa[2], fb[NB];
     float sa[2], scale = 0.f, last = 0.f;   // of the block whose results are scaled, of the one before
-    f32x4_t p[2][NB], vb[VECB ? NB : 1], vl[VECB ? NB : 1];
+    f32x4_t p[2][NB], vb[VECB ? NB : 1];   // vb: the columns' scales for the results scaled next
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       fb[b] = read_b(b);
       p[1][b] = f32x4_t{0, 0, 0, 0};
-      if constexpr (VECB) vb[b] = vl[b] = read_sb(b);
+      if constexpr (VECB) vb[b] = f32x4_t{0, 0, 0, 0};
     }
     fa[0] = read_a(0), sa[0] = read_sa(0);
     int sl = 0;
@@ -866,8 +949,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
           f32x4_t v = p[1 - cur][b];
           if constexpr (VECB) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= a == 0 ? vl[b][e] : vb[b][e];
-            if (a == MB - 1) vl[b] = vb[b], vb[b] = read_sb(b);
+            for (int e = 0; e < 4; ++e) v[e] *= vb[b][e];
+            if (a == 0) vb[b] = read_sb(b);   // (until here the last step's)
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[to][b][e] = __builtin_fmaf(v[e], last, acc[to][b][e]);
@@ -883,10 +966,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        acc[MB - 1][b][e] = __builtin_fmaf(p[1][b][e] * (VECB ? vl[b][e] : 1.f), scale, acc[MB - 1][b][e]);
+        acc[MB - 1][b][e] = __builtin_fmaf(p[1][b][e] * (VECB ? vb[b][e] : 1.f), scale, acc[MB - 1][b][e]);
+    }
     wait_barrier8<0>();   // every wave's copies and reads are done: LDS is free
-    finish<MODE, MB, NB>(g, w, acc, w.m0 + wm * (BM / WM), w.n0 + wn * COLS, lds0 + wid * (32 * COLS * 4), lane);
-    __syncthreads();   // LDS is read to its end: the next tile's copies may land
+    const Work done = w;
+    item = scalar(item + (gridDim.x + 7) / 8);
+    const bool more = item < tiles.mine;
+    if (more) {
+      w = tiles.at(g, item);
+      begin();
+    }
+    if (rows) {
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));
+      const int64_t m = done.m0 + wm * (BM / WM), n = done.n0 + wn * COLS;
+      if (g.ksplit > 1) store_slice<MB, NB>(g, done, acc, m, n, lane);
+      else if (g.dtype == 1) finish64<MODE, MB, true>(g, done, acc, m, n, lane);
+      else finish64<MODE, MB, false>(g, done, acc, m, n, lane);
+    }
+    if (!more) return;
   }
 }
 
@@ -1028,8 +1126,9 @@ hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
   if (MODE != FP8_DW && g.offsets)   // as many tiles as the offsets can make
     items = (g.M / p.tile + std::min<int64_t>(g.e, g.M)) * nt;
   else items = int64_t(mt) * nt * (MODE == FP8_DW ? g.e : 1) * p.ksplit;
+  // (the large tiles' workgroups, as many as the card holds, walk their tiles; so do all by expert)
   unsigned grid = unsigned(items);
-  if (MODE != FP8_DW && g.offsets) {
+  if (p.tile != 64 || (MODE != FP8_DW && g.offsets)) {
     const int64_t room = 256 * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 3);
     grid = unsigned(std::min<int64_t>(room, ceil_div(items, 8) * 8));
   }

@@ -14,16 +14,17 @@ constexpr int64_t kMostItems = int64_t(1) << 23;
 // 128-element steps: the form of plan_us, its constants (per mode and tile: a step of a workgroup
 // alone on its CU and of a full CU per workgroup, a workgroup's start and end) fitted to 210
 // products (17 to 4096 rows, widths 512 to 16384), whose tiles and slices were all timed: the
-// plan's choice is the fastest or within 10 % of it (205 of them within 5 %).  Weights from memory
+// plan's choice is the fastest or within 8 % of it for 204 of them (the worst 17 %, dx of 64 rows,
+// 2048 / 512).  Weights from memory
 // take at least their bytes at 5.8 TB/s.
 inline double fp8_plan_us(Fp8Mode mode, int64_t m, int64_t n, int64_t steps, int64_t batches, int bm, int64_t ks,
                           bool uneven = false) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;
   static const int held[3] = {3, 2, 1};   // workgroups a CU holds
-  static const double alone[3][3] = {{0.34, 0.75, 1.45}, {0.48, 0.89, 1.43}, {0.46, 0.84, 0.83}};
-  static const double full[3][3] = {{0.24, 0.53, 0.19}, {0.35, 0.58, 0.16}, {0.31, 0.63, 2.04}};
-  static const double ends[3][3] = {{4.3, 5.8, 8.5}, {0.7, 3.5, 6.2}, {3.3, 6.7, 17.9}};
-  static const double join[3][3] = {{1.5, 0.36, 3.9e6}, {2.9, 0.45, 2.9e6}, {3.5, 0.14, 4.3e6}};
+  static const double alone[3][3] = {{0.39, 0.77, 1.30}, {0.42, 0.78, 0.81}, {0.40, 0.79, 0.84}};
+  static const double full[3][3] = {{0.25, 0.51, 1.05}, {0.31, 0.53, 1.41}, {0.27, 0.62, 1.85}};
+  static const double ends[3][3] = {{2.5, 3.9, 6.2}, {3.3, 4.1, 6.9}, {3.7, 6.0, 10.9}};
+  static const double join[3][3] = {{3.0, 0.45, 3.6e6}, {2.5, 0.39, 3.4e6}, {2.0, 0.18, 3.5e6}};
   const int64_t per = ceil_div(steps, ks);
   // (`uneven`: m rows on average, whose tiles end with half a tile)
   const int64_t row_tiles = uneven && m > bm ? (batches * (2 * m + bm) + 2 * bm - 1) / (2 * bm) : ceil_div(m, bm) * batches;
