@@ -963,7 +963,7 @@ _E4M3 = torch.float8_e4m3fn
 
 def _out(out, dtype, shape, like, dev):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _arg(out, "out", dtype, shape, dev)
     return out
 
@@ -979,7 +979,8 @@ def _offsets(offsets, dev):
     """-> the number of experts (1 without offsets)."""
     if offsets is None:
         return 1
-    _need(offsets, torch.int32, "offsets", 1)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        _need(offsets, torch.int32, "offsets", 1)
     _arg(offsets, "offsets", torch.int32, offsets.shape, dev)
     if offsets.shape[0] < 2:
         raise ValueError("offsets must hold the first row of each expert and the end")
@@ -994,22 +995,18 @@ def moe_dispatch_forward(x, ids, num_experts, first=0, quantize=False, out=None)
     [t k, h] and scales [ceil(h / 128), t k] for fp8_linear_forward."""
     (t, h), dev = _first(x, _FLOATS, "x")
     k = _slots(ids, "ids", t, dev)
-    device, n = x.device, t * k
-    order = torch.empty(num_experts + 1 + (-(num_experts + 1)) % 4 + n + (-n) % 4 + n, dtype=torch.int32, device=device)
-    offsets = order[:num_experts + 1]
-    at = num_experts + 1 + (-(num_experts + 1)) % 4
-    perm = order[at:at + n]
-    inv = order[at + n + (-n) % 4:].view(t, k)
+    n = t * k
+    offsets, perm, inv = ids.new_empty(num_experts + 1), ids.new_empty(n), torch.empty_like(ids)
     s = None
     if quantize:
         if out is not None:
             raise ValueError("out is for rows, not for codes")
-        rows = torch.empty((n, h), dtype=_E4M3, device=device)
-        s = torch.empty((-(-h // 128), n), dtype=torch.float32, device=device)
+        rows = x.new_empty((n, h), dtype=_E4M3)
+        s = x.new_empty((-(-h // 128), n), dtype=torch.float32)
     else:
         rows = _out(out, x.dtype, (n, h), x, dev)
     nbytes = _dispatch_ws(t, k, num_experts)
-    ws = _scratch(nbytes, device)
+    ws = _scratch(nbytes, x.device)
     _call("moe_dispatch_forward", _lib.moe_dispatch_forward, dev, x.data_ptr(), _DT[x.dtype], t, h, ids.data_ptr(), k,
           first, num_experts, None if quantize else rows.data_ptr(), rows.data_ptr() if quantize else None, _dp(s),
           offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), _dp(ws), nbytes)
@@ -1029,7 +1026,7 @@ def _sorted_rows(rows, name, inv):
 def moe_dispatch_backward(dxp, inv):
     """dx [t, h] = sum_j dxp[inv[t, j]]: the gradient of moe_dispatch_forward."""
     t, k, h, dev = _sorted_rows(dxp, "dxp", inv)
-    dx = torch.empty((t, h), dtype=dxp.dtype, device=dxp.device)
+    dx = dxp.new_empty((t, h))
     _call("moe_dispatch_backward", _lib.moe_dispatch_backward, dev, dxp.data_ptr(), _DT[dxp.dtype], t, h,
           inv.data_ptr(), k, dx.data_ptr())
     return dx
@@ -1043,7 +1040,7 @@ def moe_combine_forward(y, inv, weights=None, add=None):
         _arg(weights, "weights", torch.float32, (t, k), dev)
     if add is not None:
         _arg(add, "add", y.dtype, (t, h), dev)
-    out = torch.empty((t, h), dtype=y.dtype, device=y.device)
+    out = y.new_empty((t, h))
     _call("moe_combine_forward", _lib.moe_combine_forward, dev, y.data_ptr(), _DT[y.dtype], t, h, inv.data_ptr(),
           _dp(weights), _dp(add), k, out.data_ptr())
     return out
@@ -1057,7 +1054,7 @@ def moe_combine_backward(dout, y, inv, weights=None, out=None):
     dw = None
     if weights is not None:
         _arg(weights, "weights", torch.float32, (t, k), dev)
-        dw = torch.empty((t, k), dtype=torch.float32, device=y.device)
+        dw = torch.empty_like(weights)
     dy = _out(out, y.dtype, (t * k, h), y, dev)
     _call("moe_combine_backward", _lib.moe_combine_backward, dev, dout.data_ptr(), y.data_ptr(), _DT[y.dtype], t, h,
           inv.data_ptr(), _dp(weights), k, dy.data_ptr(), _dp(dw))
@@ -1076,13 +1073,12 @@ def quantize_fp8_tokens(x, columns=False, gated=False, offsets=None):
         if k % 2:
             raise ValueError("a gated x has an even width")
         k //= 2
-    device = x.device
-    q = torch.empty((t, k), dtype=_E4M3, device=device)
-    s = torch.empty((-(-k // 128), t), dtype=torch.float32, device=device)
+    q = x.new_empty((t, k), dtype=_E4M3)
+    s = x.new_empty((-(-k // 128), t), dtype=torch.float32)
     qc = sc = None
     if columns:
-        qc = torch.empty((t, k), dtype=_E4M3, device=device)
-        sc = torch.empty((_column_groups(t, offsets, e), k), dtype=torch.float32, device=device)
+        qc = torch.empty_like(q)
+        sc = x.new_empty((_column_groups(t, offsets, e), k), dtype=torch.float32)
     _call("quantize_fp8_tokens", _lib.quantize_fp8_tokens, dev, x.data_ptr(), _DT[x.dtype], t, k, int(bool(gated)),
           _dp(offsets), e, q.data_ptr(), s.data_ptr(), _dp(qc), _dp(sc))
     return (q, s, qc, sc) if columns else (q, s)
