@@ -113,6 +113,7 @@ Q4_DEVICE uint32_t e4m3_pack4(float a, float b, float c, float d) {
 // is for quotients that round past 448 and scales below fp32's normal range.)
 Q4_DEVICE float e4m3_clamp(float q) { return __builtin_amdgcn_fmed3f(q, -kE4m3Max, kE4m3Max); }
 Q4_DEVICE u32x2_t e4m3_codes8(const float* v, float s) {
+  if (!(s > 0.f)) return u32x2_t{0, 0};
   float c[8];
   if (s >= kPlainScale) {
     const float r = 1.f / s;
@@ -120,7 +121,7 @@ Q4_DEVICE u32x2_t e4m3_codes8(const float* v, float s) {
     for (int i = 0; i < 8; ++i) c[i] = e4m3_clamp(quotient(v[i], s, r));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = s > 0.f ? e4m3_clamp(v[i] / s) : 0.f;
+    for (int i = 0; i < 8; ++i) c[i] = e4m3_clamp(v[i] / s);
   }
   return u32x2_t{e4m3_pack4(c[0], c[1], c[2], c[3]), e4m3_pack4(c[4], c[5], c[6], c[7])};
 }

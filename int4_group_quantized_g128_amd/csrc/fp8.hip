@@ -128,15 +128,18 @@ struct ExpertTiles {
 };
 
 // ---------------------------------------------------------------- quantisers
-// A workgroup takes 128 rows x 128 columns: thread i columns 8 (i % 16) .. + 7 of rows i / 16 + 16 j.
-enum Form { FORM_ROWS = 1, FORM_COLS = 2, FORM_BLOCK = 4 };
+// A workgroup takes 16 RPT rows x 128 columns: thread i columns 8 (i % 16) .. + 7 of rows i / 16 + 16 j.
+enum Form { FORM_ROWS = 1, FORM_COLS = 2 };
+// RPT of codes along the rows alone: 4096 x 7168 17.0 us (8: 22.5, 4: 19.2, 1: 16.6), 4096 x 16384
+// 50.8 (52.6, 55.1, 58.7), 333 x 1040 4.0 (7.4, 4.5, 4.8); groups of tokens take 8, all 128 rows.
+constexpr int kRowsAlone = 2;
 
-template <int DT, bool GATED>
-Q4_DEVICE void load_tile(const void* x, int64_t ld, int64_t row0, int rows, int64_t c, int64_t k, float v[8][8]) {
+template <int DT, bool GATED, int RPT>
+Q4_DEVICE void load_tile(const void* x, int64_t ld, int64_t row0, int rows, int64_t c, int64_t k, float (&v)[RPT][8]) {
   typedef Elem<DT> E;
-  typename E::Raw g[8][8 / E::VEC], u[GATED ? 8 : 1][8 / E::VEC];
+  typename E::Raw g[RPT][8 / E::VEC], u[GATED ? RPT : 1][8 / E::VEC];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < RPT; ++i) {
     const int r = (threadIdx.x >> 4) + 16 * i;
     if (r < rows && c < k) {
 #pragma unroll
@@ -147,7 +150,7 @@ Q4_DEVICE void load_tile(const void* x, int64_t ld, int64_t row0, int rows, int6
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < RPT; ++i) {
     const int r = (threadIdx.x >> 4) + 16 * i;
     const bool in = r < rows && c < k;
 #pragma unroll
@@ -161,11 +164,12 @@ Q4_DEVICE void load_tile(const void* x, int64_t ld, int64_t row0, int rows, int6
 
 template <int DT, int FORM, bool GATED>
 __global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
+  constexpr int RPT = FORM & FORM_COLS ? 8 : kRowsAlone, TILE = 16 * RPT;
   __shared__ float part[4][128];
   __shared__ Span span;
   __shared__ int32_t tot[4];
   int tile = blockIdx.x;
-  int64_t row0 = int64_t(tile) * 128, left;
+  int64_t row0 = int64_t(tile) * TILE, left;
   if (FORM & FORM_COLS && a.offsets) {
     ExpertTiles<256, 128> tiles;
     tiles.count(a.offsets, a.e, a.t, tot);
@@ -178,20 +182,20 @@ __global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
     left = end - row0;
   }
   if (left <= 0) return;
-  const int rows = int(std::min<int64_t>(left, 128));
+  const int rows = int(std::min<int64_t>(left, TILE));
   const int cb = blockIdx.y, lane16 = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int64_t c = int64_t(cb) * 128 + lane16 * 8;
-  float v[8][8];
-  load_tile<DT, GATED>(a.x, GATED ? 2 * a.k : a.k, row0, rows, c, a.k, v);
+  float v[RPT][8];
+  load_tile<DT, GATED, RPT>(a.x, GATED ? 2 * a.k : a.k, row0, rows, c, a.k, v);
   if constexpr (FORM & FORM_ROWS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
-      const float s = e4m3_scale(row16_max(m));
-      const int r = slot + 16 * i;
+    for (int i = 0; i < RPT; ++i) {
+      const int r = slot + 16 * i;   // (the same for all lanes of a group)
       if (r < rows) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
+        const float s = e4m3_scale(row16_max(m));
         if (c < a.k)
           *reinterpret_cast<u32x2_t*>(a.q_row + (row0 + r) * a.k + c) = e4m3_codes8(v[i], s);
         if (lane16 == 0) a.s_row[cb * a.t + row0 + r] = s;
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(256) k_quantize_fp8_blocks(const void* __restr
   const int rows = int(std::min<int64_t>(128, n - rb * 128));
   const int64_t row0 = x * n + rb * 128, c = int64_t(blockIdx.y) * 128 + (threadIdx.x & 15) * 8;
   float v[8][8];
-  load_tile<DT, false>(w, k, row0, rows, c, k, v);
+  load_tile<DT, false, 8>(w, k, row0, rows, c, k, v);
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -1014,9 +1018,9 @@ __global__ void __launch_bounds__(256) k_fp8_join(Fp8Args g) {
 // Few rows (per expert): bound by reading the weights once.  A workgroup owns 16 columns of y of
 // one expert, its 8 waves take the 128-code K steps in turn and feed the matrix core straight from
 // global memory, then add their sums through LDS in wave order.
-template <int RB>
+template <int RB, int MAXRB, int DEEP>
 Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws, int64_t n0, int64_t row0, int rows,
-                            f32x4_t (*sums)[4][64]) {
+                            f32x4_t (*sums)[MAXRB][64]) {
   constexpr int W = 8;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int l = lane & 15, quarter = (lane >> 4) * 16;
@@ -1060,9 +1064,13 @@ Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws,
         for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(p[e], sc[u][r], acc[r][e]);
       }
   };
-  constexpr int U = RB == 1 ? 4 : RB == 2 ? 2 : 1;
+  constexpr int U = RB == 1 ? DEEP : RB == 2 ? 2 : 1;   // steps in flight
   int s = wave;
   for (; s + (U - 1) * W < full; s += U * W) steps(std::integral_constant<int, U>{}, s);
+  if (U > 2 && s + W < full) {
+    steps(std::integral_constant<int, 2>{}, s);
+    s += 2 * W;
+  }
   for (; s < full; s += W) steps(std::integral_constant<int, 1>{}, s);
   if (s == full && g.K % 128) {   // the K tail: chunks past the row's end hold zeros
     const int64_t at = int64_t(full) * 128;
@@ -1099,8 +1107,9 @@ Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws,
   __syncthreads();
 }
 
+template <int MAXRB, int DEEP>
 __global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols) {
-  __shared__ f32x4_t sums[8][4][64];
+  __shared__ f32x4_t sums[8][MAXRB][64];
   const int x = int(blockIdx.x / ncols);
   const int64_t n0 = int64_t(blockIdx.x - x * ncols) * 16;
   int64_t first = 0, count = g.M;
@@ -1108,12 +1117,25 @@ __global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols) {
   const uint8_t* w = g.b + x * g.b_stride;
   const float* ws = g.sb + x * g.sb_stride;
   while (count > 0) {
-    const int rows = int(count < 64 ? count : 64);
-    if (rows <= 16) rows_product<1>(g, w, ws, n0, first, rows, sums);
-    else if (rows <= 32) rows_product<2>(g, w, ws, n0, first, rows, sums);
-    else rows_product<4>(g, w, ws, n0, first, rows, sums);
+    const int rows = int(count < 16 * MAXRB ? count : 16 * MAXRB);
+    if (MAXRB == 1 || rows <= 16) rows_product<1, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
+    else if (MAXRB == 2 || rows <= 32) rows_product<2, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
+    else rows_product<MAXRB, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
     first += rows, count -= rows;
   }
+}
+
+// Up to 16 rows: one step in flight per wave and as many waves as fit, but four where K is long
+// and the weights are many (one row: 2048 / 16384 7.6 us against 8.9, 7168 / 4096 7.3 / 7.6; 4096 /
+// 14336 16.3 / 13.5, 8192 / 8192 15.0 / 14.0).
+hipError_t launch_rows8(const Fp8Args& g, bool few, hipStream_t st) {
+  const uint32_t ncols = uint32_t(ceil_div(g.N, 16));
+  const dim3 grid(ncols * uint32_t(g.offsets ? g.e : 1));
+  const bool deep = g.K >= 4096 && g.N * g.K * (g.offsets ? g.e : 1) >= int64_t(48) << 20;
+  if (!few) hipLaunchKernelGGL((k_fp8_rows<4, 4>), grid, dim3(512), 0, st, g, ncols);
+  else if (deep) hipLaunchKernelGGL((k_fp8_rows<1, 4>), grid, dim3(512), 0, st, g, ncols);
+  else hipLaunchKernelGGL((k_fp8_rows<1, 1>), grid, dim3(512), 0, st, g, ncols);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- launches
@@ -1147,7 +1169,7 @@ int64_t part_bytes8(const Plan& p, int64_t m, int64_t n) { return p.ksplit > 1 ?
 template <int DT>
 hipError_t quantize_as(const Fp8QuantArgs& a, hipStream_t st) {
   const bool rows = a.q_row, cols = a.q_col;
-  const int64_t tiles = cols && a.offsets ? a.t / 128 + std::min<int64_t>(a.e, a.t) : ceil_div(a.t, 128);
+  const int64_t tiles = cols && a.offsets ? a.t / 128 + std::min<int64_t>(a.e, a.t) : ceil_div(a.t, cols ? 128 : 16 * kRowsAlone);
   const dim3 grid(unsigned(tiles), unsigned(ceil_div(a.k, 128)));
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a); };
   if (a.gated) go(k_quantize_fp8<DT, FORM_ROWS, true>);
@@ -1195,9 +1217,7 @@ hipError_t launch_fp8_linear(const uint8_t* q, const float* s, int64_t t, int64_
   g.part = static_cast<float*>(work);
   const Plan p = fp8_plan(FP8_Y, t, k, n, e, offsets != nullptr);
   if (p.tile) return launch_tiles8<FP8_Y>(g, p, st);
-  const uint32_t ncols = uint32_t(ceil_div(n, 16));
-  hipLaunchKernelGGL(k_fp8_rows, dim3(ncols * uint32_t(offsets ? e : 1)), dim3(512), 0, st, g, ncols);
-  return hipGetLastError();
+  return launch_rows8(g, offsets ? t <= 4 * int64_t(e) : t <= 16, st);
 }
 
 // Workspace of the gradients: codes and scales of dy along its rows and along the tokens, the K
