@@ -735,8 +735,8 @@ Q4_API int block_norm_backward(const q4_block_norm_t* norm, const void* dr, cons
  * Sums are fp32, in ascending j (dw: a fixed order), rounded once.  Values of inv outside
  * [0, t k) count as dropped; rows that are not read may hold anything.  Outputs may not alias
  * inputs except as stated.
- *  Requires 0 <= t < 2^23, 1 <= k <= 4096, t k < 2^26, 1 <= h <= 2^20, 1 <= e <= 4096,
- *  first >= 0.
+ *  Requires 0 <= t < 2^23, 1 <= k <= 4096, t k <= 2^26 - 4, 1 <= h <= 2^20,
+ *  t ceil(h / 256) <= 2^26 - 4, 1 <= e <= 4096, first >= 0, first + e < 2^31.
  */
 Q4_API size_t moe_dispatch_workspace_bytes(int64_t t, int32_t k, int32_t e);
 Q4_API int moe_dispatch_forward(const void* x, int dtype, int64_t t, int64_t h, const int32_t* ids, int32_t k,

@@ -982,8 +982,8 @@ def _offsets(offsets, dev):
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         _need(offsets, torch.int32, "offsets", 1)
     _arg(offsets, "offsets", torch.int32, offsets.shape, dev)
-    if offsets.shape[0] < 2:
-        raise ValueError("offsets must hold the first row of each expert and the end")
+    if not 2 <= offsets.shape[0] <= 4097:
+        raise ValueError("offsets must hold the first row of each of 1 to 4096 experts and the end")
     return offsets.shape[0] - 1
 
 
@@ -995,6 +995,8 @@ def moe_dispatch_forward(x, ids, num_experts, first=0, quantize=False, out=None)
     [t k, h] and scales [ceil(h / 128), t k] for fp8_linear_forward."""
     (t, h), dev = _first(x, _FLOATS, "x")
     k = _slots(ids, "ids", t, dev)
+    if not 1 <= num_experts <= 4096 or not 0 <= first < 2 ** 31 - num_experts:
+        raise ValueError(f"experts [{first}, {first} + {num_experts}) must be 1 to 4096 below 2^31")
     n = t * k
     offsets, perm, inv = ids.new_empty(num_experts + 1), ids.new_empty(n), torch.empty_like(ids)
     s = None

@@ -1300,12 +1300,14 @@ int block_norm_backward(const q4_block_norm_t* p, const void* dr, const void* dn
 }
 
 // ---------------------------------------------------------------- token order
-static constexpr int64_t kMostTokens = int64_t(1) << 23, kMostSlots = int64_t(1) << 26;
+// (a launch has fewer than 2^32 threads: 64 per slot, 64 per 256 columns of a token)
+static constexpr int64_t kMostTokens = int64_t(1) << 23, kMostSlots = (int64_t(1) << 26) - 4;
 
 static int validate_slots(int dtype, int64_t t, int64_t h, int32_t k) {
   Q4_REQUIRE(float_dtype(dtype), Q4_ERR_DTYPE, "dtype %d", dtype);
-  Q4_REQUIRE(t >= 0 && t < kMostTokens && k >= 1 && k <= 4096 && t * k < kMostSlots && h >= 1 && h <= kMaxWidth,
-             Q4_ERR_SHAPE, "need 0 <= t < 2^23, 1 <= k <= 4096, t k < 2^26, 1 <= h <= 2^20");
+  Q4_REQUIRE(t >= 0 && t < kMostTokens && k >= 1 && k <= 4096 && t * k <= kMostSlots && h >= 1 && h <= kMaxWidth &&
+                 t * ceil_div(h, 256) <= kMostSlots, Q4_ERR_SHAPE,
+             "need 0 <= t < 2^23, 1 <= k <= 4096, t k <= 2^26 - 4, 1 <= h <= 2^20, t ceil(h / 256) <= 2^26 - 4");
   return ok();
 }
 
@@ -1319,7 +1321,8 @@ int moe_dispatch_forward(const void* x, int dtype, int64_t t, int64_t h, const i
                          void* workspace, size_t ws_bytes, hipStream_t stream) {
   g_last_error.clear();
   if (int rc = validate_slots(dtype, t, h, k)) return rc;
-  Q4_REQUIRE(e >= 1 && e <= 4096 && first >= 0, Q4_ERR_SHAPE, "need 1 <= e <= 4096, first >= 0");
+  Q4_REQUIRE(e >= 1 && e <= 4096 && first >= 0 && first <= INT32_MAX - e, Q4_ERR_SHAPE,
+             "need 1 <= e <= 4096, first >= 0, first + e < 2^31");
   Q4_REQUIRE((q != nullptr) == (s != nullptr), Q4_ERR_NULL, "q and s go together");
   Q4_REQUIRE(!q || h % 16 == 0, Q4_ERR_SHAPE, "e4m3 codes need h %% 16 == 0");
   Q4_REQUIRE(offsets, Q4_ERR_NULL, "offsets is required");

@@ -67,6 +67,25 @@ def test_combine_validation(L):
     assert b(w=ODD) == L.Q4_ERR_ALIGN and b(dw=ODD) == L.Q4_ERR_ALIGN
 
 
+def test_token_order_limits(L):
+    """Calls whose launches would not fit, and experts that no id can name."""
+    slots = (1 << 26) - 4
+    def d(t, h, k, first=0, e=8):
+        return L.raw.moe_dispatch_forward(FAKE, 2, t, h, FAKE, k, first, e, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, 0,
+                                          None)
+    calls = (d, lambda t, h, k: L.raw.moe_dispatch_backward(None, 2, t, h, None, k, None, None),
+             lambda t, h, k: L.raw.moe_combine_forward(None, 0, t, h, None, None, None, k, None, None),
+             lambda t, h, k: L.raw.moe_combine_backward(None, None, 1, t, h, None, None, k, None, None, None))
+    for call in calls:
+        assert call(slots // 12 + 1, 64, 12) == L.Q4_ERR_SHAPE      # t k = 2^26 - 4 + 12 - ..
+        assert call(slots // 12, 64, 12) != L.Q4_ERR_SHAPE
+        assert call(1 << 22, 4096, 1) == L.Q4_ERR_SHAPE             # t ceil(h / 256) = 2^26
+        assert call(1 << 22, 3840, 1) != L.Q4_ERR_SHAPE
+    assert d(5, 64, 2, first=2 ** 31 - 8) == L.Q4_ERR_SHAPE         # experts to 2^31
+    assert d(5000, 64, 2, first=2 ** 31 - 9) == L.Q4_ERR_WORKSPACE
+    assert L.raw.moe_dispatch_workspace_bytes(slots // 12 + 1, 12, 8) == 0
+
+
 def test_quantize_fp8_validation(L):
     def f(x=FAKE, dt=2, t=5, k=64, gated=0, offsets=None, e=1, q=FAKE, s=FAKE, qc=None, sc=None):
         return L.raw.quantize_fp8_tokens(x, dt, t, k, gated, offsets, e, q, s, qc, sc, None)

@@ -221,3 +221,14 @@ def test_equal_bits(lib):
         for _ in range(3):
             two = lib.moe_combine_forward(y, inv, w), *lib.moe_combine_backward(dout, y, inv, w)
             assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+def test_experts_outside(lib):
+    """Experts that 32 bits do not hold are refused, not wrapped."""
+    x, ids = torch.ones(3, 16, device="cuda"), torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    for n, first in ((0, 0), (4097, 0), (2 ** 32 + 4, 0), (4, -1), (4, 2 ** 32), (4, 2 ** 31 - 4)):
+        with pytest.raises(ValueError):
+            lib.moe_dispatch_forward(x, ids, n, first=first)
+    ids[0, 0] = -2 ** 31
+    ids[1, 1] = 2 ** 31 - 2
+    assert lib.moe_dispatch_forward(x, ids, 4, first=2 ** 31 - 5)[1].tolist() == [0, 0, 0, 0, 1]
