@@ -773,7 +773,8 @@ Q4_API int moe_combine_backward(const void* dout, const void* y, int dtype, int6
  *  q, s     device token codes and scales along the row.    w_q, w_s: quantize_fp8_blocks' codes.
  *  offsets  NULL: one matrix w_q [n][k] (e = 1).  Else device [e + 1] int32, ascending: rows
  *           offsets[x] .. offsets[x + 1] - 1 take matrix x of w_q [e][n][k]; rows of no expert
- *           are left as they were.  (Values are kept inside [0, t].)
+ *           are left as they were.  (Values are kept inside [0, t]; with others than ascending ones the
+ *           results are unspecified, and nothing outside the arrays is touched.)
  *  y        device [t][n] of y_dtype Q4_F16 or Q4_BF16: fp32 sums of the groups, rounded once.
  *  workspace device buffer of fp8_linear_workspace_bytes(t, k, n, e, offsets != NULL) bytes (may
  *           be 0): K slices where a product has few output tiles.

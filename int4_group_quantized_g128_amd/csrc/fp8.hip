@@ -503,6 +503,9 @@ struct Tiles {
       }
       __syncthreads();
       w.group0 = span->tile;
+      // (offsets that are not ascending may count more groups than the scales have room for)
+      const int64_t room = g.K / 128 + std::min<int64_t>(g.e, g.K) - w.group0;
+      w.k_rows = std::min<int64_t>(w.k_rows, std::max<int64_t>(room, 0) * 128);
     }
     const int all = int((w.k_rows + 127) / 128), per = (all + g.ksplit - 1) / g.ksplit;
     w.slice = g.ksplit > 1 ? int(z) : 0;

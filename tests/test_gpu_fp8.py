@@ -414,6 +414,25 @@ def test_offsets_outside(lib):
     assert_equal(y[:10], x[:10].double() @ w[0].double().T, "the first expert")
 
 
+@pytest.mark.parametrize("t,k,n", [(300, 256, 144), (1500, 272, 128), (2100, 512, 528)])
+def test_offsets_not_ascending(lib, t, k, n):
+    """Offsets under which experts share rows make more groups of tokens and more tiles than there
+    is room for: the calls stay inside their arrays, and experts with rows of their own come out."""
+    e = 40
+    g = gen_of(t)
+    x, dy = torch.sign(halves(g, t, k)) * 3.5, torch.sign(halves(g, t, n)) * 7
+    w = torch.stack([halves(g, n, k) / 64 for _ in range(e)])
+    off = torch.tensor([0, t] * (e // 2) + [0], dtype=torch.int32, device="cuda")
+    q, s, qc, sc = lib.quantize_fp8_tokens(x, columns=True, offsets=off)
+    wq, ws = lib.quantize_fp8_blocks(w)
+    y = lib.fp8_linear_forward(q, s, wq, ws, offsets=off)
+    dx, dw = lib.fp8_linear_backward(dy.bfloat16(), qc, sc, wq, ws, offsets=off)
+    torch.cuda.synchronize()
+    assert y.shape == (t, n) and dx.shape == x.shape
+    assert not dw[1::2].any()                       # an end before the start: no rows
+    assert_equal(dw[0], dy.double().T @ x.double(), "dw of the first expert")
+
+
 def test_repeats_and_guards(lib):
     """Equal bits from call to call on dirty workspaces, nothing written around the outputs."""
     L = lib._lib
