@@ -22,6 +22,10 @@ template <int DT> struct Elem {
     else if constexpr (DT == 1) static_cast<uint16_t*>(p)[i] = bitcast<uint16_t>(_Float16(v));
     else static_cast<uint16_t*>(p)[i] = bitcast<uint16_t>(__bf16(v));
   }
+  static Q4_DEVICE void copy(void* to, int64_t i, const void* from, int64_t j) {   // the bits, NaNs too
+    if constexpr (DT == 0) static_cast<uint32_t*>(to)[i] = static_cast<const uint32_t*>(from)[j];
+    else static_cast<uint16_t*>(to)[i] = static_cast<const uint16_t*>(from)[j];
+  }
   struct __attribute__((packed, aligned(SIZE))) Raw {
     uint32_t w[4];
   };

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
       } else {
         for (int64_t i = c; i < c1; ++i)
           for (int j = 0; j < a.k; ++j)
-            if (p[j] >= 0) E::put(a.out, p[j] * a.h + i, E::get(a.x, row * a.h + i));
+            if (p[j] >= 0) E::copy(a.out, p[j] * a.h + i, a.x, row * a.h + i);
       }
     }
   }
@@ -437,6 +437,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, void* work, hipStream_t st) {
     if (a.dtype == 0) return dispatch_rows<true, 0>(a, base, st);
     return a.dtype == 1 ? dispatch_rows<true, 1>(a, base, st) : dispatch_rows<true, 2>(a, base, st);
   }
+  // (rows are copied bit by bit: one kernel for both 16-bit types)
   return a.dtype == 0 ? dispatch_rows<false, 0>(a, base, st) : dispatch_rows<false, 1>(a, base, st);
 }
 

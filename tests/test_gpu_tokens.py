@@ -232,3 +232,18 @@ def test_experts_outside(lib):
     ids[0, 0] = -2 ** 31
     ids[1, 1] = 2 ** 31 - 2
     assert lib.moe_dispatch_forward(x, ids, 4, first=2 ** 31 - 5)[1].tolist() == [0, 0, 0, 0, 1]
+
+
+@pytest.mark.parametrize("dt", ALL_TYPES)
+@pytest.mark.parametrize("h", [7, 64, 513])
+def test_rows_keep_their_bits(lib, dt, h):
+    """Rows are copied bit by bit: every 16-bit pattern, NaNs of either kind in fp32, whole vectors
+    and what is left of a row."""
+    bits = torch.int32 if dt is torch.float32 else torch.int16
+    n = -(-65536 // h) * h
+    v = torch.arange(n, device="cuda") % 65536
+    v = (v << 16 | 0x7fa00001).to(torch.int32) if dt is torch.float32 else v.to(torch.int16)
+    x = v.view(dt).view(-1, h)
+    ids = ids_of(gen_of(h), x.shape[0], 2, 5)
+    xp, offsets, perm, inv = lib.moe_dispatch_forward(x, ids, 5)
+    assert torch.equal(xp.view(bits), x.view(bits)[perm.long() // 2])
