@@ -777,7 +777,7 @@ Q4_API int moe_combine_backward(const void* dout, const void* y, int dtype, int6
  *           results are unspecified, and nothing outside the arrays is touched.)
  *  y        device [t][n] of y_dtype Q4_F16 or Q4_BF16: fp32 sums of the groups, rounded once.
  *  workspace device buffer of fp8_linear_workspace_bytes(t, k, n, e, offsets != NULL) bytes (may
- *           be 0): K slices where a product has few output tiles.
+ *           be 0): K slices where a product, or its last round, has few output tiles.
  *  Within a group the matrix core adds eight products at a time, dropping what lies 2^-13 below
  *  the largest of them, and the eights in fp32 (about 1.4e-5 of the result's norm).
  *

@@ -293,7 +293,8 @@ struct Fp8Args {
   void* c;
   int64_t ldc;
   int32_t ksplit;
-  float* part;                // ksplit > 1: [ksplit][M][N]
+  float* part;                // ksplit > 1: [ksplit][M][N]; by expert: a tile per workgroup
+  int32_t tail;               // by expert, large tiles: the last tiles' K steps may be split
 };
 
 Q4_DEVICE uint16_t to16(float v, int dtype) {
@@ -453,36 +454,57 @@ struct Work {
   int64_t k_first, k_rows;   // the summed index's range (dw by expert: the expert's tokens)
   int64_t group0;            // its first group (dw)
   int x, slice, s_begin, s_end;
+  int32_t part;              // >= 0: some K steps of a tile, whose sums go there to be joined later
 };
 
 // By expert, the grid's workgroups walk the tiles that the offsets make; else each has one.
-// Workgroup b runs on XCD b % 8, and each XCD takes one contiguous range of tiles (its L2 keeps
-// the panels they share), in groups of 8 row tiles that walk the column tiles together.
+// Workgroup b runs on XCD b % 8.  Tiles are numbered in bands of 8 row tiles that walk the column
+// tiles together, and a round of an XCD's workgroups is a run of them (its L2 keeps the panels
+// they share); the XCDs take the runs in turn, since experts of few rows make cheap ones.
+//
+// How many tiles there are follows from the offsets, which the host does not know, and a last
+// round of few tiles takes as long as a full one.  So where the tiles that an XCD has left are at
+// most half as many as its workgroups, they are split along K, as many slices as workgroups
+// allow; each workgroup stores the sums of its one slice, and k_fp8_tail adds them.
 template <int MODE, int NT, int BM, int BN>
 struct Tiles {
   ExpertTiles<NT, MODE == FP8_DW ? 128 : BM> experts;
-  uint32_t mtiles, ntiles, plane, start, mine;
+  uint32_t mtiles, ntiles, plane;
+  uint32_t wgs;                   // workgroups of an XCD
+  uint32_t full, slices, limit;   // items from `full` on, below `limit`, are `slices` each of a tile
+  uint32_t start;                 // tile of the first of them
   Span* span;
 
-  Q4_DEVICE Tiles(const Fp8Args& g, uint32_t mt, uint32_t nt, Span* sp, int32_t* tot) : ntiles(nt), span(sp) {
+  Q4_DEVICE Tiles(const Fp8Args& g, uint32_t mt, uint32_t nt, uint32_t per_xcd, Span* sp, int32_t* tot)
+      : ntiles(nt), wgs(per_xcd), span(sp) {
     if (g.offsets) experts.count(g.offsets, g.e, MODE == FP8_DW ? g.K : g.M, tot);
     mtiles = MODE != FP8_DW && g.offsets ? uint32_t(experts.total) : mt;
     plane = mtiles * ntiles;
     const uint32_t total = plane * (MODE == FP8_DW ? uint32_t(g.e) : 1u) * uint32_t(g.ksplit);
-    const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
-    mine = scalar(share + (xcd < rest ? 1u : 0u)), start = scalar(xcd * share + (xcd < rest ? xcd : rest));
+    const uint32_t xcd = blockIdx.x % 8, whole = total / (8 * wgs), rest = total - whole * 8 * wgs;
+    const uint32_t left = rest / 8 + (xcd < rest % 8 ? 1u : 0u);
     plane = scalar(plane), mtiles = scalar(mtiles);
+    full = scalar(whole * wgs), start = scalar(whole * 8 * wgs + xcd * (rest / 8) + min(xcd, rest % 8));
+    slices = 1;
+    if (MODE != FP8_DW && g.tail && left)
+      slices = scalar(uint32_t(max(1, fp8_tail_slices(wgs / left, int((g.K + 127) / 128)))));
+    limit = scalar(full + left * slices);
   }
-  // All threads call; item: 0 .. mine - 1 of this XCD.
+  // The items of a workgroup: one of each round, and no tile's place among the XCD's twice, so that
+  // the workgroups that get row tiles of few rows are not the same in every round.
+  Q4_DEVICE uint32_t item(uint32_t round) const { return round * wgs + (blockIdx.x / 8 + round) % wgs; }
+  // All threads call; item: 0 .. limit - 1 of this XCD.
   Q4_DEVICE Work at(const Fp8Args& g, uint32_t item) const {
-    uint32_t i = start + item;
+    const bool last = item >= full, part = MODE != FP8_DW && last && slices > 1;
+    const uint32_t round = item / wgs;
+    uint32_t i = last ? start + (item - full) / slices : (round * 8 + blockIdx.x % 8) * wgs + item - round * wgs;
     const uint32_t z = i / plane;   // expert (dw) or K slice
     i -= z * plane;
     constexpr uint32_t GM = 8;
     const uint32_t band = i / (GM * ntiles), b0 = band * GM, gm = mtiles - b0 < GM ? mtiles - b0 : GM;
     i -= band * GM * ntiles;
     const uint32_t mt = b0 + i % gm, nt = i / gm;
-    Work w{int64_t(mt) * BM, g.M, int64_t(nt) * BN, 0, g.K, 0, 0, 0, 0, 0};
+    Work w{int64_t(mt) * BM, g.M, int64_t(nt) * BN, 0, g.K, 0, 0, 0, 0, 0, part ? int32_t(scalar((item - full) * 8 + blockIdx.x % 8)) : -1};
     if (MODE != FP8_DW && g.offsets) {
       experts.find(g.offsets, g.M, int(mt), span);
       w.x = span->e;
@@ -507,8 +529,8 @@ struct Tiles {
       const int64_t room = g.K / 128 + std::min<int64_t>(g.e, g.K) - w.group0;
       w.k_rows = std::min<int64_t>(w.k_rows, std::max<int64_t>(room, 0) * 128);
     }
-    const int all = int((w.k_rows + 127) / 128), per = (all + g.ksplit - 1) / g.ksplit;
-    w.slice = g.ksplit > 1 ? int(z) : 0;
+    const int all = int((w.k_rows + 127) / 128), split = part ? int(slices) : g.ksplit, per = (all + split - 1) / split;
+    w.slice = part ? int((item - full) % slices) : g.ksplit > 1 ? int(z) : 0;
     w.s_begin = min(all, w.slice * per), w.s_end = min(all, w.s_begin + per);
     w.m0 = scalar(w.m0), w.m_end = scalar(w.m_end), w.n0 = scalar(w.n0), w.k_first = scalar(w.k_first);
     w.k_rows = scalar(w.k_rows), w.group0 = scalar(w.group0), w.x = scalar(w.x), w.slice = scalar(w.slice);
@@ -662,9 +684,9 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
   const int wm = wid % WM, wn = wid / WM;
   const uint32_t lds0 = lds_addr(ring);
   const uint32_t lba = PA::lane_base(lane), lbb = PB::lane_base(lane);
-  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
-  for (uint32_t item = blockIdx.x / 8; item < tiles.mine; item += (gridDim.x + 7) / 8) {
-    const Work w = tiles.at(g, item);
+  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, (gridDim.x + 7) / 8, &span, tot);
+  for (uint32_t round = 0; tiles.item(round) < tiles.limit; ++round) {
+    const Work w = tiles.at(g, tiles.item(round));
     const uint8_t* ap = g.a + (MODE == FP8_DW ? w.k_first * g.lda : 0);
     const uint8_t* bp = g.b + (MODE == FP8_DW ? w.k_first * g.ldb : w.x * g.b_stride);
     typename PA::Feed fda = PA::feed(ap, g.lda, w.m_end, w.k_rows, w.m0, w.s_begin);
@@ -771,9 +793,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
   const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int wm = wid / WN, wn = wid % WN;   // (a SIMD's two waves in different rows)
   const uint32_t lds0 = lds_addr(mem);
-  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, &span, tot);
-  uint32_t item = blockIdx.x / 8;
-  if (item >= tiles.mine) return;
+  const Tiles<MODE, NT, BM, BN> tiles(g, mtiles, ntiles, (gridDim.x + 7) / 8, &span, tot);
+  uint32_t round = 0, item = scalar(tiles.item(0));
+  if (item >= tiles.limit) return;
   Work w = tiles.at(g, item);
   const uint32_t lda = uint32_t(g.lda), ldb = uint32_t(g.ldb);
   // what a tile's copies need
@@ -977,8 +999,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
     }
     wait_barrier8<0>();   // every wave's copies and reads are done: LDS is free
     const Work done = w;
-    item = scalar(item + (gridDim.x + 7) / 8);
-    const bool more = item < tiles.mine;
+    item = scalar(tiles.item(++round));
+    const bool more = item < tiles.limit;
     if (more) {
       w = tiles.at(g, item);
       begin();
@@ -987,12 +1009,46 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
       int lane = threadIdx.x & 63;
       asm volatile("" : "+v"(lane));
       const int64_t m = done.m0 + wm * (BM / WM), n = done.n0 + wn * COLS;
-      if (g.ksplit > 1) store_slice<MB, NB>(g, done, acc, m, n, lane);
+      if (MODE != FP8_DW && done.part >= 0) {
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(g.part) + ((int64_t(done.part) * NW + wid) * MB * NB) * 64 + lane;
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) o[(a * NB + b) * 64] = acc[a][b];
+      } else if (g.ksplit > 1) store_slice<MB, NB>(g, done, acc, m, n, lane);
       else if (g.dtype == 1) finish64<MODE, MB, true>(g, done, acc, m, n, lane);
       else finish64<MODE, MB, false>(g, done, acc, m, n, lane);
     }
     if (!more) return;
   }
+}
+
+// Adds the slices of the tiles whose K steps were split, in slice order: a wave per 16 rows and 64
+// columns, 4 waves of the product's WM x WN per workgroup; `room`: the product's workgroups.
+template <int MODE, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(256) k_fp8_tail(Fp8Args g, uint32_t mtiles, uint32_t ntiles, uint32_t room) {
+  constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
+  __shared__ Span span;
+  __shared__ int32_t tot[4];
+  const uint32_t wgs = room / 8;
+  const Tiles<MODE, 256, BM, BN> tiles(g, mtiles, ntiles, wgs, &span, tot);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const uint32_t item = tiles.full + blockIdx.x / 8 * tiles.slices;   // the tile's first slice
+  if (tiles.slices == 1 || item >= tiles.limit) return;
+  const Work w = tiles.at(g, item);
+  const int piece = int(blockIdx.y) * 4 + wave, wid = piece / MB, a = piece % MB;   // of NW * MB
+  const int64_t m = w.m0 + wid / WN * (BM / WM) + 16 * a, n = w.n0 + wid % WN * (16 * NB);
+  if (m >= w.m_end) return;
+  f32x4_t acc[1][NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[0][b] = f32x4_t{0, 0, 0, 0};
+  for (uint32_t s = 0; s < tiles.slices; ++s) {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(g.part) + ((int64_t(w.part + int(s) * 8) * NW + wid) * MB + a) * NB * 64 + lane;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[0][b] += p[b * 64];
+  }
+  if (g.dtype == 1) finish64<MODE, 1, true>(g, w, acc, m, n, lane);
+  else finish64<MODE, 1, false>(g, w, acc, m, n, lane);
 }
 
 // Adds the K slices of a split product in slice order, four columns per thread.
@@ -1145,6 +1201,7 @@ hipError_t launch_rows8(const Fp8Args& g, bool few, hipStream_t st) {
 template <int MODE>
 hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
   g.ksplit = p.ksplit;
+  g.tail = fp8_has_tail(p, Fp8Mode(MODE), ceil_div(g.K, 128), g.offsets != nullptr);
   const uint32_t nt = uint32_t(ceil_div(g.N, p.tile));
   uint32_t mt = uint32_t(ceil_div(g.M, p.tile));
   int64_t items;
@@ -1155,19 +1212,28 @@ hipError_t launch_tiles8(Fp8Args g, const Plan& p, hipStream_t st) {
   unsigned grid = unsigned(items);
   if (p.tile != 64 || (MODE != FP8_DW && g.offsets)) {
     const int64_t room = 256 * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 3);
-    grid = unsigned(std::min<int64_t>(room, ceil_div(items, 8) * 8));
+    grid = unsigned(g.tail ? room : std::min<int64_t>(room, ceil_div(items, 8) * 8));
   }
   if (p.tile == 256) hipLaunchKernelGGL((k_fp8_big<MODE, 256, 256, 2, 4, 2>), dim3(grid), dim3(512), 0, st, g, mt, nt);
   else if (p.tile == 128) hipLaunchKernelGGL((k_fp8_big<MODE, 128, 128, 2, 2, 2>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   else hipLaunchKernelGGL((k_fp8<MODE, 64, 64, 2, 2, 3>), dim3(grid), dim3(256), 0, st, g, mt, nt);
   const hipError_t e = hipGetLastError();
+  if constexpr (MODE != FP8_DW)
+    if (e == hipSuccess && g.tail) {   // (at most half of an XCD's workgroups have a tile to split)
+      if (p.tile == 256) hipLaunchKernelGGL((k_fp8_tail<MODE, 256, 256, 2, 4>), dim3(grid / 2, 16), dim3(256), 0, st, g, mt, nt, grid);
+      else hipLaunchKernelGGL((k_fp8_tail<MODE, 128, 128, 2, 2>), dim3(grid / 2, 4), dim3(256), 0, st, g, mt, nt, grid);
+      return hipGetLastError();
+    }
   if (e != hipSuccess || p.ksplit == 1) return e;
   const int64_t threads = g.M * ((g.N + 3) / 4);
   hipLaunchKernelGGL(k_fp8_join, dim3(unsigned(ceil_div(threads, 256))), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 
-int64_t part_bytes8(const Plan& p, int64_t m, int64_t n) { return p.ksplit > 1 ? int64_t(p.ksplit) * m * n * 4 : 0; }
+int64_t part_bytes8(const Plan& p, Fp8Mode mode, int64_t m, int64_t n, int64_t steps, bool grouped) {
+  if (fp8_has_tail(p, mode, steps, grouped)) return int64_t(256) * (p.tile == 256 ? 1 : 2) * p.tile * p.tile * 4;
+  return p.ksplit > 1 ? int64_t(p.ksplit) * m * n * 4 : 0;
+}
 
 template <int DT>
 hipError_t quantize_as(const Fp8QuantArgs& a, hipStream_t st) {
@@ -1200,7 +1266,7 @@ hipError_t launch_quantize_fp8_blocks(const void* w, int dtype, int64_t e, int64
 }
 
 int64_t fp8_linear_workspace(int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {
-  return t == 0 ? 0 : part_bytes8(fp8_plan(FP8_Y, t, k, n, e, grouped), t, n);
+  return t == 0 ? 0 : part_bytes8(fp8_plan(FP8_Y, t, k, n, e, grouped), FP8_Y, t, n, ceil_div(k, 128), grouped);
 }
 
 hipError_t launch_fp8_linear(const uint8_t* q, const float* s, int64_t t, int64_t k, const uint8_t* wq, const float* ws,
@@ -1243,7 +1309,8 @@ static Fp8GradWork grad_work8(void* base, int64_t t, int64_t k, int64_t n, int32
   w.q_row = take(t * n), w.q_col = take(t * n);
   w.s_row = reinterpret_cast<float*>(take(ceil_div(n, 128) * t * 4));
   w.s_col = reinterpret_cast<float*>(take((grouped ? t / 128 + std::min<int64_t>(e, t) : ceil_div(t, 128)) * n * 4));
-  w.part = reinterpret_cast<float*>(take(std::max(part_bytes8(w.dx, t, k), part_bytes8(w.dw, n, k))));
+  w.part = reinterpret_cast<float*>(take(std::max(part_bytes8(w.dx, FP8_DX, t, k, ceil_div(n, 128), grouped),
+                                                      part_bytes8(w.dw, FP8_DW, n, k, 0, grouped))));
   return w;
 }
 int64_t fp8_linear_bwd_workspace(int64_t t, int64_t k, int64_t n, int32_t e, bool grouped) {

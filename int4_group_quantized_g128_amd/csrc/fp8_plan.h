@@ -10,6 +10,18 @@ enum Fp8Mode { FP8_Y = 0, FP8_DX = 1, FP8_DW = 2 };
 // A launch holds fewer workgroups than this (of up to 512 threads: below 2^32 in all).
 constexpr int64_t kMostItems = int64_t(1) << 23;
 
+// K slices of each tile of a last round (by expert) that leaves `room` workgroups per tile: at least
+// 4 steps each, 8 at most.
+constexpr int fp8_tail_slices(int64_t room, int steps) {
+  const int most = steps / 4 < 8 ? steps / 4 : 8;
+  return room < most ? int(room) : most;
+}
+// (From K = 4096 on: 32 experts of 128 rows and one of 300, 7168 / 4096, 298 -> 257 us; but 8 of 1024
+// rows, 2048 / 4096, 102 -> 106, and 16 of 312, 1024 / 2048, 27 -> 31: the slices' join is a launch.)
+inline bool fp8_has_tail(const Plan& p, Fp8Mode mode, int64_t steps, bool grouped) {
+  return grouped && mode != FP8_DW && p.tile >= 128 && steps >= 32;
+}
+
 // Estimated time (us) of `batches` products with square tiles of `bm` and K in `ks` slices of whole
 // 128-element steps: the form of plan_us, its constants (per mode and tile: a step of a workgroup
 // alone on its CU and of a full CU per workgroup, a workgroup's start and end) fitted to 210

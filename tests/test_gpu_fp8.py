@@ -310,6 +310,46 @@ def test_linear_backward_by_expert_exact(lib, counts, k, n, start):
     assert (dx[:start] == 9).all() and (dx[start + total:] == 9).all()
 
 
+# (rows, experts, k, n; tile of the plan): the tiles that the offsets make fill the last round to any part
+TAILS = [(1500, 5, 4112, 2064, 128), (3200, 16, 4112, 2064, 256), (5400, 9, 4112, 2064, 256), (1800, 9, 8208, 4112, 256)]
+TAIL_COUNTS = [[10], [300, 0, 0, 257], [129] * 5, [1, 0, 512, 256, 700], [1400], [256] * 3 + [0, 400], [0] * 5]
+
+
+@pytest.mark.parametrize("t,e,k,n,tile", TAILS)
+@pytest.mark.parametrize("counts", TAIL_COUNTS, ids=str)
+def test_last_round_by_expert(lib, t, e, k, n, tile, counts):
+    """Products by expert whose last tiles' K steps are split, in both directions."""
+    L = lib._lib
+    room = 256 * (1 if tile == 256 else 2) * tile * tile * 4
+    assert L.raw.fp8_linear_workspace_bytes(t, k, n, e, 1) == room
+    counts = counts + [0] * (e - len(counts))
+    start, total = 5, sum(counts)
+    g = gen_of(total + k)
+    dt = torch.bfloat16 if total % 2 else torch.float16
+    x, dy = halves(g, t, k) / 64, torch.sign(halves(g, t, k)) / 8
+    w = torch.stack([halves(g, n, k) / 64 for _ in range(e)])
+    off = offsets_of(counts, start)
+    q, s = lib.quantize_fp8_tokens(x)
+    wq, ws = lib.quantize_fp8_blocks(w)
+    y = torch.full((t, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=y)
+    # the other direction sums over k as well: W is [k, n]
+    u = torch.stack([torch.sign(halves(g, k, n)) for _ in range(e)])
+    uq, us = lib.quantize_fp8_blocks(u)
+    qc, sc = lib.quantize_fp8_tokens(torch.sign(halves(g, t, n)), columns=True, offsets=off)[2:]
+    dx = torch.full((t, n), 9.0, dtype=dt, device="cuda")
+    lib.fp8_linear_backward(dy.to(dt), qc, sc, uq, us, offsets=off, out=dx)
+
+    def check(z, r):
+        assert_equal(y[r], x[r].double() @ w[z].double().T, f"y of expert {z}")
+        if r.stop > r.start:   # (1 / 448 and 1 / 8 / 448, the scales, are rounded: 7 divides 448)
+            near(dx[r], rows_of(*row_ref(dy[r].to(dt))), blocks_of(uq[z], us[z]), f"dx of expert {z}")
+
+    by_expert(counts, start, check)
+    for out in (y, dx):
+        assert (out[:start] == 9).all() and (out[start + total:] == 9).all()
+
+
 # ------------------------------------------------------------------ products of any values
 def near(got, a, b, what):
     """got against a @ b (64 bits, both factors codes times scales) by the bound at the top."""
