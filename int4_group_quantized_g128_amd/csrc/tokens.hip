@@ -297,14 +297,17 @@ __global__ void __launch_bounds__(kThreads) k_tokens_combine(const void* __restr
     for (int u = 0; u < U; ++u) {
       const int j = min(j0 + u, k - 1);
       const uint32_t r = uint32_t(p[j]);
-      ok[u] = j0 + u < k && r < rows;   // (a dropped slot is -1; its row is read from row 0 and left out)
+      ok[u] = j0 + u < k && r < rows;   // (a dropped slot is -1 and left out)
       at[u] = int64_t(ok[u] ? r : 0) * h + c;
       wj[u] = wt ? wt[j] : 1.f;
     }
     typename E::Raw v[U];
     if (whole) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = E::template load<NT>(y, at[u]);
+      for (int u = 0; u < U; ++u) {   // (one branch of the whole wave: 4096 tokens of 7168, one slot of 8 held, 51 -> 45 us)
+        if (ok[u]) v[u] = E::template load<NT>(y, at[u]);
+        else v[u] = typename E::Raw{};
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
