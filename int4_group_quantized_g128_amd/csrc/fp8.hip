@@ -465,7 +465,8 @@ struct Work {
 // How many tiles there are follows from the offsets, which the host does not know, and a last
 // round of few tiles takes as long as a full one.  So where the tiles that an XCD has left are at
 // most half as many as its workgroups, they are split along K, as many slices as workgroups
-// allow; each workgroup stores the sums of its one slice, and k_fp8_tail adds them.
+// allow; each workgroup stores the sums of its one slice, and k_fp8_tail adds them (32 experts of 128
+// rows and one of 300, 7168 / 4096: 298 -> 257 us).
 template <int MODE, int NT, int BM, int BN>
 struct Tiles {
   ExpertTiles<NT, MODE == FP8_DW ? 128 : BM> experts;
@@ -661,7 +662,9 @@ Q4_DEVICE void finish64(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB
 }
 
 // BM x BN per workgroup of WM x WN waves, a ring of NS K steps in LDS: step s + NS - 1 is copied
-// while step s is multiplied, one barrier per step.
+// while step s is multiplied, one barrier per step.  Three steps of 64 x 64 let a CU hold three
+// workgroups; a lone one takes 0.4 us a step, the 16 KB that its CU reads (rings of 5 and 8 steps,
+// and two steps per barrier, were no faster).  64 x 7168 x 4096 in 4 K slices 11.6 us.
 template <int MODE, int BM, int BN, int WM, int WN, int NS>
 __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
@@ -771,6 +774,11 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
 // A workgroup's next tile is on its way while the results of one are stored.  (Everything that has
 // one value per workgroup is kept in scalar registers and every helper inlined: as soon as the
 // arguments went through memory the loops spilled, dw of 4096 x 7168 x 4096 141 -> 233 us.)
+//
+// 4096 x 7168 x 4096 takes 108 us (2.2 PFLOP/s), 4096 x 2048 x 16384 150 to 172 (1.6 to 1.8).  A step
+// of the 256 tile has 2048 matrix cycles per SIMD and moves 256 KB through LDS, which at 128 bytes a
+// cycle are 2048 as well; the matrix core is busy 43 to 50 % of the time, without bank conflicts, at
+// a clock that falls to 1.9 GHz.
 template <int MODE, int BM, int BN, int WM, int WN, int SLOTS>
 __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
@@ -1074,7 +1082,7 @@ __global__ void __launch_bounds__(256) k_fp8_join(Fp8Args g) {
   store_row<4>(g.c, g.dtype, m * g.ldc + n, v, count);
 }
 
-// Few rows (per expert): bound by reading the weights once.  A workgroup owns 16 columns of y of
+// Few rows (per expert): bound by reading the weights once (one row, 2048 / 16384: 8 us, 4.2 TB/s).  A workgroup owns 16 columns of y of
 // one expert, its 8 waves take the 128-code K steps in turn and feed the matrix core straight from
 // global memory, then add their sums through LDS in wave order.
 template <int RB, int MAXRB, int DEEP>

@@ -27,8 +27,8 @@ inline bool fp8_has_tail(const Plan& p, Fp8Mode mode, int64_t steps, bool groupe
 // alone on its CU and of a full CU per workgroup, a workgroup's start and end) fitted to 210
 // products (17 to 4096 rows, widths 512 to 16384), whose tiles and slices were all timed: the
 // plan's choice is the fastest or within 8 % of it for 204 of them (the worst 17 %, dx of 64 rows,
-// 2048 / 512).  Weights from memory
-// take at least their bytes at 5.8 TB/s.
+// 2048 / 512).  Weights from memory take at least their bytes at 5.8 TB/s.  (By expert a split last
+// round is not in the estimate: how many tiles it has the offsets say.)
 inline double fp8_plan_us(Fp8Mode mode, int64_t m, int64_t n, int64_t steps, int64_t batches, int bm, int64_t ks,
                           bool uneven = false) {
   const int t = bm == 64 ? 0 : bm == 128 ? 1 : 2;

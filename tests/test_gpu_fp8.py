@@ -350,6 +350,37 @@ def test_last_round_by_expert(lib, t, e, k, n, tile, counts):
         assert (out[:start] == 9).all() and (out[start + total:] == 9).all()
 
 
+def test_last_round_in_a_graph(lib):
+    """A captured product by expert follows the offsets that it finds at each replay."""
+    t, e, k, n = 3200, 16, 4112, 2064
+    g = gen_of(3)
+    x = halves(g, t, k) / 64
+    w = torch.stack([halves(g, n, k) / 64 for _ in range(e)])
+    q, s = lib.quantize_fp8_tokens(x)
+    wq, ws = lib.quantize_fp8_blocks(w)
+    off = offsets_of([200] * e)
+    y = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=y)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=y)
+    for counts in ([200] * e, [10], [1400], [300, 0, 0, 257], [3200], [0], [1] * e, [10]):
+        counts = counts + [0] * (e - len(counts))
+        off.copy_(offsets_of(counts))
+        y.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.full_like(y, 9)
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=want)
+        assert torch.equal(y, want)
+        for z, (r, one) in enumerate(by_expert(counts, 0, lambda z, r: (r, x[r].double() @ w[z].double().T))):
+            assert_equal(y[r], one, f"y of expert {z}")
+
+
 # ------------------------------------------------------------------ products of any values
 def near(got, a, b, what):
     """got against a @ b (64 bits, both factors codes times scales) by the bound at the top."""
