@@ -1082,9 +1082,9 @@ __global__ void __launch_bounds__(256) k_fp8_join(Fp8Args g) {
   store_row<4>(g.c, g.dtype, m * g.ldc + n, v, count);
 }
 
-// Few rows (per expert): bound by reading the weights once (one row, 2048 / 16384: 8 us, 4.2 TB/s).  A workgroup owns 16 columns of y of
-// one expert, its 8 waves take the 128-code K steps in turn and feed the matrix core straight from
-// global memory, then add their sums through LDS in wave order.
+// Few rows (per expert): bound by reading the weights once (one row, 2048 / 16384: 8 us, 4.2 TB/s).
+// A workgroup owns 16 columns of y of one expert, its 8 waves take the 128-code K steps in turn and
+// feed the matrix core straight from global memory, then add their sums through LDS in wave order.
 template <int RB, int MAXRB, int DEEP>
 Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws, int64_t n0, int64_t row0, int rows,
                             f32x4_t (*sums)[MAXRB][64]) {
