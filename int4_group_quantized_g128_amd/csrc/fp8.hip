@@ -1206,11 +1206,40 @@ Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws,
   __syncthreads();
 }
 
+// The expert with the i-th of the runs of rows that are not empty, or -1: all of a workgroup's 8
+// waves call, 64 experts each at a time.
+Q4_DEVICE int nth_run(const int32_t* offsets, int e, int64_t t, int i, uint64_t* runs /* LDS [8] */) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  for (int x0 = 0; x0 < e; x0 += 512) {
+    int64_t first, count = 0;
+    if (x0 + int(threadIdx.x) < e) expert_rows(offsets, x0 + int(threadIdx.x), t, first, count);
+    const uint64_t own = __ballot(count > 0);
+    if (lane == 0) runs[wave] = own;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const uint64_t m = scalar(runs[w]);
+      const int n = __popcll(m);
+      if (i < n) {
+        const bool mine = (m >> lane & 1) && __popcll(m & ((uint64_t(1) << lane) - 1)) == i;
+        return scalar(x0 + 64 * w + __ffsll((unsigned long long)__ballot(mine)) - 1);
+      }
+      i -= n;
+    }
+    __syncthreads();
+  }
+  return -1;
+}
+
+// Workgroup (x, n): 16 columns of expert x; with `search`, of the x-th expert that has a row.
 template <int MAXRB, int DEEP>
-__global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols) {
+__global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols, int search) {
   __shared__ f32x4_t sums[8][MAXRB][64];
-  const int x = int(blockIdx.x / ncols);
+  __shared__ uint64_t runs[8];
+  int x = int(blockIdx.x / ncols);
   const int64_t n0 = int64_t(blockIdx.x - x * ncols) * 16;
+  if (search) x = nth_run(g.offsets, g.e, g.M, x, runs);
+  if (x < 0) return;
   int64_t first = 0, count = g.M;
   if (g.offsets) expert_rows(g.offsets, x, g.M, first, count);
   const uint8_t* w = g.b + x * g.b_stride;
@@ -1229,11 +1258,13 @@ __global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols) {
 // 14336 16.3 / 13.5, 8192 / 8192 15.0 / 14.0).
 hipError_t launch_rows8(const Fp8Args& g, bool few, hipStream_t st) {
   const uint32_t ncols = uint32_t(ceil_div(g.N, 16));
-  const dim3 grid(ncols * uint32_t(g.offsets ? g.e : 1));
+  const int64_t e = g.offsets ? g.e : 1;
+  const bool search = fp8_rows_search(g.M, g.N, e);   // (never with one)
+  const dim3 grid(unsigned(fp8_rows_grid(g.M, g.N, e)));
   const bool deep = g.K >= 4096 && g.N * g.K * (g.offsets ? g.e : 1) >= int64_t(48) << 20;
-  if (!few) hipLaunchKernelGGL((k_fp8_rows<4, 4>), grid, dim3(512), 0, st, g, ncols);
-  else if (deep) hipLaunchKernelGGL((k_fp8_rows<1, 4>), grid, dim3(512), 0, st, g, ncols);
-  else hipLaunchKernelGGL((k_fp8_rows<1, 1>), grid, dim3(512), 0, st, g, ncols);
+  if (!few) hipLaunchKernelGGL((k_fp8_rows<4, 4>), grid, dim3(512), 0, st, g, ncols, search);
+  else if (deep) hipLaunchKernelGGL((k_fp8_rows<1, 4>), grid, dim3(512), 0, st, g, ncols, search);
+  else hipLaunchKernelGGL((k_fp8_rows<1, 1>), grid, dim3(512), 0, st, g, ncols, search);
   return hipGetLastError();
 }
 
