@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(256) k_fp8_join(Fp8Args g) {
 // Few rows (per expert): bound by reading the weights once (one row, 2048 / 16384: 8 us, 4.2 TB/s).
 // A workgroup owns 16 columns of y of one expert, its 8 waves take the 128-code K steps in turn and
 // feed the matrix core straight from global memory, then add their sums through LDS in wave order.
-template <int RB, int MAXRB, int DEEP>
+template <int RB, int MAXRB>
 Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws, int64_t n0, int64_t row0, int rows,
                             f32x4_t (*sums)[MAXRB][64]) {
   constexpr int W = 8;
@@ -1163,13 +1163,9 @@ Q4_DEVICE void rows_product(const Fp8Args& g, const uint8_t* w, const float* ws,
         for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(p[e], sc[u][r], acc[r][e]);
       }
   };
-  constexpr int U = RB == 1 ? DEEP : RB == 2 ? 2 : 1;   // steps in flight
+  constexpr int U = MAXRB > 1 && RB <= 2 ? 2 : 1;   // steps in flight
   int s = wave;
   for (; s + (U - 1) * W < full; s += U * W) steps(std::integral_constant<int, U>{}, s);
-  if (U > 2 && s + W < full) {
-    steps(std::integral_constant<int, 2>{}, s);
-    s += 2 * W;
-  }
   for (; s < full; s += W) steps(std::integral_constant<int, 1>{}, s);
   if (s == full && g.K % 128) {   // the K tail: chunks past the row's end hold zeros
     const int64_t at = int64_t(full) * 128;
@@ -1232,7 +1228,7 @@ Q4_DEVICE int nth_run(const int32_t* offsets, int e, int64_t t, int i, uint64_t*
 }
 
 // Workgroup (x, n): 16 columns of expert x; with `search`, of the x-th expert that has a row.
-template <int MAXRB, int DEEP>
+template <int MAXRB>
 __global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols, int search) {
   __shared__ f32x4_t sums[8][MAXRB][64];
   __shared__ uint64_t runs[8];
@@ -1246,25 +1242,28 @@ __global__ void __launch_bounds__(512) k_fp8_rows(Fp8Args g, uint32_t ncols, int
   const float* ws = g.sb + x * g.sb_stride;
   while (count > 0) {
     const int rows = int(count < 16 * MAXRB ? count : 16 * MAXRB);
-    if (MAXRB == 1 || rows <= 16) rows_product<1, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
-    else if (MAXRB == 2 || rows <= 32) rows_product<2, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
-    else rows_product<MAXRB, MAXRB, DEEP>(g, w, ws, n0, first, rows, sums);
+    if constexpr (MAXRB == 1) {
+      rows_product<1, 1>(g, w, ws, n0, first, rows, sums);
+    } else {
+      if (rows <= 16) rows_product<1, MAXRB>(g, w, ws, n0, first, rows, sums);
+      else if (rows <= 32) rows_product<2, MAXRB>(g, w, ws, n0, first, rows, sums);
+      else rows_product<MAXRB, MAXRB>(g, w, ws, n0, first, rows, sums);
+    }
     first += rows, count -= rows;
   }
 }
 
-// Up to 16 rows: one step in flight per wave and as many waves as fit, but four where K is long
-// and the weights are many (one row: 2048 / 16384 7.6 us against 8.9, 7168 / 4096 7.3 / 7.6; 4096 /
-// 14336 16.3 / 13.5, 8192 / 8192 15.0 / 14.0).
+// Passes of 16 rows with one step in flight per wave and as many waves as fit (four steps in flight
+// of fewer waves: one row, 8192 / 8192, 16.6 -> 17 us, 4096 / 14336 15.7 -> 17, 16 rows of 8192 / 8192
+// 21 -> 23, 64 rows of 32 experts, 7168 / 4096, 143 -> 166), or of 64 with two (8 to 32 rows of 32
+// experts, 16384 / 256, 38 us; with one 41).
 hipError_t launch_rows8(const Fp8Args& g, bool few, hipStream_t st) {
   const uint32_t ncols = uint32_t(ceil_div(g.N, 16));
   const int64_t e = g.offsets ? g.e : 1;
   const bool search = fp8_rows_search(g.M, g.N, e);   // (never with one)
   const dim3 grid(unsigned(fp8_rows_grid(g.M, g.N, e)));
-  const bool deep = g.K >= 4096 && g.N * g.K * (g.offsets ? g.e : 1) >= int64_t(48) << 20;
-  if (!few) hipLaunchKernelGGL((k_fp8_rows<4, 4>), grid, dim3(512), 0, st, g, ncols, search);
-  else if (deep) hipLaunchKernelGGL((k_fp8_rows<1, 4>), grid, dim3(512), 0, st, g, ncols, search);
-  else hipLaunchKernelGGL((k_fp8_rows<1, 1>), grid, dim3(512), 0, st, g, ncols, search);
+  if (few) hipLaunchKernelGGL((k_fp8_rows<1>), grid, dim3(512), 0, st, g, ncols, search);
+  else hipLaunchKernelGGL((k_fp8_rows<4>), grid, dim3(512), 0, st, g, ncols, search);
   return hipGetLastError();
 }
 
@@ -1357,7 +1356,7 @@ hipError_t launch_fp8_linear(const uint8_t* q, const float* s, int64_t t, int64_
   g.part = static_cast<float*>(work);
   const Plan p = fp8_plan(FP8_Y, t, k, n, e, offsets != nullptr);
   if (p.tile) return launch_tiles8<FP8_Y>(g, p, st);
-  return launch_rows8(g, offsets ? t <= 4 * int64_t(e) : t <= 16, st);
+  return launch_rows8(g, fp8_rows_sixteen(t, e, offsets != nullptr), st);
 }
 
 // Workspace of the gradients: codes and scales of dy along its rows and along the tokens, the K

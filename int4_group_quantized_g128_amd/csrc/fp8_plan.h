@@ -61,8 +61,8 @@ inline double fp8_rows_us(int64_t m, int64_t k, int64_t n, int64_t batches) {
 // By expert only the device knows which experts have rows.  The few-rows kernel gets a workgroup per
 // expert and 16 columns, or per run of rows that may not be empty, `runs` of them at most, and each
 // workgroup searches for its run: a workgroup of an expert without a row costs 0.7 ns, a search 0.9 us
-// per 512 experts in every round of 1024 workgroups (8 rows of 256 experts, 7168 / 4096: 85 us for all
-// experts, 48 with the search; 300 rows of 300, 256 / 4096: 125 and 191).
+// per 512 experts in every round of 1024 workgroups (8 rows of 256 experts, 7168 / 4096: 67 us for all
+// experts, 42 with the search; 300 rows of 300, 256 / 4096: 125 and 191).
 inline double fp8_idle_us(int64_t runs, int64_t e, int64_t n) { return double(e - runs) * ceil_div(n, 16) * 0.7e-3; }
 inline double fp8_search_us(int64_t runs, int64_t e, int64_t n) {
   return std::max(1.0, double(runs) * ceil_div(n, 16) / 1024) * 0.9 * ceil_div(e, 512);
@@ -75,6 +75,9 @@ inline bool fp8_rows_search(int64_t t, int64_t n, int64_t e) {
 inline int64_t fp8_rows_grid(int64_t t, int64_t n, int64_t e) {
   return (fp8_rows_search(t, n, e) ? std::min(e, t) : e) * ceil_div(n, 16);
 }
+
+// Whether the few-rows kernel takes 16 rows a pass, else 64.
+inline bool fp8_rows_sixteen(int64_t t, int32_t e, bool grouped) { return grouped ? t <= 4 * int64_t(e) : t <= 16; }
 
 inline Plan fp8_tiles(Fp8Mode mode, int64_t m, int64_t n, int64_t steps, int64_t batches, bool split, double* us,
                       bool uneven = false) {

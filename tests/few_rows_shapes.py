@@ -7,3 +7,11 @@ SCATTERED = [(8, 4112, 4100, 256, {0: 1, 3: 1, 63: 1, 64: 1, 65: 1, 127: 1, 200:
              (20, 4112, 48, 4096, {0: 3, 511: 1, 512: 1, 513: 2, 1023: 1, 1024: 4, 3583: 1, 3584: 2, 4095: 5}),
              (12, 2064, 1008, 1000, {448: 1, 449: 1, 511: 1, 999: 1}), (6, 2064, 2000, 700, {600: 5, 699: 1}),
              (3, 2048, 600, 513, {512: 3}), (5, 1040, 640, 512, {511: 4}), (7, 2064, 1008, 300, {})]
+
+# Rows of each expert (None: one matrix), k, n; whether in passes of 16 rows or of 64.  Experts of more
+# rows than a pass, K steps of a wave that end with one and with two in flight, K ends of 16 to 112.
+PASSES = [(None, 1, 8192, 8192, 16), (None, 3, 14352, 4096, 16), (None, 16, 4208, 1030, 16), (None, 2, 1136, 48, 16),
+          (None, 65, 2048, 96, 64), (None, 17, 2176, 1000, 64), (None, 33, 3200, 96, 64), (None, 24, 7280, 4096, 64),
+          ([17, 0, 1, 33, 0, 60, 0, 2] + [0] * 40, 4176, 132, 16), ([40] + [0] * 12, 2048, 1030, 16),
+          ([3, 1, 0, 29, 0, 0, 7, 16] + [0] * 9, 7184, 520, 16), ([0] * 31 + [128], 1296, 36, 16),
+          ([65, 1, 130, 0, 20, 33, 7], 4112, 100, 64), ([0, 0, 200, 5], 5168, 48, 64), ([40, 9, 64, 16, 17], 16384, 80, 64)]

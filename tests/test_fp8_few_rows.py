@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 from tests.conftest import ROOT
-from tests.few_rows_shapes import SCATTERED
+from tests.few_rows_shapes import PASSES, SCATTERED
 
 SOURCE = r"""
 #include "fp8_plan.h"
@@ -20,6 +20,7 @@ extern "C" int fits(int64_t t, int64_t k, int64_t n, int e, int grouped) {
 }
 extern "C" int search(int64_t t, int64_t n, int64_t e) { return q4::fp8_rows_search(t, n, e); }
 extern "C" int64_t grid(int64_t t, int64_t n, int64_t e) { return q4::fp8_rows_grid(t, n, e); }
+extern "C" int sixteen(int64_t t, int e, int grouped) { return q4::fp8_rows_sixteen(t, e, grouped); }
 """
 MOST = 1 << 23   # workgroups of a launch
 
@@ -38,6 +39,7 @@ def plan(tmp_path_factory):
     i64, i32 = ctypes.c_int64, ctypes.c_int
     lib.tile.argtypes = lib.fits.argtypes = [i64, i64, i64, i32, i32]
     lib.search.argtypes = lib.grid.argtypes = [i64, i64, i64]
+    lib.sixteen.argtypes = [i64, i32, i32]
     lib.grid.restype = i64
     return lib
 
@@ -66,3 +68,12 @@ def test_launches_fit(plan):
             assert min(t, e) * -(-n // 16) <= grid < MOST
             seen.add(plan.search(t, n, e))
     assert seen == {0, 1}
+
+
+def test_shapes_take_both_passes(plan):
+    for counts, *t, k, n, rows in PASSES:
+        t, e, grouped = (t[0], 1, 0) if counts is None else (sum(counts), len(counts), 1)
+        assert plan.tile(t, k, n, e, grouped) == 0, (counts, t, k, n)
+        assert plan.sixteen(t, e, grouped) == (rows == 16), (counts, t, k, n)
+    for many in (16, 64):   # more rows than a pass, of one matrix or expert
+        assert any(max(c[0] or [c[1]]) > c[-1] for c in PASSES if c[-1] == many)
