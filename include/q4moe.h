@@ -779,8 +779,9 @@ Q4_API int moe_combine_backward(const void* dout, const void* y, int dtype, int6
  *  workspace device buffer of fp8_linear_workspace_bytes(t, k, n, e, offsets != NULL) bytes (may
  *           be 0): K slices where a product, or its last round, has few output tiles.
  *  Within a group the matrix core adds eight products at a time, dropping what lies 2^-13 below
- *  the largest of them, and the eights in fp32 (about 1.4e-5 of the result's norm; few rows are
- *  multiplied without that loss).
+ *  the largest of them, and the eights in fp32 (about 1.4e-5 of the result's norm).  A call of up to
+ *  16 rows (t <= 16, with offsets or without) is multiplied without that loss, all sums in fp32;
+ *  for more rows it depends on the sizes whether there is one.
  *
  * fp8_linear_backward -- given dy device [t][n] of dtype Q4_F16 or Q4_BF16: dy is quantised along
  * its rows for dx and along the tokens for dw, each by quantize_fp8_tokens' rule, and

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 from tests.conftest import ROOT
-from tests.few_rows_shapes import PASSES, SCATTERED
+from tests.few_rows_shapes import PASSES, SCATTERED, SIXTEEN
 
 SOURCE = r"""
 #include "fp8_plan.h"
@@ -77,3 +77,15 @@ def test_shapes_take_both_passes(plan):
         assert plan.sixteen(t, e, grouped) == (rows == 16), (counts, t, k, n)
     for many in (16, 64):   # more rows than a pass, of one matrix or expert
         assert any(max(c[0] or [c[1]]) > c[-1] for c in PASSES if c[-1] == many)
+
+
+def test_up_to_sixteen_rows_take_passes_of_sixteen(plan):
+    for t, k, n, counts in SIXTEEN:
+        assert plan.tile(t, k, n, len(counts or [0]), int(counts is not None)) == 0
+    rng = random.Random(6)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    for _ in range(20000):
+        t, k, n = rng.randint(1, 16), log(1, 1 << 16) * 16, log(1, 1 << 20)
+        for e, grouped in ((1, 0), (log(1, 4096), 1)):
+            assert plan.tile(t, k, n, e, grouped) == 0 and plan.sixteen(t, e, grouped)
+            assert plan.fits(t, k, n, e, grouped)

@@ -3,7 +3,7 @@ exact in fp32, as in the products' other tests)."""
 import pytest
 import torch
 
-from tests.few_rows_shapes import PASSES, SCATTERED
+from tests.few_rows_shapes import PASSES, SCATTERED, SIXTEEN
 from tests.helpers import require_gpu
 from tests.test_gpu_fp8 import E4M3, TYPES, assert_equal, by_expert, ceil, gen_of, halves, offsets_of
 
@@ -56,3 +56,39 @@ def test_passes(lib, shape, dt):
     y = lib.fp8_linear_forward(q, s, *lib.quantize_fp8_blocks(w), offsets=offsets_of(counts), out_dtype=dt)
     for z, (r, one) in enumerate(by_expert(counts, 0, lambda z, r: (r, x[r].double() @ w[z].double().T))):
         assert_equal(y[r], one, f"expert {z}")
+
+
+def beside_large(g, t, n, k):
+    """x [t, k] and w [n, k] whose codes are their values: in each eight of the summed index one product
+    of +-448^2 and seven of at most 4 in steps of 1 / 4; the large ones cancel within each group of 128.  Every
+    sum in any order is a multiple of 1 / 4 below 2^22, exact in fp32; one that drops what is 2^-13
+    below an eight's largest loses nearly all of the result."""
+    small = lambda rows: torch.randint(1, 5, (rows, k), generator=g, device="cuda") * 0.5 * (
+        torch.randint(0, 2, (rows, k), generator=g, device="cuda") * 2.0 - 1)
+    x, w = small(t), small(n)
+    eights = torch.arange(k // 8, device="cuda")
+    at = eights * 8 + torch.randint(0, 8, (k // 8,), generator=g, device="cuda")
+    sign = torch.randint(0, 2, (k // 8,), generator=g, device="cuda") * 2.0 - 1
+    x[:, at], w[:, at] = 448 * sign, 448 * sign * (1 - 2.0 * (eights % 2))
+    return x, w
+
+
+@pytest.mark.parametrize("t,k,n,counts", SIXTEEN)
+@pytest.mark.parametrize("dt", TYPES)
+def test_small_products_beside_large_ones(lib, t, k, n, counts, dt):
+    """Up to 16 rows are multiplied without the narrow matrix instructions' loss."""
+    g = gen_of(t + k + n)
+    x, w = beside_large(g, t, n, k)
+    q, s = lib.quantize_fp8_tokens(x)
+    assert (s == 1).all()
+    if counts is None:
+        return assert_equal(lib.fp8_linear_forward(q, s, *lib.quantize_fp8_blocks(w), out_dtype=dt),
+                            x.double() @ w.double().T, "y")
+    scale = [2.0 ** (z % 3) for z in range(len(counts))]   # experts that differ
+    wq, ws = lib.quantize_fp8_blocks(torch.stack([w * v for v in scale]))
+    y = lib.fp8_linear_forward(q, s, wq, ws, offsets=offsets_of(counts), out_dtype=dt)
+    at = 0
+    for c, v in zip(counts, scale):
+        assert_equal(y[at:at + c], x[at:at + c].double() @ w.double().T * v, "y of an expert")
+        at += c
+    assert at <= t
