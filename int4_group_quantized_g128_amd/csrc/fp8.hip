@@ -403,7 +403,7 @@ struct Panel8 {
     else return (16 * q + (s >> 1)) * R + (swz(16 * q + (s >> 1)) << 4) + ((s & 1) << 3);
   }
   // The same through addresses kept in registers, with constant offsets: `at` panel bytes on, rows
-  // (columns) r0 (a constant) on.
+  // (columns) r0 (a constant, MC: below 64) on.  MC: the panel's LDS address is a multiple of 64.
   struct Reader {
     uint32_t lo, hi;
     Q4_DEVICE void start(uint32_t lds, int lane, int first) {   // first: a multiple of 16 (MC: of 64)
@@ -825,7 +825,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(
   constexpr int S1 = S0 + SLOTS * HR * 4, SB = S1 + SLOTS * HR * 4, BYTES = SB + (VECB ? SLOTS * BN * 4 : 0);
   static_assert(HR % 64 == 0 && CA >= 1 && CB >= 1 && MB >= 4, "");
   static_assert(COLS == 64, "a wave's columns lie in one block of W, and finish64");
-  __shared__ __align__(16) uint8_t mem[BYTES];
+  // (a Reader's transposing reads flip bits 4 and 5 of LDS addresses: every panel starts at a multiple of 64)
+  __shared__ __align__(128) uint8_t mem[BYTES];
+  static_assert(A0 % 64 == 0 && A1 % 64 == 0 && PA::BYTES % 64 == 0 && PB::BYTES % 64 == 0, "");
   __shared__ Span span;
   __shared__ int32_t tot[NW];
 
