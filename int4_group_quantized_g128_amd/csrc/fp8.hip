@@ -450,13 +450,11 @@ struct Panel8 {
 
 template <typename P, int N>
 Q4_DEVICE void copies8(const u32x4_t& rs, uint32_t at, int first, int lane, int64_t ld, int64_t left) {
+  static_assert(N % 2 == 0, "two copies at a time");
 #pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    if constexpr (N == 1) copy_to_lds(rs, at + first * 1024, P::offset(first, lane, ld, left));
-    else
-      copy2_to_lds(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left),
-                   P::offset(first + j + 1, lane, ld, left));
-  }
+  for (int j = 0; j < N; j += 2)
+    copy2_to_lds(rs, at + (first + j) * 1024, P::offset(first + j, lane, ld, left),
+                 P::offset(first + j + 1, lane, ld, left));
 }
 
 template <int N>
