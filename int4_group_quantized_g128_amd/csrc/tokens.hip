@@ -12,6 +12,7 @@
 
 #include "e4m3.h"
 #include "tokens.h"
+#include "tokens_plan.h"
 
 namespace q4 {
 
@@ -410,9 +411,7 @@ hipError_t dispatch_as(const DispatchArgs& a, const int32_t* base, hipStream_t s
 
 template <bool QUANT, int DT>
 hipError_t dispatch_rows(const DispatchArgs& a, const int32_t* base, hipStream_t st) {
-  // a wave per token where rows are narrow, or not wide and go to few places (4096 tokens of 2048,
-  // k = 2: 22.5 -> 19.5 us, of 1024, k = 4: 23.5 -> 20.3)
-  if (a.h * Elem<DT>::SIZE <= (a.k <= 4 ? 4096 : 1024) && a.k <= 64) return dispatch_as<QUANT, DT, 4, false>(a, base, st);
+  if (dispatch_by_waves(a.t, a.k, a.h * Elem<DT>::SIZE)) return dispatch_as<QUANT, DT, 4, false>(a, base, st);
   if (!QUANT && a.t * a.k * a.h * Elem<DT>::SIZE > kCacheBytes) return dispatch_as<QUANT, DT, 1, !QUANT>(a, base, st);
   return dispatch_as<QUANT, DT, 1, false>(a, base, st);
 }
