@@ -992,7 +992,8 @@ def moe_dispatch_forward(x, ids, num_experts, first=0, quantize=False, out=None)
     inv [t, k]) for the choices ids [t, k] int32; experts [first, first + num_experts) are held,
     slots of others dropped (inv -1, perm -1 behind the held rows; rows of xp from offsets[-1] on
     are not written).  With ``quantize`` -> (q, s, offsets, perm, inv): the rows as e4m3 codes
-    [t k, h] and scales [ceil(h / 128), t k] for fp8_linear_forward."""
+    [t k, h] and scales [ceil(h / 128), t k] for fp8_linear_forward.  The gradient is
+    moe_dispatch_backward (a call of its own: the results carry no autograd graph)."""
     (t, h), dev = _first(x, _FLOATS, "x")
     k = _slots(ids, "ids", t, dev)
     if not 1 <= num_experts <= 4096 or not 0 <= first < 2 ** 31 - num_experts:
@@ -1026,7 +1027,8 @@ def _sorted_rows(rows, name, inv):
 
 
 def moe_dispatch_backward(dxp, inv):
-    """dx [t, h] = sum_j dxp[inv[t, j]]: the gradient of moe_dispatch_forward."""
+    """dx [t, h] = sum_j dxp[inv[t, j]]: the gradient of moe_dispatch_forward (itself without an
+    autograd graph, as its counterparts)."""
     t, k, h, dev = _sorted_rows(dxp, "dxp", inv)
     dx = dxp.new_empty((t, h))
     _call("moe_dispatch_backward", _lib.moe_dispatch_backward, dev, dxp.data_ptr(), _DT[dxp.dtype], t, h,
@@ -1036,7 +1038,8 @@ def moe_dispatch_backward(dxp, inv):
 
 def moe_combine_forward(y, inv, weights=None, add=None):
     """out [t, h] = sum_j weights[t, j] y[inv[t, j]] (+ add) for rows y [t k, h] in expert order;
-    weights [t, k] fp32 or None (ones), add [t, h] or None."""
+    weights [t, k] fp32 or None (ones), add [t, h] or None.  The gradients are
+    moe_combine_backward (a call of its own: the result carries no autograd graph)."""
     t, k, h, dev = _sorted_rows(y, "y", inv)
     if weights is not None:
         _arg(weights, "weights", torch.float32, (t, k), dev)
@@ -1050,7 +1053,7 @@ def moe_combine_forward(y, inv, weights=None, add=None):
 
 def moe_combine_backward(dout, y, inv, weights=None, out=None):
     """Gradients (dy [t k, h], dweights [t, k] fp32 or None) of moe_combine_forward for dout [t, h];
-    rows of dy that no slot has are not written."""
+    rows of dy that no slot has are not written.  (No autograd graph.)"""
     t, k, h, dev = _sorted_rows(y, "y", inv)
     _arg(dout, "dout", y.dtype, (t, h), dev)
     dw = None
@@ -1068,7 +1071,8 @@ def quantize_fp8_tokens(x, columns=False, gated=False, offsets=None):
     row; ``gated``: of silu(x[:, :k]) x[:, k:] for x [t, 2 k].  With ``columns`` -> (q, s, qc, sc):
     also in groups of 128 tokens, sc [groups, k], for fp8_linear_backward.  ``offsets`` (of
     moe_dispatch_forward): rows behind the last expert are left out, and the groups of tokens
-    start anew with each expert."""
+    start anew with each expert.  (For fp8_linear_backward the codes count as x itself; no
+    autograd graph leads through them.)"""
     (t, k), dev = _first(x, _FLOATS, "x")
     e = _offsets(offsets, dev)
     if gated:
@@ -1092,7 +1096,8 @@ def _column_groups(t, offsets, e):
 
 def quantize_fp8_blocks(w):
     """e4m3 codes and scales [.., ceil(n / 128), ceil(k / 128)] of weights w [n, k] or [e, n, k] by
-    blocks of 128 x 128."""
+    blocks of 128 x 128.  (For fp8_linear_backward the codes count as w itself; no autograd graph
+    leads through them.)"""
     _need(w, _FLOATS, "w")
     if w.dim() not in (2, 3):
         raise ValueError("w must be [n, k] or [e, n, k]")
@@ -1121,7 +1126,8 @@ def fp8_linear_forward(q, s, w_q, w_s, offsets=None, out_dtype=torch.bfloat16, o
     """y [t, n] of out_dtype (fp16 or bf16): the product of token codes q [t, k] e4m3 with scales s
     [ceil(k / 128), t] and weight codes w_q [n, k] with block scales w_s.  With ``offsets`` [e + 1]
     the rows offsets[x] .. offsets[x + 1] - 1 take matrix x of w_q [e, n, k]; rows of no expert
-    are not written."""
+    are not written.  The gradients are fp8_linear_backward (a call of its own: the result carries
+    no autograd graph)."""
     (t, k), dev = _first(q, (_E4M3,), "q")
     _arg(s, "s", torch.float32, (-(-k // 128), t), dev)
     e, n = _fp8_weights(w_q, w_s, k, offsets, dev)
@@ -1140,7 +1146,7 @@ def fp8_linear_backward(dy, x_q, x_s, w_q, w_s, offsets=None, out=None):
     """Gradients (dx [t, k], dw like w_q) of fp8_linear_forward, of dy's type, for dy [t, n]: dy is
     quantised in groups of 128 along its rows (dx) and along the tokens (dw); x_q, x_s are the
     forward's x by quantize_fp8_tokens(x, columns=True).  out: dx; its rows of no expert are not
-    written."""
+    written.  (No autograd graph.)"""
     (t, n), dev = _first(dy, _16BIT, "dy")
     k = _first(x_q, (_E4M3,), "x_q")[0][1]
     _arg(x_q, "x_q", _E4M3, (t, k), dev)
