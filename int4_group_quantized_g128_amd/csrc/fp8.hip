@@ -161,6 +161,9 @@ struct ExpertTiles {
 
 // ---------------------------------------------------------------- quantisers
 // A workgroup takes 16 RPT rows x 128 columns: thread i columns 8 (i % 16) .. + 7 of rows i / 16 + 16 j.
+// Codes along the rows alone are bound by their bytes (4096 x 7168 bf16 17.1 us, 5.2 TB/s); with those along the
+// tokens by vector instructions, 31 a value (maxima, quotients, conversions, twice) that take 86 % of the cycles
+// at 4096 x 16384 (73 to 80 us, 3.4 to 3.7 TB/s) and 71 % at 8192 x 2048 (29 us).
 enum Form { FORM_ROWS = 1, FORM_COLS = 2 };
 // RPT of codes along the rows alone: 4096 x 7168 17.0 us (8: 22.5, 4: 19.2, 1: 16.6), 4096 x 16384
 // 50.8 (52.6, 55.1, 58.7), 333 x 1040 4.0 (7.4, 4.5, 4.8); groups of tokens take 8, all 128 rows.
@@ -283,6 +286,8 @@ __global__ void __launch_bounds__(256) k_quantize_fp8(Fp8QuantArgs a) {
   }
 }
 
+// Bound by its bytes: 16384 x 2048 bf16 28 us, 32 matrices of 4096 x 7168 560 (5.0 TB/s), fp32 36 and 968; one
+// of 2048 x 2048 7.2.
 template <int DT>
 __global__ void __launch_bounds__(256) k_quantize_fp8_blocks(const void* __restrict__ w, int64_t n, int64_t k,
                                                              uint32_t row_blocks, uint8_t* __restrict__ q,
@@ -694,7 +699,8 @@ Q4_DEVICE void finish64(const Fp8Args& g, const Work& w, const f32x4_t (&acc)[MB
 // BM x BN per workgroup of WM x WN waves, a ring of NS K steps in LDS: step s + NS - 1 is copied
 // while step s is multiplied, one barrier per step.  Three steps of 64 x 64 let a CU hold three
 // workgroups; a lone one takes 0.4 us a step, the 16 KB that its CU reads (rings of 5 and 8 steps,
-// and two steps per barrier, were no faster).  64 x 7168 x 4096 in 4 K slices 11.6 us.
+// and two steps per barrier, were no faster).  64 x 7168 x 4096 in 4 K slices 11.6 us: 14 steps, 5.6 us, and the
+// start and end of 256 lone workgroups, with 4 MB of slices stored.
 template <int MODE, int BM, int BN, int WM, int WN, int NS>
 __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;
@@ -805,10 +811,13 @@ __global__ void __launch_bounds__(64 * WM * WN) k_fp8(Fp8Args g, uint32_t mtiles
 // one value per workgroup is kept in scalar registers and every helper inlined: as soon as the
 // arguments went through memory the loops spilled, dw of 4096 x 7168 x 4096 141 -> 233 us.)
 //
-// 4096 x 7168 x 4096 takes 108 us (2.2 PFLOP/s), 4096 x 2048 x 16384 150 to 172 (1.6 to 1.8).  A step
-// of the 256 tile has 2048 matrix cycles per SIMD and moves 256 KB through LDS, which at 128 bytes a
-// cycle are 2048 as well; the matrix core is busy 43 to 50 % of the time, without bank conflicts, at
-// a clock that falls to 1.9 GHz.
+// 4096 x 7168 x 4096 takes 108 us (2.2 PFLOP/s), 4096 x 2048 x 16384 143 to 175 (1.6 to 1.9): y 143, dx 131
+// and dW 156 on an idle card, up to 175, 158 and 190 in a row of passes, when the clock falls to 1.9 GHz.
+// The matrix core is busy 54 % of the cycles there, here 46 (y), 52 (dx) and 43 (dW); the vector
+// instructions take 37, 39, 34 and 50 % more.  The loops have 5.0 (y), 4.9 (dx) and 8.5 (dW) of them to a
+// matrix instruction, 4, 4 and 8 of which are the scaled sums, and the two units hardly overlap: their
+// sum is 85 to 94 % of the cycles, in the order of the products' times.  LDS reads take 21 to 24 %,
+// without bank conflicts.
 template <int MODE, int BM, int BN, int WM, int WN, int SLOTS>
 __global__ void __launch_bounds__(64 * WM * WN, 512 / (64 * WM * WN)) k_fp8_big(Fp8Args g, uint32_t mtiles, uint32_t ntiles) {
   constexpr bool AMC = MODE == FP8_DW, BMC = MODE != FP8_Y, VECB = MODE == FP8_DW;

@@ -166,6 +166,12 @@ __device__ void offsets_of(const DispatchArgs& a, int32_t* hist, int32_t* tot) {
 // same expert's slots of the range, on top of the range's first position.  Then the rows go out,
 // each token read once and written k times.  NT: rows larger than the last-level cache are written
 // past it (4096 tokens of 7168, k = 8: 121 -> 106 us).
+//
+// 4096 tokens of 7168, k = 8, take 93 us, the rows' bytes.  Where a rank holds an eighth of the slots the ranking
+// remains: 39 us as codes, 14 to 18 for the bytes; vector instructions (825 a wave, for the ranks of two
+// slots among 1024 and for 1792 codes) take 64 % of the cycles, the waits for slots, ranks and rows in
+// turn the rest.  4096 of 2048, k = 2, by waves: 15.5 us against 10 for the bytes, where waves wait for
+// these three quarters of their time.
 template <bool QUANT, int DT, int TPW, bool NT>
 __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t per, const int32_t* __restrict__ base,
                                                        int64_t col_block) {
@@ -271,7 +277,9 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(DispatchArgs a, int64_t p
 // out[t] = sum_j w y[inv] (+ add): a wave per token and 64 vectors of columns, U rows in flight (as
 // many as k: 4096 tokens of 2048, k = 2, 8 in flight 13.6 us, 2 9.5).  NT: rows larger than the
 // last-level cache are read past it (4096 tokens of 7168, k = 8: 105 -> 91 us; of 2048, k = 2, which
-// the cache holds, 10.0 -> 11.0).
+// the cache holds, 10.0 -> 11.0).  Where a rank holds an eighth of the slots of 4096 tokens of 7168,
+// k = 8, 41 us (24 for the bytes): a row that is left out costs its vector instructions all the same,
+// and these take 77 % of the cycles.
 template <int DT, int U, bool NT>
 __global__ void __launch_bounds__(kThreads) k_tokens_combine(const void* __restrict__ y, const int32_t* __restrict__ inv,
                                                              const float* __restrict__ w, const void* __restrict__ add,
