@@ -76,8 +76,8 @@ inline int64_t fp8_rows_grid(int64_t t, int64_t n, int64_t e) {
   return (fp8_rows_search(t, n, e) ? std::min(e, t) : e) * ceil_div(n, 16);
 }
 
-// Calls of up to this many rows take the few-rows kernel in passes of 16, which multiplies without the
-// narrow instructions' loss, whatever is faster: 0.5 to 1.26 times the tiles' time (one row,
+// Calls of up to this many rows take the few-rows kernel, which multiplies without the narrow
+// instructions' loss, whatever is faster: 0.5 to 1.26 times the tiles' time (one row,
 // 256 / 4096, 4.6 -> 3.7 us; 16 rows, 256 / 512, 4.6 -> 2.9, 8192 / 8192 20.2 -> 21.2, 16384 / 1000 14.5
 // -> 17.2, 7168 / 16384 28.4 -> 34.4; 8 rows of 8 experts, 256 / 512, 5.7 -> 3.0, of 1024, 256 / 4096,
 // 9.9 -> 12.3).

@@ -21,3 +21,7 @@ SIXTEEN = [(1, 16, 8, None), (1, 256, 4096, None), (2, 144, 33, None), (16, 256,
            (2, 5120, 16384, None), (16, 2048, 16384, None), (1, 7168, 16384, None), (16, 8192, 8192, None),
            (12, 16384, 1000, None), (8, 256, 512, [1] * 8), (8, 272, 1040, [0, 3, 0, 5]), (16, 2048, 4096, [0, 16, 0, 0]),
            (5, 144, 2000, [0] * 250 + [2, 0, 3]), (16, 512, 48, [0, 0, 9, 1])]
+
+# The same for passes of 64: (t, k, n, rows of each expert or None)
+SIXTY_FOUR = [(shape[1], *shape[2:4], None) if shape[0] is None else (sum(shape[0]), *shape[1:3], shape[0])
+              for shape in PASSES if shape[-1] == 64]

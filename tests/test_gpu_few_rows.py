@@ -3,7 +3,7 @@ exact in fp32, as in the products' other tests)."""
 import pytest
 import torch
 
-from tests.few_rows_shapes import PASSES, SCATTERED, SIXTEEN
+from tests.few_rows_shapes import PASSES, SCATTERED, SIXTEEN, SIXTY_FOUR
 from tests.helpers import require_gpu
 from tests.test_gpu_fp8 import E4M3, TYPES, assert_equal, by_expert, ceil, gen_of, halves, offsets_of
 
@@ -73,10 +73,11 @@ def beside_large(g, t, n, k):
     return x, w
 
 
-@pytest.mark.parametrize("t,k,n,counts", SIXTEEN)
+@pytest.mark.parametrize("t,k,n,counts", SIXTEEN + SIXTY_FOUR)
 @pytest.mark.parametrize("dt", TYPES)
 def test_small_products_beside_large_ones(lib, t, k, n, counts, dt):
-    """Up to 16 rows are multiplied without the narrow matrix instructions' loss."""
+    """Up to 16 rows, and whatever else the few-rows kernel takes, are multiplied without the narrow matrix
+    instructions' loss."""
     g = gen_of(t + k + n)
     x, w = beside_large(g, t, n, k)
     q, s = lib.quantize_fp8_tokens(x)
