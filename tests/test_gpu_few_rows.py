@@ -93,3 +93,49 @@ def test_small_products_beside_large_ones(lib, t, k, n, counts, dt):
         assert_equal(y[at:at + c], x[at:at + c].double() @ w.double().T * v, "y of an expert")
         at += c
     assert at <= t
+
+
+def test_searched_runs_in_a_graph(lib):
+    """A captured product finds the runs of the offsets that it meets at each replay."""
+    t, k, n, e = 8, 2064, 1040, 300
+    g = gen_of(2)
+    x, w = halves(g, t, k) / 64, torch.stack([halves(g, n, k) / 64 for _ in range(e)])
+    q, s = lib.quantize_fp8_tokens(x)
+    wq, ws = lib.quantize_fp8_blocks(w)
+    off = offsets_of([0] * e)
+    y = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=y)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=y)
+    for held in ({0: 8}, {299: 1}, {}, {z: 1 for z in range(60, 68)}, {255: 3, 256: 5}, {0: 8}):
+        off.copy_(offsets_of([held.get(z, 0) for z in range(e)]))
+        y.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.full_like(y, 9)
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=off, out=want)
+        assert torch.equal(y, want)
+        at = 0
+        for z, c in sorted(held.items()):
+            assert_equal(y[at:at + c], x[at:at + c].double() @ w[z].double().T, f"expert {z}")
+            at += c
+        assert (y[at:] == 9).all()
+
+
+def test_searched_runs_of_offsets_not_ascending(lib):
+    """More runs than there can be with ascending offsets: nothing outside the result is written."""
+    t, k, n, e = 6, 1040, 520, 256
+    q, s = lib.quantize_fp8_tokens(torch.ones(t, k, device="cuda"))
+    wq, ws = lib.quantize_fp8_blocks(torch.ones(e, n, k, device="cuda"))
+    for off in ([0, t] * (e // 2) + [0], [t] + [0] * (e - 1) + [2 ** 31 - 1], [-5, 2 ** 31 - 1] * (e // 2) + [3],
+                list(range(e, -1, -1))):
+        buf = torch.full((t * n + 128,), -3.0, dtype=torch.bfloat16, device="cuda")
+        y = buf[64:64 + t * n].view(t, n)
+        lib.fp8_linear_forward(q, s, wq, ws, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), out=y)
+        assert (buf[:64] == -3).all() and (buf[64 + t * n:] == -3).all()
+        assert ((y == -3) | (y == k)).all()
