@@ -786,7 +786,8 @@ Q4_API int moe_combine_backward(const void* dout, const void* y, int dtype, int6
  * fp8_linear_backward -- given dy device [t][n] of dtype Q4_F16 or Q4_BF16: dy is quantised along
  * its rows for dx and along the tokens for dw, each by quantize_fp8_tokens' rule, and
  *   dx = dy_hat W_hat,   dw = dy_hat^T x_hat
- *  (x_hat, W_hat, dy_hat: codes times scales; the quantisers count as the identity).
+ *  (x_hat, W_hat, dy_hat: codes times scales; the quantisers count as the identity).  Both lose
+ *  within a group what the forward pass of many rows may lose, for any number of rows.
  *  x_q, x_s device q_col and s_col of the forward's x (with the same offsets).
  *  dx       device [t][k]; dw device [e][n][k] (overwritten; zeros for an expert without rows);
  *           of dtype, fp32 sums rounded once.  Rows of dx of no expert are left as they were.

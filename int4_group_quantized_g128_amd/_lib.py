@@ -1126,8 +1126,9 @@ def fp8_linear_forward(q, s, w_q, w_s, offsets=None, out_dtype=torch.bfloat16, o
     """y [t, n] of out_dtype (fp16 or bf16): the product of token codes q [t, k] e4m3 with scales s
     [ceil(k / 128), t] and weight codes w_q [n, k] with block scales w_s.  With ``offsets`` [e + 1]
     the rows offsets[x] .. offsets[x + 1] - 1 take matrix x of w_q [e, n, k]; rows of no expert
-    are not written.  The gradients are fp8_linear_backward (a call of its own: the result carries
-    no autograd graph)."""
+    are not written.  Sums are fp32; more than 16 rows may lose within a group what lies 2^-13 below
+    the largest of eight products.  The gradients are fp8_linear_backward (a call of its own: the
+    result carries no autograd graph)."""
     (t, k), dev = _first(q, (_E4M3,), "q")
     _arg(s, "s", torch.float32, (-(-k // 128), t), dev)
     e, n = _fp8_weights(w_q, w_s, k, offsets, dev)
